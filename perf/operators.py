@@ -404,6 +404,8 @@ def _exact_sequences(s, grads):
                 dc = (q * dq).sum(-1) - (k * dkk).sum(-1)
                 dc[-1] += (hT * dhT).sum()
                 out["dg"][b, h, :n] = dc.flip(0).cumsum(0).flip(0)
+                if s["h0"] is None:
+                    out["dg"][b, h, 0] = 0   # the first gate decays nothing: exactly zero
     return out
 
 
