@@ -23,14 +23,15 @@ LIB_PATH = os.path.join(HERE, "libdn.so")
 DN_OK, DN_ERR_INVALID, DN_ERR_SHAPE, DN_ERR_DTYPE, DN_ERR_WORKSPACE, DN_ERR_UNSUPPORTED, DN_ERR_HIP = (
     0, -1, -2, -3, -4, -5, -6)
 DN_F32, DN_BF16 = 0, 1
-DN_GATE_NONE, DN_GATE_SCALAR, DN_GATE_VECTOR = 0, 1, 2
+DN_GATE_NONE, DN_GATE_SCALAR, DN_GATE_VECTOR, DN_GATE_HEAD = 0, 1, 2, 3
 DN_PASS_FWD, DN_PASS_BWD, DN_PASS_BWD_RECOMPUTE = 0, 1, 2
 DN_FLAG_KACZMARZ, DN_FLAG_NO_SCAN = 1, 2
 DN_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 EXPORTS = ("dn_states_bytes", "dn_states_layout", "dn_workspace_bytes", "dn_workspace_layout", "dn_chunk_fwd",
            "dn_chunk_fwd_noalloc", "dn_chunk_bwd", "dn_recurrent_fwd", "dn_recurrent_phase_fwd", "dn_phase_states_bytes",
-           "dn_phase_workspace_bytes", "dn_chunk_phase_fwd", "dn_chunk_phase_bwd", "dn_status_string", "dn_last_error",
+           "dn_phase_workspace_bytes", "dn_chunk_phase_fwd", "dn_chunk_phase_bwd", "dn_linear_workspace_bytes",
+           "dn_linear_fwd", "dn_linear_bwd", "dn_linear_recurrent_fwd", "dn_status_string", "dn_last_error",
            "dn_profile_enable", "dn_profile_collect")
 
 
@@ -86,6 +87,14 @@ def lib():
     L.dn_chunk_phase_fwd.restype = i32
     L.dn_chunk_phase_bwd.argtypes = [sp] + [vp] * 21 + [sz, vp]
     L.dn_chunk_phase_bwd.restype = i32
+    L.dn_linear_workspace_bytes.argtypes = [sp, i32]
+    L.dn_linear_workspace_bytes.restype = sz
+    L.dn_linear_fwd.argtypes = [sp] + [vp] * 9 + [sz, vp]
+    L.dn_linear_fwd.restype = i32
+    L.dn_linear_bwd.argtypes = [sp] + [vp] * 14 + [sz, vp]
+    L.dn_linear_bwd.restype = i32
+    L.dn_linear_recurrent_fwd.argtypes = [sp] + [vp] * 7
+    L.dn_linear_recurrent_fwd.restype = i32
     L.dn_status_string.argtypes = [i32]
     L.dn_status_string.restype = ctypes.c_char_p
     L.dn_last_error.argtypes = []
@@ -118,7 +127,7 @@ def make_shape(B, H, T, dk, dv, C, dtype, gate, kaczmarz_eps=None, no_scan=False
     ``no_scan`` sets DN_FLAG_NO_SCAN (one sequential state pass, never the chunk-parallel scan)."""
     dt = {torch.float32: DN_F32, torch.bfloat16: DN_BF16, "fp32": DN_F32, "bf16": DN_BF16}.get(dtype, dtype)
     gt = {None: DN_GATE_NONE, "none": DN_GATE_NONE, "scalar": DN_GATE_SCALAR,
-          "vector": DN_GATE_VECTOR}.get(gate, gate)
+          "vector": DN_GATE_VECTOR, "head": DN_GATE_HEAD}.get(gate, gate)
     flags, eps = (0, 0.0) if kaczmarz_eps is None else (DN_FLAG_KACZMARZ, float(kaczmarz_eps))
     if no_scan:
         flags |= DN_FLAG_NO_SCAN
@@ -241,6 +250,29 @@ def dn_chunk_phase_bwd(shape, q, k, v, beta, g, theta, h0_re, h0_im, dout, dhT_r
                                     _ptr(h0_re), _ptr(h0_im), _ptr(dout), _ptr(dhT_re), _ptr(dhT_im), _ptr(states),
                                     _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbeta), _ptr(dg), _ptr(dtheta), _ptr(dh0_re),
                                     _ptr(dh0_im), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def dn_linear_workspace_bytes(shape: Shape, pass_: int) -> int:
+    return lib().dn_linear_workspace_bytes(ctypes.byref(shape), int(pass_))
+
+
+def dn_linear_fwd(shape, q, k, v, g, lens, h0, o, hT, ws=None, ws_bytes=0, stream=None) -> int:
+    """Raw call; returns the dn_status (no exception)."""
+    return lib().dn_linear_fwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lens), _ptr(h0), _ptr(o),
+                               _ptr(hT), _ptr(ws), int(ws_bytes), _stream(stream))
+
+
+def dn_linear_bwd(shape, q, k, v, g, lens, h0, dout, dhT, dq, dk, dv, dg, dh0, ws=None, ws_bytes=0, stream=None) -> int:
+    """Raw call; returns the dn_status (no exception)."""
+    return lib().dn_linear_bwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lens), _ptr(h0),
+                               _ptr(dout), _ptr(dhT), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dh0), _ptr(ws),
+                               int(ws_bytes), _stream(stream))
+
+
+def dn_linear_recurrent_fwd(shape, q, k, v, g, state, o, stream=None) -> int:
+    """Raw call; returns the dn_status (no exception)."""
+    return lib().dn_linear_recurrent_fwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(o),
+                                         _stream(stream))
 
 
 # ------------------------------------------------------------------ convenience
@@ -476,3 +508,112 @@ class DeltaRule(torch.autograd.Function):
                        None if dhT is None else dhT.contiguous(), states, C=ctx.C, kaczmarz_eps=ctx.kz)
         return (gr["dq"], gr["dk"], gr["dv"], gr["dbeta"], gr["dg"], (gr["dh0"] if h0 is not None else None),
                 None, None, None)
+
+
+# ------------------------------------------------------------------ linear attention with a decay per head
+
+
+def _check_tensors(first, want):
+    """``want``: {name: (tensor or None, dtype, shape)}.  Every tensor of that type and
+    shape, contiguous, on the CUDA device of ``first``.  Raises ValueError."""
+    dev = first.device
+    for name, (t, dt, shp) in want.items():
+        if t is None:
+            continue
+        if t.dtype != dt:
+            raise ValueError(f"{name} must be {dt}, got {t.dtype}")
+        if t.shape != shp:
+            raise ValueError(f"{name} must have shape {tuple(shp)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        if t.device != dev:
+            raise ValueError(f"every tensor must be on {dev}, found one on {t.device}")
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, found one on {dev}")
+
+
+def _linear_gate(g, B, H, T, dk=None):
+    """Gate kind and the shape of g: None, [H] (per head), [B,H,T] (per step) or, where
+    ``dk`` is given, [B,H,T,dk] (per channel)."""
+    if g is None:
+        return DN_GATE_NONE, None
+    if g.dim() == 1:
+        return DN_GATE_HEAD, (H,)
+    if g.dim() == 4 and dk is not None:
+        return DN_GATE_VECTOR, (B, H, T, dk)
+    return DN_GATE_SCALAR, (B, H, T)
+
+
+def _linear_args(q, k, v, g, no_scan=False, **more):
+    """Shape descriptor of checked tensors; ``more``: {name: (tensor, "q" | "v" | "state" | "lens")}."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"q must be [B,H,T,dk] and v [B,H,T,dv], got shapes {tuple(q.shape)}, {tuple(v.shape)}")
+    B, H, T, dk = q.shape
+    dv = v.shape[3]
+    if q.dtype not in _IO_DTYPES:
+        raise ValueError(f"q must be float32 or bfloat16, got {q.dtype}")
+    kind, gshape = _linear_gate(g, B, H, T)
+    kinds = {"q": (q.dtype, (B, H, T, dk)), "v": (q.dtype, (B, H, T, dv)), "state": (torch.float32, (B, H, dv, dk)),
+             "lens": (torch.int32, (B,))}
+    want = {"q": (q, *kinds["q"]), "k": (k, *kinds["q"]), "v": (v, *kinds["v"]), "g": (g, torch.float32, gshape)}
+    want.update((n, (t, *kinds[what])) for n, (t, what) in more.items())
+    _check_tensors(q, want)
+    return Shape(B, H, T, dk, dv, 64, DN_BF16 if q.dtype == torch.bfloat16 else DN_F32, kind,
+                 DN_FLAG_NO_SCAN if no_scan else 0, 0.0)
+
+
+def _linear_ws(shape, pass_, ws, device):
+    n = dn_linear_workspace_bytes(shape, pass_)
+    if ws is None and n:
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+    return ws, (0 if ws is None else ws.numel())
+
+
+def linear_fwd(q, k, v, g=None, h0=None, lens=None, want_hT=True, ws=None, stream=None, no_scan=False):
+    """Linear attention with a decay per head over whole sequences: S_t = exp(g_t) S_{t-1} + v_t k_t^T,
+    o_t = S_t q_t.  ``g``: None, [H] (a constant log-decay per head) or [B,H,T] (per step); ``lens``:
+    int32 [B], the steps of each batch element (o is zero past them, hT the state after them).
+    Returns (o, hT or None)."""
+    sh = _linear_args(q, k, v, g, no_scan, h0=(h0, "state"), lens=(lens, "lens"))
+    o = torch.empty_like(v)
+    hT = torch.empty(sh.B, sh.H, sh.dv, sh.dk, dtype=torch.float32, device=q.device) if want_hT else None
+    ws, n = _linear_ws(sh, DN_PASS_FWD, ws, q.device)
+    _check(dn_linear_fwd(sh, q, k, v, g, lens, h0, o, hT, ws, n, stream))
+    return o, hT
+
+
+def linear_bwd(q, k, v, g, h0, do, dhT=None, lens=None, want_dh0=True, ws=None, stream=None, no_scan=False):
+    """Backward of linear_fwd.  Returns dict dq, dk, dv, dg (None unless g is per step), dh0 (or None)."""
+    sh = _linear_args(q, k, v, g, no_scan, h0=(h0, "state"), do=(do, "v"), dhT=(dhT, "state"), lens=(lens, "lens"))
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dg = torch.empty_like(g) if sh.gate == DN_GATE_SCALAR else None
+    dh0 = torch.empty(sh.B, sh.H, sh.dv, sh.dk, dtype=torch.float32, device=q.device) if want_dh0 else None
+    ws, n = _linear_ws(sh, DN_PASS_BWD, ws, q.device)
+    _check(dn_linear_bwd(sh, q, k, v, g, lens, h0, do, dhT, dq, dk, dv, dg, dh0, ws, n, stream))
+    return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dh0": dh0}
+
+
+def linear_recurrent_fwd(q, k, v, g, state, stream=None):
+    """T recurrent steps of linear attention (decode); ``state`` (fp32 [B,H,dv,dk]) is updated in
+    place.  ``g`` as for linear_fwd.  Returns o."""
+    sh = _linear_args(q, k, v, g, state=(state, "state"))
+    o = torch.empty_like(v)
+    _check(dn_linear_recurrent_fwd(sh, q, k, v, g, state, o, stream))
+    return o
+
+
+class LinearAttention(torch.autograd.Function):
+    """o, hT = LinearAttention.apply(q, k, v, g, h0, lens); g [H] gets no gradient."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g=None, h0=None, lens=None):
+        o, hT = linear_fwd(q, k, v, g, h0, lens=lens)
+        ctx.save_for_backward(q, k, v, g, h0, lens)
+        return o, hT
+
+    @staticmethod
+    def backward(ctx, do, dhT):
+        q, k, v, g, h0, lens = ctx.saved_tensors
+        gr = linear_bwd(q, k, v, g, h0, do.contiguous(), None if dhT is None else dhT.contiguous(), lens=lens,
+                        want_dh0=h0 is not None)
+        return gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["dh0"], None

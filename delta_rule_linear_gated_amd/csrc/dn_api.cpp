@@ -13,6 +13,7 @@
 
 #include "dn.h"
 #include "dn_internal.h"
+#include "dn_linear_api.h"
 
 namespace {
 
@@ -678,6 +679,169 @@ dn_status dn_recurrent_phase_fwd(const dn_shape* shape, const void* q, const voi
                                  const float* beta, const float* g, const float* theta, float* state_re,
                                  float* state_im, void* o, void* stream) {
     return recurrent_call(shape, q, k, v, beta, g, theta, state_re, state_im, o, stream, true);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Shape checks of linear attention; recurrent: the token-by-token form's wider dv.
+dn_status linear_shape(const dn_shape* s, bool recurrent, dn::LinProblem* pr, Dims* d) {
+    if (!s) return fail(DN_ERR_INVALID, "shape is NULL");
+    if (s->B < 0 || s->H < 0 || s->T < 0) return fail(DN_ERR_SHAPE, "B, H, T must be >= 0");
+    if (s->dk <= 0 || s->dv <= 0) return fail(DN_ERR_SHAPE, "dk and dv must be > 0");
+    if (s->dtype != DN_F32 && s->dtype != DN_BF16) return fail(DN_ERR_DTYPE, "unknown dtype %d", s->dtype);
+    if (s->gate < DN_GATE_NONE || s->gate > DN_GATE_HEAD) return fail(DN_ERR_INVALID, "unknown gate %d", s->gate);
+    if (s->gate == DN_GATE_VECTOR) return fail(DN_ERR_UNSUPPORTED, "linear attention has no per-channel gate");
+    DN_TRY(check_flags(s));
+    if (s->flags & DN_FLAG_KACZMARZ) return fail(DN_ERR_UNSUPPORTED, "linear attention has no step size");
+    auto width = [](int x) { return x == 16 || x == 32 || x == 64 || x == 128; };
+    if (!width(s->dk)) return fail(DN_ERR_UNSUPPORTED, "dk must be 16, 32, 64 or 128");
+    if (recurrent) {
+        if (s->dv % 16 != 0) return fail(DN_ERR_UNSUPPORTED, "dv must be a positive multiple of 16");
+        if ((long long)s->B * s->H * (s->dv / 16) > 0x7fffffffLL) return fail(DN_ERR_UNSUPPORTED, "B*H*dv/16 too large");
+    } else {
+        if (!width(s->dv)) return fail(DN_ERR_UNSUPPORTED, "dv must be 16, 32, 64 or 128");
+        if ((long long)s->B * s->H > 65535) return fail(DN_ERR_UNSUPPORTED, "B*H must be <= 65535");
+        if (s->T > 0x7fffff00) return fail(DN_ERR_UNSUPPORTED, "T too large");
+    }
+    pr->B = s->B;
+    pr->H = s->H;
+    pr->T = s->T;
+    pr->dk = s->dk;
+    pr->dv = s->dv;
+    pr->bf16 = s->dtype == DN_BF16;
+    pr->gate = s->gate == DN_GATE_NONE ? 0 : s->gate == DN_GATE_SCALAR ? 1 : 2;
+    pr->no_scan = (s->flags & DN_FLAG_NO_SCAN) ? 1 : 0;
+    *d = Dims{};
+    d->BH = (size_t)s->B * s->H;
+    d->T = (size_t)s->T;
+    d->dk = (size_t)s->dk;
+    d->dv = (size_t)s->dv;
+    d->E = pr->bf16 ? 2 : 4;
+    return DN_OK;
+}
+
+size_t gate_bytes(const dn_shape* s, const Dims& d) {
+    switch (s->gate) {
+        case DN_GATE_SCALAR: return d.BH * d.T * 4;
+        case DN_GATE_VECTOR: return d.BH * d.T * d.dk * 4;
+        case DN_GATE_HEAD: return (size_t)s->H * 4;
+        default: return 0;
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dn_linear_workspace_bytes(const dn_shape* shape, int pass) {
+    dn::LinProblem pr;
+    Dims d;
+    if (pass != DN_PASS_FWD && pass != DN_PASS_BWD) return 0;
+    if (linear_shape(shape, false, &pr, &d) != DN_OK) return 0;
+    return dn::lin_workspace_bytes(pr, pass);
+}
+
+dn_status dn_linear_fwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* g,
+                        const int32_t* lens, const float* h0, void* o, float* hT, void* ws, size_t ws_bytes,
+                        void* stream) {
+    g_err[0] = '\0';
+    dn::LinProblem pr;
+    Dims d;
+    DN_TRY(linear_shape(shape, false, &pr, &d));
+    const size_t nk = d.BH * d.T * d.dk * d.E, nv = d.BH * d.T * d.dv * d.E, ng = gate_bytes(shape, d);
+    const size_t ns = d.BH * d.dv * d.dk * 4, nl = (size_t)shape->B * 4, nws = dn::lin_workspace_bytes(pr, 0);
+    if (shape->gate == DN_GATE_NONE && g) return fail(DN_ERR_INVALID, "g must be NULL without a gate");
+    DN_TRY(need(q, nk, "q"));
+    DN_TRY(need(k, nk, "k"));
+    DN_TRY(need(v, nv, "v"));
+    DN_TRY(need(g, ng, "g"));
+    DN_TRY(need(o, nv, "o"));
+    if (ws_bytes < nws) return fail(DN_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, nws);
+    DN_TRY(need(ws, nws, "workspace"));
+    DN_TRY(check_buffers({{"q", q, nk, false},
+                          {"k", k, nk, false},
+                          {"v", v, nv, false},
+                          {"g", g, ng, false},
+                          {"lens", lens, nl, false},
+                          {"h0", h0, ns, false},
+                          {"o", o, nv, true},
+                          {"hT", hT, ns, true},
+                          {"workspace", ws, nws, true}}));
+    const dn::LinFwd f{q, k, v, g, lens, h0, o, hT};
+    const hipError_t e = dn::launch_linear_fwd(pr, f, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return DN_OK;
+}
+
+dn_status dn_linear_bwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* g,
+                        const int32_t* lens, const float* h0, const void* dout, const float* dhT, void* dq, void* dk,
+                        void* dv, float* dg, float* dh0, void* ws, size_t ws_bytes, void* stream) {
+    g_err[0] = '\0';
+    dn::LinProblem pr;
+    Dims d;
+    DN_TRY(linear_shape(shape, false, &pr, &d));
+    const size_t nk = d.BH * d.T * d.dk * d.E, nv = d.BH * d.T * d.dv * d.E, ng = gate_bytes(shape, d);
+    const size_t ns = d.BH * d.dv * d.dk * 4, nl = (size_t)shape->B * 4, nws = dn::lin_workspace_bytes(pr, 1);
+    const size_t ndg = shape->gate == DN_GATE_SCALAR ? ng : 0;
+    if (shape->gate == DN_GATE_NONE && g) return fail(DN_ERR_INVALID, "g must be NULL without a gate");
+    if (shape->gate != DN_GATE_SCALAR && dg) return fail(DN_ERR_INVALID, "dg must be NULL without a gate per step");
+    DN_TRY(need(q, nk, "q"));
+    DN_TRY(need(k, nk, "k"));
+    DN_TRY(need(v, nv, "v"));
+    DN_TRY(need(g, ng, "g"));
+    DN_TRY(need(dout, nv, "dout"));
+    DN_TRY(need(dq, nk, "dq"));
+    DN_TRY(need(dk, nk, "dk"));
+    DN_TRY(need(dv, nv, "dv"));
+    DN_TRY(need(dg, ndg, "dg"));
+    if (ws_bytes < nws) return fail(DN_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, nws);
+    DN_TRY(need(ws, nws, "workspace"));
+    DN_TRY(check_buffers({{"q", q, nk, false},
+                          {"k", k, nk, false},
+                          {"v", v, nv, false},
+                          {"g", g, ng, false},
+                          {"lens", lens, nl, false},
+                          {"h0", h0, ns, false},
+                          {"dout", dout, nv, false},
+                          {"dhT", dhT, ns, false},
+                          {"dq", dq, nk, true},
+                          {"dk", dk, nk, true},
+                          {"dv", dv, nv, true},
+                          {"dg", dg, ndg, true},
+                          {"dh0", dh0, ns, true},
+                          {"workspace", ws, nws, true}}));
+    const dn::LinBwd f{q, k, v, g, lens, h0, dout, dhT, dq, dk, dv, dg, dh0};
+    const hipError_t e = dn::launch_linear_bwd(pr, f, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return DN_OK;
+}
+
+dn_status dn_linear_recurrent_fwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* g,
+                                  float* state, void* o, void* stream) {
+    g_err[0] = '\0';
+    dn::LinProblem pr;
+    Dims d;
+    DN_TRY(linear_shape(shape, true, &pr, &d));
+    const size_t nk = d.BH * d.T * d.dk * d.E, nv = d.BH * d.T * d.dv * d.E, ng = gate_bytes(shape, d);
+    const size_t ns = d.BH * d.dv * d.dk * 4;
+    if (shape->gate == DN_GATE_NONE && g) return fail(DN_ERR_INVALID, "g must be NULL without a gate");
+    DN_TRY(need(q, nk, "q"));
+    DN_TRY(need(k, nk, "k"));
+    DN_TRY(need(v, nv, "v"));
+    DN_TRY(need(g, ng, "g"));
+    DN_TRY(need(state, ns, "state"));
+    DN_TRY(need(o, nv, "o"));
+    DN_TRY(check_buffers({{"q", q, nk, false},
+                          {"k", k, nk, false},
+                          {"v", v, nv, false},
+                          {"g", g, ng, false},
+                          {"state", state, ns, true},
+                          {"o", o, nv, true}}));
+    const hipError_t e = dn::launch_linear_recurrent(pr, q, k, v, g, state, o, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return DN_OK;
 }
 
 const char* dn_status_string(dn_status status) {

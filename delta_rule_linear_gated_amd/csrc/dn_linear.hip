@@ -1,0 +1,384 @@
+// dn_linear.hip -- linear attention with a decay per head: the split of the steps,
+// the launch sequences, the kernels between the chunk kernels (dn_linear_kernels.h)
+// and the recurrent form.
+#include "dn_device.h"
+#include "dn_internal.h"
+#include "dn_linear.h"
+#include "dn_linear_api.h"
+
+namespace dn {
+
+namespace {
+
+// Boundary states of the parallel segments: entry s of snap holds segment s's own
+// contribution (from a zero state) and gets the state the segment starts from,
+//     start_{s+1} = dec_s start_s + end_s,
+// walked first to last (rev: last to first).  A thread owns four elements of one
+// (b, h) state; the next segment's load is issued before the current one is used.
+// Bytes: each entry read and written once; nothing to gain from a tree at the few
+// dozen segments a plan makes.
+__global__ __launch_bounds__(256) void lin_join_kernel(LinArgs a) {
+    const int quads = a.kd * a.nd / 4;   // a multiple of 64
+    const int per = (quads + 255) / 256;
+    const int oi = blockIdx.y;
+    const int bh = blockIdx.x / per, at = (blockIdx.x % per) * 256 + threadIdx.x;
+    if (at >= quads) return;
+    const LinOp& op = a.op[oi];
+    const long se = (long)a.kd * a.nd;
+    float* base = op.snap + bh * op.snap_bh + 4 * at;
+    const float* dec = a.segdec + ((long)oi * a.BH + bh) * a.nseg;
+    f32x4 cur = op.init ? *reinterpret_cast<const f32x4*>(op.init + bh * se + 4 * at) : zero4();
+    auto slot = [&](int i) {   // i-th segment walked -> its entry
+        const int s = op.rev ? a.nseg - 1 - i : i;
+        const int c0 = s * a.seg_len, c1 = min(a.NT, c0 + a.seg_len);
+        return reinterpret_cast<f32x4*>(base + (op.rev ? (c1 - 1) / a.snap : c0 / a.snap) * se);
+    };
+    f32x4 own = *slot(0);
+    for (int i = 0; i + 1 < a.nseg; ++i) {
+        const f32x4 nxt = i + 2 < a.nseg ? *slot(i + 1) : zero4();
+        *slot(i) = cur;
+        cur = cur * dec[op.rev ? a.nseg - 1 - i : i] + own;
+        own = nxt;
+    }
+    *slot(a.nseg - 1) = cur;
+}
+
+// Gate gradient of the steps t0 .. t1 - 1 that one kept state covers:
+//     dg_t = B + sum_{t <= s < t1} (a_s - b_s),   B = e^{g_{t1}} <S_{t1 - 1}, D_{t1}>
+// (the pairs that straddle t1), a_s - b_s summed over the channel blocks of the two
+// evaluations that wrote them.  Restarting from B at every kept state keeps the
+// rounding of the differences from adding up over the sequence.  Sums in 64 bits.
+__global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* h0, const float* s_snap,
+                                                        const float* d_snap, const float* dhT, const float* dots1,
+                                                        int n1, const float* dots2, int n2, float* dg) {
+    __shared__ double part[256];
+    const int bh = blockIdx.x / a.nent, e = blockIdx.x % a.nent, tid = threadIdx.x;
+    const int n = lin_len(a.lens, bh / a.H, a.T);
+    const int len = a.snap * kLinC, t0 = e * len, t1 = min(t0 + len, n);
+    const int tend = min(t0 + len, a.T);
+    const long row = (long)bh * a.T, se = (long)a.kd * a.nd;
+    if (t0 >= n) {
+        for (int t = t0 + tid; t < tend; t += 256) dg[row + t] = 0.f;
+        return;
+    }
+    // B: past the last step the cotangent is dhT and the state the last one
+    const bool last = t1 >= n;
+    const float* S = s_snap + (long)bh * (a.nent + 1) * se + (last ? a.nent : e + 1) * se;
+    const float* D = last ? (dhT ? dhT + bh * se : nullptr) : d_snap + (long)bh * a.nent * se + e * se;
+    double x = 0.0;
+    if (D) {
+        for (long i = 4 * tid; i < se; i += 1024) {
+            const f32x4 u = *reinterpret_cast<const f32x4*>(S + i), v = *reinterpret_cast<const f32x4*>(D + i);
+            x += (double)u[0] * v[0] + (double)u[1] * v[1] + (double)u[2] * v[2] + (double)u[3] * v[3];
+        }
+        if (!last) x *= (double)expf(a.g[row + t1]);
+    }
+    part[tid] = x;
+    __syncthreads();
+    for (int d = 128; d > 0; d /= 2) {
+        if (tid < d) part[tid] += part[tid + d];
+        __syncthreads();
+    }
+    const double B = part[0];
+    __syncthreads();
+    // each thread: a run of consecutive steps, then the sums of the runs after it
+    const int per = (t1 - t0 + 255) / 256, ta = t0 + tid * per, tb = min(ta + per, t1);
+    auto term = [&](int t) {
+        double d = 0.0;
+        for (int i = 0; i < n1; ++i) d += dots1[((long)i * a.BH + bh) * a.T + t];
+        for (int i = 0; i < n2; ++i) d += dots2[((long)i * a.BH + bh) * a.T + t];
+        return d;
+    };
+    double own = 0.0;
+    for (int t = ta; t < tb; ++t) own += term(t);
+    part[tid] = own;
+    __syncthreads();
+    for (int d = 1; d < 256; d *= 2) {   // suffix sums
+        const double y = tid + d < 256 ? part[tid + d] : 0.0;
+        __syncthreads();
+        part[tid] += y;
+        __syncthreads();
+    }
+    double acc = B + (tid < 255 ? part[tid + 1] : 0.0);
+    for (int t = tb - 1; t >= ta; --t) {
+        acc += term(t);
+        dg[row + t] = t == 0 && !h0 ? 0.f : (float)acc;   // the first gate decays nothing without h0
+    }
+    for (int t = t1 + tid; t < tend; t += 256) dg[row + t] = 0.f;
+}
+
+// Recurrent form: T steps of S_t = e^{g_t} S_{t-1} + v_t k_t^T, o_t = S_t q_t for every
+// (b, h), the fp32 state in place.  A workgroup takes 16 state rows, 16 lanes a row
+// (consecutive keys a lane), so that the state, which is nearly all the bytes of a
+// single token, is read and written once in whole cache lines; S q is a DPP sum.
+constexpr int kRecThreads = 256, kRecRows = 16;
+
+template <typename T, int DK>
+__global__ __launch_bounds__(kRecThreads) void lin_recurrent_kernel(const T* q, const T* k, const T* v, const float* g,
+                                                                    int gate, int H, int steps, int DV, float* state,
+                                                                    T* o) {
+    constexpr int E = DK / 16;
+    const int nblk = DV / kRecRows, bh = blockIdx.x / nblk, blk = blockIdx.x % nblk;
+    const int lane = lane_id(), j = lane & 15, row = blk * kRecRows + wave_id() * 4 + (lane >> 4), c0 = j * E;
+    float* srow = state + ((long)bh * DV + row) * DK + c0;
+    const long tok0 = (long)bh * steps;
+    float s[E], kc[E], qc[E], vc, gc;
+    auto fetch = [&](int t, float(&kk)[E], float(&qq)[E], float& vv, float& gg) {
+        const long tok = tok0 + t;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            kk[e] = to_f(k[tok * DK + c0 + e]);
+            qq[e] = to_f(q[tok * DK + c0 + e]);
+        }
+        vv = to_f(v[tok * DV + row]);
+        gg = gate == kLinNone ? 0.f : gate == kLinHead ? g[bh % H] : g[tok];
+    };
+    fetch(0, kc, qc, vc, gc);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[e] = srow[e];
+    for (int t = 0; t < steps; ++t) {
+        float kn[E], qn[E], vn, gn;
+        fetch(min(t + 1, steps - 1), kn, qn, vn, gn);
+        const float d = expf(gc);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            s[e] = s[e] * d + vc * kc[e];
+            sum += s[e] * qc[e];
+        }
+        sum = row16_sum(sum);
+        if (j == 0) o[(tok0 + t) * DV + row] = from_f<T>(sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) kc[e] = kn[e], qc[e] = qn[e];
+        vc = vn, gc = gn;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) srow[e] = s[e];
+}
+
+template <typename T>
+hipError_t rec_launch(const LinProblem& pr, const void* q, const void* k, const void* v, const float* g, float* state,
+                      void* o, hipStream_t s) {
+    const dim3 grid((unsigned)((long)pr.B * pr.H * (pr.dv / kRecRows))), block(kRecThreads);
+#define DN_REC(D)                                                                                                   \
+    case D:                                                                                                         \
+        hipLaunchKernelGGL((lin_recurrent_kernel<T, D>), grid, block, 0, s, static_cast<const T*>(q),               \
+                           static_cast<const T*>(k), static_cast<const T*>(v), g, pr.gate, pr.H, pr.T, pr.dv, state, \
+                           static_cast<T*>(o));                                                                     \
+        break;
+    switch (pr.dk) {
+        DN_REC(16)
+        DN_REC(32)
+        DN_REC(64)
+        DN_REC(128)
+        default: return hipErrorInvalidValue;
+    }
+#undef DN_REC
+    return hipGetLastError();
+}
+
+size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+int blocks_of(int nd, int bf16) { return nd / lin_vb(nd, bf16 != 0); }
+
+// Parallel segments of the steps.  One run of all chunks reads every tensor once; s > 1
+// segments cost a pass over the two tensors of the state and the boundary states, and
+// pay while the device has idle compute units.
+LinPlan lin_plan(const LinProblem& pr, int nops, bool dots) {
+    const int NT = ceil_div(pr.T, kLinC);
+    const long wgs = (long)pr.B * pr.H * blocks_of(pr.dv, pr.bf16) * nops;
+    constexpr long kWant = 512, kMinLen = 4, kMaxSeg = 64;   // two workgroups on each compute unit
+    long ns = wgs > 0 ? (kWant + wgs - 1) / wgs : 1;
+    if (pr.no_scan || 2 * wgs > kWant) ns = 1;
+    if (ns > kMaxSeg) ns = kMaxSeg;
+    if (ns > NT / kMinLen) ns = NT / kMinLen;
+    if (ns < 1) ns = 1;
+    LinPlan p;
+    p.seg_len = NT > 0 ? ceil_div(NT, (int)ns) : 1;
+    if (dots && ns > 1 && p.seg_len > kLinSnap) p.seg_len = ceil_div(p.seg_len, kLinSnap) * kLinSnap;
+    p.nseg = NT > 0 ? ceil_div(NT, p.seg_len) : 1;
+    p.snap = dots ? (p.nseg > 1 && p.seg_len < kLinSnap ? p.seg_len : kLinSnap) : p.seg_len;
+    p.nent = NT > 0 ? ceil_div(NT, p.snap) : 1;
+    return p;
+}
+
+const LinLaunch kLaunch[2][3] = {{lin_f32_k32, lin_f32_k64, lin_f32_k128}, {lin_bf16_k32, lin_bf16_k64, lin_bf16_k128}};
+
+hipError_t launch_chunks(const LinProblem& pr, const LinArgs& a, int mode, hipStream_t s) {
+    const int ki = a.kd <= 32 ? 0 : a.kd == 64 ? 1 : 2;
+    return kLaunch[pr.bf16 ? 1 : 0][ki](a, lin_vb(a.nd, pr.bf16 != 0) / 16, mode, s);
+}
+
+LinArgs base_args(const LinProblem& pr, const LinPlan& pl, const float* g, const int* lens) {
+    LinArgs a{};
+    a.BH = pr.B * pr.H;
+    a.H = pr.H;
+    a.T = pr.T;
+    a.NT = ceil_div(pr.T, kLinC);
+    a.nseg = pl.nseg;
+    a.seg_len = pl.seg_len;
+    a.snap = pl.snap;
+    a.nent = pl.nent;
+    a.g = g;
+    a.gate = pr.gate;
+    a.lens = lens;
+    return a;
+}
+
+void set_dims(LinArgs& a, const LinProblem& pr, int kd, int nd) {
+    a.kd = kd;
+    a.nd = nd;
+    a.nblk = blocks_of(nd, pr.bf16);
+}
+
+// Boundary states of every op of `a` (their y, z, init, snap, rev).
+hipError_t launch_boundaries(const LinProblem& pr, LinArgs a, hipStream_t s) {
+    prof_begin(s, "linear_segments");
+    hipError_t e = launch_chunks(pr, a, kLinState, s);
+    prof_end(s);
+    if (e != hipSuccess) return e;
+    prof_begin(s, "linear_join");
+    const int per = (a.kd * a.nd / 4 + 255) / 256;
+    hipLaunchKernelGGL(lin_join_kernel, dim3((unsigned)(a.BH * per), a.nops), dim3(256), 0, s, a);
+    prof_end(s);
+    return hipGetLastError();
+}
+
+struct LinWs {
+    size_t s_snap, d_snap, segdec, dots1, dots2, total;
+};
+LinWs lin_ws(const LinProblem& pr, int pass) {
+    const size_t BH = (size_t)pr.B * pr.H, se = (size_t)pr.dk * pr.dv * 4;
+    const bool bwd = pass != 0, dots = bwd && pr.gate == kLinScalar;
+    const LinPlan p = lin_plan(pr, bwd ? 3 : 1, dots);
+    const bool keep = p.nseg > 1 || dots;
+    LinWs w{};
+    size_t off = 0;
+    w.s_snap = off;
+    off += keep ? al256(BH * (p.nent + 1) * se) : 0;
+    w.d_snap = off;
+    off += keep && bwd ? al256(BH * p.nent * se) : 0;
+    w.segdec = off;
+    off += p.nseg > 1 ? al256((bwd ? 2 : 1) * BH * p.nseg * 4) : 0;
+    w.dots1 = off;
+    off += dots ? al256((size_t)blocks_of(pr.dk, pr.bf16) * BH * pr.T * 4) : 0;
+    w.dots2 = off;
+    off += dots ? al256((size_t)blocks_of(pr.dv, pr.bf16) * BH * pr.T * 4) : 0;
+    w.total = off;
+    return w;
+}
+
+}  // namespace
+
+size_t lin_workspace_bytes(const LinProblem& pr, int pass) { return lin_ws(pr, pass).total; }
+
+hipError_t launch_linear_fwd(const LinProblem& pr, const LinFwd& f, char* ws, hipStream_t s) {
+    if (pr.B * pr.H == 0) return hipSuccess;
+    const LinPlan pl = lin_plan(pr, 1, false);
+    const LinWs w = lin_ws(pr, 0);
+    LinArgs a = base_args(pr, pl, f.g, f.lens);
+    set_dims(a, pr, pr.dk, pr.dv);
+    LinOp& op = a.op[0];
+    op.x = f.q;
+    op.y = f.k;
+    op.z = f.v;
+    op.out = f.o;
+    op.init = f.h0;
+    op.fin = f.hT;
+    op.snap = pl.nseg > 1 ? reinterpret_cast<float*>(ws + w.s_snap) : nullptr;
+    op.snap_bh = (long)(pl.nent + 1) * pr.dk * pr.dv;
+    op.sn = pr.dk;
+    op.sk = 1;
+    a.nops = 1;
+    a.segdec = reinterpret_cast<float*>(ws + w.segdec);
+    if (pl.nseg > 1) {
+        const hipError_t e = launch_boundaries(pr, a, s);
+        if (e != hipSuccess) return e;
+    }
+    prof_begin(s, "linear_fwd");
+    const hipError_t e = launch_chunks(pr, a, kLinOut, s);
+    prof_end(s);
+    return e;
+}
+
+hipError_t launch_linear_bwd(const LinProblem& pr, const LinBwd& f, char* ws, hipStream_t s) {
+    if (pr.B * pr.H == 0) return hipSuccess;
+    const bool dots = pr.gate == kLinScalar;
+    const LinPlan pl = lin_plan(pr, 3, dots);
+    const LinWs w = lin_ws(pr, 1);
+    const bool keep = pl.nseg > 1 || dots;
+    float* s_snap = keep ? reinterpret_cast<float*>(ws + w.s_snap) : nullptr;
+    float* d_snap = keep ? reinterpret_cast<float*>(ws + w.d_snap) : nullptr;
+    const long se = (long)pr.dk * pr.dv;
+    LinArgs base = base_args(pr, pl, f.g, f.lens);
+    base.segdec = reinterpret_cast<float*>(ws + w.segdec);
+    LinOp dq{}, dk{}, dv{};
+    dq.x = f.dout, dq.y = f.v, dq.z = f.k, dq.out = f.dq;
+    dq.init = f.h0, dq.snap = s_snap, dq.snap_bh = (pl.nent + 1) * se, dq.sn = 1, dq.sk = pr.dk;
+    dv.x = f.k, dv.y = f.q, dv.z = f.dout, dv.out = f.dv, dv.rev = 1;
+    dv.init = f.dhT, dv.fin = f.dh0, dv.snap = d_snap, dv.snap_bh = pl.nent * se, dv.sn = pr.dk, dv.sk = 1;
+    dk.x = f.v, dk.y = f.dout, dk.z = f.q, dk.out = f.dk, dk.rev = 1;
+    dk.init = f.dhT, dk.snap = d_snap, dk.snap_bh = pl.nent * se, dk.sn = 1, dk.sk = pr.dk;
+    hipError_t e = hipSuccess;
+    if (pl.nseg > 1) {
+        LinArgs a = base;
+        set_dims(a, pr, pr.dk, pr.dv);
+        a.nops = 2;
+        a.op[0] = dv;
+        a.op[1] = dv;
+        a.op[0].y = f.k, a.op[0].z = f.v, a.op[0].init = f.h0, a.op[0].rev = 0;
+        a.op[0].snap = s_snap, a.op[0].snap_bh = dq.snap_bh;
+        if ((e = launch_boundaries(pr, a, s)) != hipSuccess) return e;
+    }
+    if (dots) {
+        dq.r = f.q, dq.role = 1, dq.dots = reinterpret_cast<float*>(ws + w.dots1);
+        dv.r = f.v, dv.role = 2, dv.dots = reinterpret_cast<float*>(ws + w.dots2);
+    }
+    // evaluations of the same widths and mode share a launch (and their rows in L2)
+    auto run = [&](const LinOp* ops, int n, int kd, int nd, int mode) {
+        LinArgs a = base;
+        set_dims(a, pr, kd, nd);
+        a.nops = n;
+        for (int i = 0; i < n; ++i) a.op[i] = ops[i];
+        return launch_chunks(pr, a, mode, s);
+    };
+    const int mode = dots ? kLinDots : kLinOut;
+    prof_begin(s, "linear_bwd");
+    if (pr.dk == pr.dv && !dots) {
+        const LinOp all[3] = {dq, dk, dv};
+        e = run(all, 3, pr.dk, pr.dv, mode);
+    } else if (pr.dk == pr.dv) {
+        const LinOp two[2] = {dq, dv};
+        e = run(two, 2, pr.dk, pr.dv, mode);
+        if (e == hipSuccess) e = run(&dk, 1, pr.dv, pr.dk, kLinOut);
+    } else {
+        if (dots) {
+            e = run(&dq, 1, pr.dv, pr.dk, mode);
+            if (e == hipSuccess) e = run(&dk, 1, pr.dv, pr.dk, kLinOut);
+        } else {
+            const LinOp two[2] = {dq, dk};
+            e = run(two, 2, pr.dv, pr.dk, mode);
+        }
+        if (e == hipSuccess) e = run(&dv, 1, pr.dk, pr.dv, mode);
+    }
+    prof_end(s);
+    if (e != hipSuccess || !dots || pr.T == 0) return e;
+    prof_begin(s, "linear_dgate");
+    set_dims(base, pr, pr.dk, pr.dv);
+    hipLaunchKernelGGL(lin_dgate_kernel, dim3((unsigned)(base.BH * pl.nent)), dim3(256), 0, s, base, f.h0, s_snap, d_snap,
+                       f.dhT, dq.dots, blocks_of(pr.dk, pr.bf16), dv.dots, blocks_of(pr.dv, pr.bf16), f.dg);
+    prof_end(s);
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_recurrent(const LinProblem& pr, const void* q, const void* k, const void* v, const float* g,
+                                   float* state, void* o, hipStream_t s) {
+    if ((long)pr.B * pr.H * pr.T == 0) return hipSuccess;
+    prof_begin(s, "linear_recurrent");
+    const hipError_t e = pr.bf16 ? rec_launch<bf16>(pr, q, k, v, g, state, o, s)
+                                 : rec_launch<float>(pr, q, k, v, g, state, o, s);
+    prof_end(s);
+    return e;
+}
+
+}  // namespace dn

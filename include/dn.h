@@ -91,7 +91,9 @@ typedef enum {
 
 typedef enum { DN_F32 = 0, DN_BF16 = 1 } dn_dtype;
 
-typedef enum { DN_GATE_NONE = 0, DN_GATE_SCALAR = 1, DN_GATE_VECTOR = 2 } dn_gate;
+/* DN_GATE_HEAD: one constant log-decay per head, g [H] (the linear-attention and tree
+ * entry points only; the others return DN_ERR_INVALID for it). */
+typedef enum { DN_GATE_NONE = 0, DN_GATE_SCALAR = 1, DN_GATE_VECTOR = 2, DN_GATE_HEAD = 3 } dn_gate;
 
 /* Which call a workspace is sized for. */
 typedef enum {
@@ -306,6 +308,49 @@ dn_status dn_chunk_phase_bwd(const dn_shape* shape, const void* q, const void* k
                              const void* dout, const float* dhT_re, const float* dhT_im, const float* states, void* dq,
                              void* dk, void* dv, float* dbeta, float* dg, float* dtheta, float* dh0_re, float* dh0_im,
                              void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Linear attention with a decay per head (the recurrence of the operator above without
+ * its erase; the linear-attention family the ReWY and KLA abstracts set the delta rule
+ * against):
+ *     S_t = exp(g_t) S_{t-1} + v_t k_t^T,     o_t = S_t q_t,     S_0 = h0, hT = S_T,
+ * over whole sequences in chunks of 64 steps, and its gradients.
+ *   shape  : B, H, T >= 0 with B*H <= 65535; dk, dv in {16, 32, 64, 128} (they may
+ *            differ); dtype; gate: DN_GATE_NONE (no decay), DN_GATE_SCALAR (g [B][H][T],
+ *            with its gradient) or DN_GATE_HEAD (g [H], a constant of the model: no
+ *            gradient is formed); C unused; flags 0 or DN_FLAG_NO_SCAN (one run of the
+ *            steps per head, never parallel segments); other flags and gates:
+ *            DN_ERR_UNSUPPORTED
+ *   lens   : int32 [B] on the device or NULL: the steps of each batch element (clamped
+ *            to 0 .. T).  Steps from there on are not part of the sequence: what the
+ *            inputs hold there is not used, hT is the state after the last step, o, dq,
+ *            dk, dv and dg are zero there
+ *   g      : any value below -1000 acts as -1000 (a factor of zero: -inf resets the
+ *            state); positive values grow the state and overflow as the recurrence does
+ *   forward : q, k, v, g (NULL iff no gate), h0 (NULL = zero) -> o, hT (NULL = not wanted)
+ *   backward: the vector-Jacobian products of L = <o, dout> + <hT, dhT> (dhT NULL =
+ *            zero): dq, dk, dv, dg (DN_GATE_SCALAR only, else NULL), dh0 (NULL = not
+ *            wanted); nothing of the forward is kept
+ *   ws     : >= dn_linear_workspace_bytes(shape, DN_PASS_FWD or DN_PASS_BWD)
+ * States, running sums and gate gradients are held to fp32 for bf16 I/O too.  Layouts,
+ * validation and errors as for dn_chunk_fwd.
+ */
+size_t dn_linear_workspace_bytes(const dn_shape* shape, int pass);
+dn_status dn_linear_fwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* g,
+                        const int32_t* lens, const float* h0, void* o, float* hT, void* ws, size_t ws_bytes,
+                        void* stream);
+dn_status dn_linear_bwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* g,
+                        const int32_t* lens, const float* h0, const void* dout, const float* dhT, void* dq, void* dk,
+                        void* dv, float* dg, float* dh0, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Its recurrent form (decode): T steps per batch element and head, the state (fp32
+ * [B][H][dv][dk]) updated in place, as dn_recurrent_fwd.
+ *   shape  : dk in {16, 32, 64, 128}, dv a positive multiple of 16; gate as for
+ *            dn_linear_fwd; C unused; flags as for dn_linear_fwd
+ */
+dn_status dn_linear_recurrent_fwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* g,
+                                  float* state, void* o, void* stream);
 
 /* Static description of a status code. */
 const char* dn_status_string(dn_status status);
