@@ -11,7 +11,6 @@ namespace dn {
 enum LinGate { kLinNone = 0, kLinScalar = 1, kLinHead = 2 };
 
 constexpr int kLinC = 64;         // steps of a chunk
-constexpr int kLinThreads = 256;  // four waves: one per 16 steps of a chunk
 constexpr int kLinSnap = 16;      // chunks between kept states, for the gate gradient
 
 // One evaluation of
@@ -29,7 +28,7 @@ struct LinOp {
     void* out;
     const float* init;   // state before the first step (NULL: zero)
     float* fin;          // state after the last one (NULL: not wanted)
-    float* snap;         // kept states [BH][nent + 1 or nent][dv][dk] (see LinArgs)
+    float* snap;         // kept states [BH][nent + 1][dv][dk] (see LinArgs)
     long snap_bh;        // floats of one (b, h) there
     int sn, sk;          // strides of state element (z channel, y channel) in init, fin, snap
     int rev;
@@ -42,9 +41,10 @@ struct LinOp {
     int role;
 };
 
-// State entries: forward, entry e = the state before chunk e * snap and entry nent the
-// last state; rev, entry e = the state that enters chunks [e * snap, (e + 1) * snap)
-// from the right.  Parallel segments cover seg_len chunks (a multiple of snap).
+// State entries: forward, entry e = the state before chunk e * snap; rev, entry e = the
+// state that enters chunks [e * snap, (e + 1) * snap) from the right; entry nent = the
+// last state of the evaluation.  Parallel segments cover seg_len chunks (a multiple of
+// snap).
 struct LinArgs {
     LinOp op[3];
     int nops, BH, H, T, NT;
@@ -74,6 +74,10 @@ __device__ __forceinline__ int lin_len(const int* lens, int b, int T) {
 }
 
 enum LinMode { kLinState = 0, kLinOut = 1, kLinDots = 2 };
+// Waves a SIMD holds at once: the registers of fp32 rows leave room for two.
+__host__ __device__ constexpr int lin_waves(int mode, bool bf16) { return mode == 0 || !bf16 ? 2 : 4; }
+// Four waves carry the state; four more form the outputs.
+__host__ __device__ constexpr int lin_threads(int mode) { return mode == kLinState ? 256 : 512; }
 typedef hipError_t (*LinLaunch)(const LinArgs& a, int nv, int mode, hipStream_t s);
 hipError_t lin_bf16_k32(const LinArgs&, int, int, hipStream_t);
 hipError_t lin_bf16_k64(const LinArgs&, int, int, hipStream_t);

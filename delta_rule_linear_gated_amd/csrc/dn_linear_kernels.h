@@ -11,8 +11,9 @@
 // Every product is formed transposed so that its accumulator is the next one's
 // operand or a row piece in memory: P^T stays in registers (a lane's four
 // accumulator rows are four consecutive K slots of the product with z), out^T
-// gives a lane 4 NV consecutive channels of one step, S^T four consecutive
-// channels of y.  A wave owns 16 steps of the outputs and a share of the state.
+// gives a lane 16-byte pieces of one step's channels, S^T four consecutive channels
+// of y.  Four waves form the outputs, 16 steps each; four more the state, so
+// that the two halves of a chunk's work, which only share the tiles, run side by side.
 //
 // Rounding (bf16 I/O): P enters its product with z as two bf16 parts (16 bits: a
 // sequence of one step has a single P, whose rounding nothing averages), S is
@@ -23,6 +24,8 @@
 // with x in three parts too: that gradient is an fp32 sum of x . S terms.
 // fp32 I/O: every product on fp32 matrix-core steps.
 #pragma once
+
+#include <type_traits>
 
 #include "dn_device.h"
 #include "dn_linear.h"
@@ -62,12 +65,30 @@ template <> struct LinT<float> {
     }
 };
 
-// x as three bf16 parts: x = a + b + c up to 2^-24 of x.
-__device__ __forceinline__ void split3(float x, bf16& a, bf16& b, bf16& c) {
-    a = (bf16)x;
-    const float r = x - (float)a;
-    b = (bf16)r;
-    c = (bf16)(r - (float)b);
+// Buffer accesses: loads past the range give zero, stores past it do nothing, so that
+// rows past a sequence's end need neither branches (behind which the compiler would
+// wait for every access in flight, the outputs' stores among them: 1.8 times the time of
+// a chunk) nor selects.  The base is uniform; kNowhere is past every range.
+typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
+typedef __attribute__((ext_vector_type(2))) unsigned u32x2;
+constexpr int kNowhere = 0x7ffffff0;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t lin_range(const void* base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes > 0 ? bytes : 0, 0x00020000);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int at) {
+    return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+}
+
+// Two floats as two packed bf16; what that leaves of them stays in a, b.  N such steps
+// hold 8 N bits of each.  (Written on pairs: one conversion and four more operations a
+// step.)
+__device__ __forceinline__ unsigned take_bf16(float& a, float& b) {
+    typedef __attribute__((ext_vector_type(2))) float f32x2;
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+    const unsigned u = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{a, b}), bf16x2));
+    a -= __builtin_bit_cast(float, u << 16);
+    b -= __builtin_bit_cast(float, u & 0xffff0000u);
+    return u;
 }
 
 template <typename T, int KD, int NV, bool DG> struct LinLds {
@@ -77,25 +98,30 @@ template <typename T, int KD, int NV, bool DG> struct LinLds {
     T y[kLinC * LY];
     T z[kLinC * LZ];
     T s[NS][VB * LY];
-    // per parity: G (two floats), e^G, e^{G_63 - G}; the chunk's factor
-    float hi[2][kLinC], lo[2][kLinC], eg[2][kLinC], ew[2][kLinC], etot[2];
+    // R: G from the first step of the row's 16 (two floats); e^{G_63 - G};
+    // e^{G_16w - G_j} of the rows j before 16 w, w = 1, 2, 3; e^{G_16w}; the chunk's factor
+    float hi[kLinC], lo[kLinC], ew[kLinC], tab[3][kLinC], eref[4], etot;
     float rowe[DG ? 4 : 1][DG ? kLinC : 1], colb[DG ? kLinC : 1];
 };
 
-// Log-decay (base 2) that the state takes when step t is entered: the step's own
-// gate, or with rev that of the step after it; none past the length.  Below -1000 a
-// factor is zero in fp32 whatever the rest, so that -inf (a reset) gives no inf - inf.
-__device__ __forceinline__ double lin_gate(const LinArgs& a, int bh, int h, int n, int t, int rev) {
+// Gate that the state takes when step t is entered: the step's own, or with rev that of
+// the step after it; none past the length.  The load is free of branches (addresses
+// clamped), so that nothing waits for it before lin_log2 uses it.
+__device__ __forceinline__ float lin_gate(const LinArgs& a, const float* g, int n, int t, int rev) {
     const int at = rev ? t + 1 : t;
-    if (a.gate == kLinNone || at >= n || t < 0) return 0.0;
-    float g = a.gate == kLinHead ? a.g[h] : a.g[(long)bh * a.T + at];
-    g = g < -1000.f ? -1000.f : g;   // NaN stays
-    return (double)g * 1.4426950408889634;
+    return a.gate == kLinNone ? 0.f : g[a.gate == kLinScalar ? min(at, n - 1) : 0];
+}
+// Its logarithm to base 2.  Below -1000 a factor is zero in fp32 whatever the rest, so
+// that -inf (a reset) gives no inf - inf; NaN stays.
+__device__ __forceinline__ double lin_log2(float g, int n, int t, int rev) {
+    if ((rev ? t + 1 : t) >= n) return 0.0;
+    return (double)(g < -1000.f ? -1000.f : g) * 1.4426950408889634;
 }
 
 template <typename T, int KD, int NV, int MODE>
-__global__ __launch_bounds__(kLinThreads, 2) void lin_kernel(LinArgs a) {
+__global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2)) void lin_kernel(LinArgs a) {
     constexpr bool OUT = MODE != kLinState, DG = MODE == kLinDots;
+    constexpr int TH = lin_threads(MODE);
     using X = LinT<T>;
     using Frag = typename X::Frag;
     using L = LinLds<T, KD, NV, DG>;
@@ -103,9 +129,13 @@ __global__ __launch_bounds__(kLinThreads, 2) void lin_kernel(LinArgs a) {
     constexpr int XF = KD / (4 * E);                         // fragments of an x row
     constexpr int WV = 4 / NV;                               // waves that share a state tile column
     constexpr int CT = KD / 16 / WV > 0 ? KD / 16 / WV : 1;  // state tiles of a wave
-    constexpr int PY = KD / E, NY = (kLinC * PY + kLinThreads - 1) / kLinThreads;   // 16-byte pieces
-    constexpr int PZ = VB / E, NZ = (kLinC * PZ + kLinThreads - 1) / kLinThreads;
+    constexpr int PY = KD / E, NY = (kLinC * PY + TH - 1) / TH;   // 16-byte pieces
+    constexpr int PZ = VB / E, NZ = (kLinC * PZ + TH - 1) / TH;
     __shared__ __align__(16) L s;
+    // z channel of accumulator element i of lane group q in output tile `tile`: a lane's
+    // elements of TP tiles are 16 bytes of a row, and the four groups' follow each other
+    constexpr int TP = sizeof(T) == 2 && NV > 1 ? 2 : 1;
+    auto out_col = [](int tile, int q, int i) { return 16 * TP * (tile / TP) + 4 * TP * q + 4 * (tile % TP) + i; };
 
     // Workgroups go to the 8 XCDs in turn: the blocks and evaluations of one (b, h) and
     // segment, which read the same rows, get ids equal mod 8 (one L2).
@@ -119,8 +149,10 @@ __global__ __launch_bounds__(kLinThreads, 2) void lin_kernel(LinArgs a) {
     const int rev = op.rev;
     if (!OUT && (rev ? seg == 0 : seg == a.nseg - 1)) return;   // nothing starts from its end
 
-    const int tid = threadIdx.x, w = wave_id(), l = lane_id(), g = l >> 4, m = l & 15;
-    const int h = bh % a.H, n = lin_len(a.lens, bh / a.H, a.T);
+    // waves 0 .. 3 form the outputs (16 steps each), the others the state
+    const int tid = threadIdx.x, l = lane_id(), g = l >> 4, m = l & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;   // uniform: branches on it are scalar
+    const int h = bh % a.H, n = __builtin_amdgcn_readfirstlane(lin_len(a.lens, bh / a.H, a.T));
     const int c0 = seg * a.seg_len, c1 = min(a.NT, c0 + a.seg_len);
     const int cv = min(c1, (n + kLinC - 1) / kLinC);   // chunks past it hold no step
     const long rows = (long)bh * a.T;
@@ -130,368 +162,443 @@ __global__ __launch_bounds__(kLinThreads, 2) void lin_kernel(LinArgs a) {
     const int vt = w % NV, ct0 = (w / NV) * CT;        // this wave's state tiles
     const bool owns = ct0 * 16 < KD;
     const int vrow = blk * VB + 16 * vt + m;           // the state row of this lane
+    const float* gp = a.gate == kLinNone ? nullptr : a.gate == kLinHead ? a.g + h : a.g + rows;
 
-    // ---- state block
-    f32x4 S[CT];
-    auto each_piece = [&](auto f) {                    // f(tile, offset of its four elements in a state)
-        if (!owns) return;
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            const int k0 = 16 * (ct0 + ct) + 4 * g;
-            if (k0 < a.kd) f(ct, (long)vrow * op.sn + (long)k0 * op.sk);
-        }
-    };
-    auto load_state = [&](const float* base) {
-        each_piece([&](int ct, long at) {
-            if (op.sk == 1) {
-                S[ct] = *reinterpret_cast<const f32x4*>(base + at);
-            } else {
-                const long d = op.sk;
-                S[ct] = f32x4{base[at], base[at + d], base[at + 2 * d], base[at + 3 * d]};
-            }
-        });
-    };
-    auto store_state = [&](float* base, float f) {
-        each_piece([&](int ct, long at) {
-            const f32x4 v = S[ct] * f;
-            if (op.sk == 1) {
-                *reinterpret_cast<f32x4*>(base + at) = v;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) base[at + (long)i * op.sk] = v[i];
-            }
-        });
-    };
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) S[ct] = zero4();
     float* snap = op.snap ? op.snap + bh * op.snap_bh : nullptr;
-    const long se = (long)a.kd * a.nd;                 // floats of a kept state
+    const long se = (long)a.kd * a.nd;                        // floats of a kept state
     const int ent0 = rev ? (c1 - 1) / a.snap : c0 / a.snap;   // the segment's first entry
-    if (OUT && a.nseg > 1) {
-        load_state(snap + ent0 * se);
-    } else if (OUT && op.init) {
-        load_state(op.init + bh * se);
-    }
-    auto put_state = [&]() {
-        if (!OUT || !owns) return;
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            const int at = (16 * vt + m) * LY + 16 * (ct0 + ct) + 4 * g;
-            if constexpr (NS == 1) {
-                st4<T>(&s.s[0][at], S[ct]);
-            } else {
-                typename Vec4<bf16>::type p0, p1, p2;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    bf16 u0, u1, u2;
-                    split3(S[ct][i], u0, u1, u2);
-                    p0[i] = u0, p1[i] = u1, p2[i] = u2;
-                }
-                *reinterpret_cast<typename Vec4<bf16>::type*>(&s.s[0][at]) = p0;
-                *reinterpret_cast<typename Vec4<bf16>::type*>(&s.s[1][at]) = p1;
-                *reinterpret_cast<typename Vec4<bf16>::type*>(&s.s[2][at]) = p2;
-            }
-        }
-    };
-
-    // ---- loads of a chunk (addresses clamped into the sequence, rows past it zeroed later)
+    const int step = rev ? -1 : 1, first = rev ? cv - 1 : c0, count = cv - c0;
+    const int trow = 16 * w + m;                              // an output lane's step within the chunk
     auto time_of = [&](int c, int row) { return c * kLinC + (rev ? kLinC - 1 - row : row); };
-    uint4 yr[NY], zr[NZ];
-    Frag xn[XF], x[XF];
-    const int trow = 16 * w + m;                       // this lane's step within the chunk
-    auto load = [&](int c) {
-#pragma unroll
-        for (int i = 0; i < NY; ++i) {
-            const int id = tid + kLinThreads * i, t = min(time_of(c, (id / PY) % kLinC), n - 1);
-            const int col = (id % PY) * E;
-            yr[i] = *reinterpret_cast<const uint4*>(yp + (long)t * a.kd + (col < a.kd ? col : 0));
-        }
-#pragma unroll
-        for (int i = 0; i < NZ; ++i) {
-            const int id = tid + kLinThreads * i, t = min(time_of(c, (id / PZ) % kLinC), n - 1);
-            zr[i] = *reinterpret_cast<const uint4*>(zp + (long)t * a.nd + (id % PZ) * E);
-        }
-        if constexpr (OUT) {
-            const int t = min(time_of(c, trow), n - 1);
-#pragma unroll
-            for (int f = 0; f < XF; ++f) {
-                const int col = 4 * E * f + E * g;
-                xn[f] = *reinterpret_cast<const Frag*>(xp + (long)t * a.kd + (col < a.kd ? col : 0));
-            }
-        }
-    };
-    auto put_tiles = [&](int c) {
-#pragma unroll
-        for (int i = 0; i < NY; ++i) {
-            const int id = tid + kLinThreads * i, row = id / PY, col = (id % PY) * E;
-            if (kLinC * PY % kLinThreads == 0 || row < kLinC)
-                *reinterpret_cast<uint4*>(&s.y[row * LY + col]) =
-                    time_of(c, row) < n && col < a.kd ? yr[i] : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < NZ; ++i) {
-            const int id = tid + kLinThreads * i, row = id / PZ;
-            if (kLinC * PZ % kLinThreads == 0 || row < kLinC)
-                *reinterpret_cast<uint4*>(&s.z[row * LZ + (id % PZ) * E]) =
-                    time_of(c, row) < n ? zr[i] : make_uint4(0u, 0u, 0u, 0u);
-        }
-        if constexpr (OUT) {
-            const bool ok = time_of(c, trow) < n;
-#pragma unroll
-            for (int f = 0; f < XF; ++f) {
-                const uint4 v = __builtin_bit_cast(uint4, xn[f]);
-                x[f] = __builtin_bit_cast(Frag, ok && 4 * E * f + E * g < a.kd ? v : make_uint4(0u, 0u, 0u, 0u));
-            }
-        }
-    };
-    // running log-decay of a chunk: lane = row, sums in 64 bits (wave 0, which has the
-    // fewest pairs under the diagonal)
-    double dec = 0.0;                                  // of the run so far
-    auto put_gates = [&](double x2, int par) {
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const double y2 = __shfl_up(x2, d);
-            if (l >= d) x2 += y2;
-        }
-        const double tot = __shfl(x2, 63);
-        const float hi = (float)x2, lo = (float)(x2 - (double)hi);
-        const float e = exp2_hw(hi);
-        s.hi[par][l] = hi;
-        s.lo[par][l] = lo;
-        s.eg[par][l] = e + e * lo * 0.69314718f;
-        s.ew[par][l] = exp2_hw((float)(tot - x2));
-        if (l == 63) s.etot[par] = exp2_hw((float)tot);
-        dec += tot;
-    };
 
-    const int step = rev ? -1 : 1;
-    const int first = rev ? cv - 1 : c0, count = cv - c0;
-    if (count > 0) {
-        load(first);
-        if (w == 0) put_gates(lin_gate(a, bh, h, n, time_of(first, l), rev), 0);
-        put_tiles(first);
-        put_state();
-    }
-    int par = 0;
-    for (int ci = 0; ci < count; ++ci, par ^= 1) {
-        const int c = first + step * ci;
-        const bool more = ci + 1 < count;
-        __syncthreads();
-        double gn = 0.0;
-        if (more) {
-            load(c + step);
-            if (w == 0) gn = lin_gate(a, bh, h, n, time_of(c + step, l), rev);
+    // The run of one wave of the outputs (O) or of the state: the same barriers in both, and
+    // registers for one of them only.
+    auto run = [&](auto outs) {
+        constexpr bool O = decltype(outs)::value;
+        // ---- tiles of a chunk: 16-byte pieces, places in bytes from the chunk's first row
+        u32x4 yr[NY], zr[NZ];
+        Frag xn[O ? XF : 1], x[O ? XF : 1];
+        auto row_at = [&](int row, int width) { return (rev ? kLinC - 1 - row : row) * width * (int)sizeof(T); };
+        int yo[NY], zo[NZ];
+#pragma unroll
+        for (int i = 0; i < NY; ++i) {
+            const int id = tid + TH * i, col = (id % PY) * E;
+            yo[i] = col < a.kd && id / PY < kLinC ? row_at(id / PY, a.kd) + col * (int)sizeof(T) : kNowhere;
         }
-        if constexpr (DG) {   // the states the gate's gradient is summed from
-            const int e = c / a.snap;
-            if (snap && (rev ? (c + 1) % a.snap == 0 || ci == 0 : c % a.snap == 0) && !(a.nseg > 1 && e == ent0))
-                store_state(snap + e * se, 1.f);
+#pragma unroll
+        for (int i = 0; i < NZ; ++i) {
+            const int id = tid + TH * i;
+            zo[i] = id / PZ < kLinC ? row_at(id / PZ, a.nd) + (id % PZ) * 16 : kNowhere;
         }
-        f32x4 acc[NV];
-        if constexpr (OUT) {
-            const int tt = time_of(c, trow);
-            // rows of the other factor of the gate's gradient, 4 NV channels of this lane's step
-            T r[DG ? 4 * NV : 1];
-            float dot = 0.f, col = 0.f;
+        const int xo = row_at(trow, a.kd) + 16 * g;
+        auto load = [&](int c) {
+            const int row0 = c * kLinC, live = min(n - row0, kLinC);
+            const auto yb = lin_range(yp + (long)row0 * a.kd, live * a.kd * (int)sizeof(T));
+            const auto zb = lin_range(zp + (long)row0 * a.nd, (live * a.nd - blk * VB) * (int)sizeof(T));
+#pragma unroll
+            for (int i = 0; i < NY; ++i) yr[i] = load16(yb, yo[i]);
+#pragma unroll
+            for (int i = 0; i < NZ; ++i) zr[i] = load16(zb, zo[i]);
+            if constexpr (O) {
+                const auto xb = lin_range(xp + (long)row0 * a.kd, live * a.kd * (int)sizeof(T));
+#pragma unroll
+                for (int f = 0; f < XF; ++f)
+                    xn[f] = __builtin_bit_cast(
+                        Frag, load16(xb, KD > 32 || 4 * E * f + E * g < a.kd ? xo + 64 * f : kNowhere));
+            }
+        };
+        auto put_tiles = [&]() {
+#pragma unroll
+            for (int i = 0; i < NY; ++i) {
+                const int id = tid + TH * i;
+                if (kLinC * PY % TH == 0 || id / PY < kLinC)
+                    *reinterpret_cast<u32x4*>(&s.y[(id / PY) * LY + (id % PY) * E]) = yr[i];
+            }
+#pragma unroll
+            for (int i = 0; i < NZ; ++i) {
+                const int id = tid + TH * i;
+                if (kLinC * PZ % TH == 0 || id / PZ < kLinC)
+                    *reinterpret_cast<u32x4*>(&s.z[(id / PZ) * LZ + (id % PZ) * E]) = zr[i];
+            }
+            if constexpr (O) {
+#pragma unroll
+                for (int f = 0; f < XF; ++f) x[f] = xn[f];
+            }
+        };
+        // ---- running log-decay of a chunk: lane = row, sums in 64 bits.  One wave forms it
+        // (of the outputs' the one with the fewest pairs under the diagonal) and holds it
+        // until the chunk before is done.
+        const bool gates = wave == 0;
+        double dec = 0.0;                                  // of the run so far
+        float ghi = 0.f, glo = 0.f, gew = 0.f, gtab[4] = {}, getot = 0.f, geref = 0.f;
+        auto form_gates = [&](double x2) {
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const double y2 = __shfl_up(x2, d);
+                if (l >= d) x2 += y2;
+            }
+            const double tot = __shfl(x2, 63), own = __shfl(x2, l & 48);
+            ghi = (float)(x2 - own), glo = (float)(x2 - own - (double)ghi);
+            gew = exp2_hw((float)(tot - x2));
+            getot = exp2_hw((float)tot);
+            geref = exp2_hw((float)own);
+            if constexpr (OUT) {
+#pragma unroll
+                for (int u = 1; u < 4; ++u) gtab[u] = exp2_hw((float)(__shfl(x2, 16 * u) - x2));
+            }
+            dec += tot;
+        };
+        auto put_gates = [&]() {
+            s.ew[l] = gew;
+            if (l == 0) s.etot = getot;
+            if constexpr (OUT) {
+                s.hi[l] = ghi, s.lo[l] = glo;
+                if ((l & 15) == 0) s.eref[l >> 4] = geref;
+#pragma unroll
+                for (int u = 1; u < 4; ++u) s.tab[u - 1][l] = gtab[u];
+            }
+        };
+        auto put_dot = [&](int c, int at, float d) {
             if constexpr (DG) {
-                const T* rp = static_cast<const T*>(op.r) + (rows + min(tt, n - 1)) * a.nd + blk * VB + 4 * NV * g;
-                typedef typename Vec4<T>::type V4;
+                const auto db = lin_range(op.dots + ((long)blk * a.BH + bh) * a.T + c * kLinC, min(n - c * kLinC, kLinC) * 4);
+                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, d), db, at, 0, 0);
+            }
+        };
+        // ---- state block: element pieces of this lane in global memory and in LDS
+        f32x4 S[O ? 1 : CT];
+        auto each_piece = [&](auto f) {                    // f(tile, offset of its four elements)
+            if (!owns) return;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const V4 v = *reinterpret_cast<const V4*>(rp + 4 * i);
+            for (int ct = 0; ct < CT; ++ct) {
+                const int k0 = 16 * (ct0 + ct) + 4 * g;
+                if (k0 < a.kd) f(ct, (long)vrow * op.sn + (long)k0 * op.sk);
+            }
+        };
+        auto load_state = [&](const float* base) {
+            each_piece([&](int ct, long at) {
+                if (op.sk == 1) {
+                    S[ct] = *reinterpret_cast<const f32x4*>(base + at);
+                } else {
+                    const long d = op.sk;
+                    S[ct] = f32x4{base[at], base[at + d], base[at + 2 * d], base[at + 3 * d]};
+                }
+            });
+        };
+        auto store_state = [&](float* base, float f) {
+            each_piece([&](int ct, long at) {
+                const f32x4 v = S[ct] * f;
+                if (op.sk == 1) {
+                    *reinterpret_cast<f32x4*>(base + at) = v;
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) r[4 * i + e] = tt < n ? (T)v[e] : (T)0.f;
+                    for (int i = 0; i < 4; ++i) base[at + (long)i * op.sk] = v[i];
+                }
+            });
+        };
+        auto put_state = [&]() {
+            if (!owns) return;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const int at = (16 * vt + m) * LY + 16 * (ct0 + ct) + 4 * g;
+                if constexpr (NS == 1) {
+                    st4<T>(&s.s[0][at], S[ct]);
+                } else {
+                    float v0 = S[ct][0], v1 = S[ct][1], v2 = S[ct][2], v3 = S[ct][3];
+#pragma unroll
+                    for (int p = 0; p < NS; ++p) {
+                        const u32x2 v = {take_bf16(v0, v1), take_bf16(v2, v3)};
+                        *reinterpret_cast<u32x2*>(&s.s[p][at]) = v;
+                    }
                 }
             }
+        };
+        if constexpr (!O) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) acc[i] = zero4();
-            // ---- from earlier chunks
+            for (int ct = 0; ct < CT; ++ct) S[ct] = zero4();
+            if (OUT && a.nseg > 1)
+                load_state(snap + ent0 * se);
+            else if (OUT && op.init)
+                load_state(op.init + bh * se);
+        }
+
+        if (count > 0) {
+            const float g0 = lin_gate(a, gp, n, time_of(first, l), rev);
+            load(first);
+            if (gates) {
+                form_gates(lin_log2(g0, n, time_of(first, l), rev));
+                put_gates();
+            }
+            put_tiles();
+            if constexpr (OUT && !O) put_state();
+        }
+        for (int ci = 0; ci < count; ++ci) {
+            const int c = first + step * ci;
+            const int next = ci + 1 < count ? c + step : c;   // after the last chunk: it again, unused
+            __syncthreads();
+            const float gn = lin_gate(a, gp, n, time_of(next, l), rev);
+            load(next);
+            if constexpr (O) {
+                f32x4 acc[NV];
+                const int row0 = c * kLinC;
+                // rows of the other factor of the gate's gradient, the lane's output channels
+                T r[DG ? 4 * NV : 1];
+                float dot = 0.f, col = 0.f;
+                if constexpr (DG) {
+                    const auto rb = lin_range(static_cast<const T*>(op.r) + (rows + row0) * a.nd + blk * VB,
+                                              (min(n - row0, kLinC) * a.nd - blk * VB) * (int)sizeof(T));
 #pragma unroll
-            for (int f = 0; f < XF; ++f)
+                    for (int i = 0; i < NV; i += TP) {
+                        const int at = row_at(trow, a.nd) + out_col(i, g, 0) * (int)sizeof(T);
+                        if constexpr (TP * 4 * sizeof(T) == 16) {
+                            const Frag v = __builtin_bit_cast(Frag, load16(rb, at));
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int at = (4 * NV * (m >> 2) + 4 * i + (m & 3)) * LY + 4 * E * f + E * g;
+                            for (int e = 0; e < E; ++e) r[4 * i + e] = v[e];
+                        } else {
+                            typedef typename Vec4<T>::type V4;
+                            const V4 v = __builtin_bit_cast(V4, __builtin_amdgcn_raw_buffer_load_b64(rb, at, 0, 0));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) r[4 * i + e] = v[e];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NV; ++i) acc[i] = zero4();
+                // ---- from earlier chunks
+#pragma unroll
+                for (int f = 0; f < XF; ++f)
 #pragma unroll
                     for (int p = 0; p < NS; ++p)
-                        acc[i] = X::mma(*reinterpret_cast<const Frag*>(&s.s[p][at]), x[f], acc[i]);
-                }
-            const float eg = s.eg[par][trow];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                acc[i] = acc[i] * eg;
-                if constexpr (DG) {
+                        for (int i = 0; i < NV; ++i) {   // consecutive steps: different accumulators
+                            const int at = out_col(i, m >> 2, m & 3) * LY + 4 * E * f + E * g;
+                            acc[i] = X::mma(*reinterpret_cast<const Frag*>(&s.s[p][at]), x[f], acc[i]);
+                        }
+                // The factors of a step's row: e^{G_16w} and e^{R}; pairs with the 16-step blocks before
+                // take theirs in between (the table), so that only the diagonal block forms a factor
+                // for each pair.
+                const float er = s.eref[w], hi = s.hi[trow], lo = s.lo[trow], es = exp2_hw(hi + lo);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dot += acc[i][e] * to_f(r[4 * i + e]);
-                }
-            }
-            // ---- pairs of the chunk
-            const float hi = s.hi[par][trow], lo = s.lo[par][trow];
-            constexpr int NP = JS / 16;
+                for (int i = 0; i < NV; ++i) {
+                    acc[i] = acc[i] * er;
+                    if constexpr (DG) {
 #pragma unroll
-            for (int js = 0; js < kLinC / JS; ++js) {
-                if (js * NP > w) continue;
-                float p[NP][4];
-#pragma unroll
-                for (int u = 0; u < NP; ++u) {
-                    const int jt = js * NP + u;
-                    if (jt > w) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) p[u][i] = 0.f;
-                        continue;
+                        for (int e = 0; e < 4; ++e) dot += acc[i][e] * to_f(r[4 * i + e]);
                     }
-                    f32x4 pa = zero4();
+                }
+                if constexpr (DG) dot *= es;
+                // ---- pairs of the chunk
+                constexpr int NP = JS / 16;
+                auto block = [&](int js, auto diagonal) {   // steps JS js .., the last of them w's own
+                    constexpr bool D = decltype(diagonal)::value;
+                    float p[NP][4];
+                    f32x4 pa[NP];
+#pragma unroll
+                    for (int u = 0; u < NP; ++u) pa[u] = zero4();
 #pragma unroll
                     for (int f = 0; f < XF; ++f)
-                        pa = X::mma(*reinterpret_cast<const Frag*>(&s.y[(16 * jt + m) * LY + 4 * E * f + E * g]), x[f], pa);
-                    const f32x4 hj = *reinterpret_cast<const f32x4*>(&s.hi[par][16 * jt + 4 * g]);
-                    const f32x4 lj = *reinterpret_cast<const f32x4*>(&s.lo[par][16 * jt + 4 * g]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int j = 16 * jt + 4 * g + i;
-                        const float d = (hi - hj[i]) + (lo - lj[i]);
-                        p[u][i] = pa[i] * exp2_hw(j <= trow ? d : -INFINITY);
-                    }
-                    if constexpr (DG) {
-                        if (op.role == 2) {   // E = P o (r z^T), summed along both axes
-                            f32x4 q = zero4();
-                            const T* zr_ = &s.z[(16 * jt + m) * LZ + 4 * NV * g];
-                            if constexpr (4 * NV >= E) {
+                        for (int u = 0; u < NP; ++u)   // a tile past the diagonal is formed too and masked below
+                            pa[u] = X::mma(
+                                *reinterpret_cast<const Frag*>(&s.y[(16 * (js * NP + u) + m) * LY + 4 * E * f + E * g]),
+                                x[f], pa[u]);
 #pragma unroll
-                                for (int f = 0; f < 4 * NV / E; ++f) {
-                                    Frag rb;
+                    for (int u = 0; u < NP; ++u) {
+                        const int jt = js * NP + u;
+                        if (!D || jt < w) {
+                            const f32x4 f = *reinterpret_cast<const f32x4*>(&s.tab[w - 1][16 * jt + 4 * g]);
 #pragma unroll
-                                    for (int e = 0; e < E; ++e) rb[e] = r[E * f + e];
-                                    q = X::mma(*reinterpret_cast<const Frag*>(zr_ + E * f), rb, q);
-                                }
-                            } else {   // 16 channels of bf16: half of the K slots are zero
-                                Frag za, rb;
-                                const typename Vec4<T>::type v = *reinterpret_cast<const typename Vec4<T>::type*>(zr_);
-#pragma unroll
-                                for (int e = 0; e < E; ++e) {
-                                    za[e] = e < 4 ? (T)v[e & 3] : (T)0.f;
-                                    rb[e] = e < 4 ? r[e & 3] : (T)0.f;
-                                }
-                                q = X::mma(za, rb, q);
-                            }
+                            for (int i = 0; i < 4; ++i) p[u][i] = pa[u][i] * (D ? f[i] * es : f[i]);
+                        } else {
+                            const f32x4 hj = *reinterpret_cast<const f32x4*>(&s.hi[16 * jt + 4 * g]);
+                            const f32x4 lj = *reinterpret_cast<const f32x4*>(&s.lo[16 * jt + 4 * g]);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const int j = 16 * jt + 4 * g + i;
-                                const float e = j == trow ? 0.f : p[u][i] * q[i];   // the diagonal cancels
-                                col += e;
-                                const float rs = row16_sum(e);
-                                if (m == 0) s.rowe[w][j] = rs;
+                                const float d = (hi - hj[i]) + (lo - lj[i]);
+                                p[u][i] = pa[u][i] * exp2_hw(j <= trow ? d : -INFINITY);
+                            }
+                        }
+                        if constexpr (DG) {
+                            if (op.role == 2) {   // E = P o (r z^T), summed along both axes
+                                f32x4 q = zero4();
+                                const T* zj = &s.z[(16 * jt + m) * LZ];
+                                if constexpr (4 * NV >= E) {
+#pragma unroll
+                                    for (int f = 0; f < 4 * NV / E; ++f) {
+                                        Frag rb;
+#pragma unroll
+                                        for (int e = 0; e < E; ++e) rb[e] = r[E * f + e];
+                                        q = X::mma(*reinterpret_cast<const Frag*>(zj + 4 * E * f + E * g), rb, q);
+                                    }
+                                } else {   // 16 channels of bf16: half of the K slots are zero
+                                    Frag za, rb;
+                                    const typename Vec4<T>::type v = *reinterpret_cast<const typename Vec4<T>::type*>(zj + 4 * g);
+#pragma unroll
+                                    for (int e = 0; e < E; ++e) {
+                                        za[e] = e < 4 ? (T)v[e & 3] : (T)0.f;
+                                        rb[e] = e < 4 ? r[e & 3] : (T)0.f;
+                                    }
+                                    q = X::mma(za, rb, q);
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int j = 16 * jt + 4 * g + i;
+                                    const float e = j == trow ? 0.f : p[u][i] * q[i] * (D ? 1.f : es);   // the diagonal cancels
+                                    col += e;
+                                    const float rs = row16_sum(e);
+                                    if (m == 0) s.rowe[w][j] = rs;
+                                }
                             }
                         }
                     }
+                    constexpr int PP = sizeof(T) == 2 ? 2 : 1;   // parts of P
+                    Frag pf[PP];
+                    if constexpr (PP == 2) {
+                        u32x4 part[PP];
+#pragma unroll
+                        for (int e = 0; e < E; e += 2)
+#pragma unroll
+                            for (int q = 0; q < PP; ++q) part[q][e / 2] = take_bf16(p[e / 4][e & 3], p[e / 4][(e & 3) + 1]);
+#pragma unroll
+                        for (int q = 0; q < PP; ++q) pf[q] = __builtin_bit_cast(Frag, part[q]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) pf[0][e] = from_f<T>(p[0][e]);
+                    }
+                    Frag zf[NV];
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int col0 = sizeof(T) == 2 ? out_col(i, m & 3, 0) : out_col(i, m >> 2, m & 3);
+                        zf[i] = X::load_t(s.z, LZ, js * JS, col0);
+                    }
+#pragma unroll
+                    for (int u = 0; u < PP; ++u)
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) acc[i] = X::mma(zf[i], pf[u], acc[i]);
+                };
+#pragma unroll
+                for (int js = 0; js < kLinC / JS; ++js) {   // whole blocks before w's own, then the rest
+                    if ((js + 1) * NP <= w) block(js, std::false_type{});
                 }
-                constexpr int PP = sizeof(T) == 2 ? 2 : 1;   // parts of P
-                Frag pf[PP];
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float v = p[e / 4][e & 3];
-                    pf[0][e] = from_f<T>(v);
-                    if constexpr (PP == 2) pf[1][e] = from_f<T>(v - to_f(pf[0][e]));
+                for (int i = 0; i < NV; ++i) acc[i] = acc[i] * es;
+                block(w / NP, std::true_type{});
+                // ---- out: 16-byte pieces, 64 consecutive bytes of a step for the four lanes that share it
+                const auto ob = lin_range(static_cast<T*>(op.out) + (rows + row0) * a.nd + blk * VB,
+                                          (min(n - row0, kLinC) * a.nd - blk * VB) * (int)sizeof(T));
+#pragma unroll
+                for (int i = 0; i < NV; i += TP) {
+                    const int at = row_at(trow, a.nd) + out_col(i, g, 0) * (int)sizeof(T);
+                    if constexpr (sizeof(T) == 4) {
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i]), ob, at, 0, 0);
+                    } else {
+                        u32x2 v[TP];
+#pragma unroll
+                        for (int u = 0; u < TP; ++u) {
+                            typename Vec4<bf16>::type b;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) b[e] = (bf16)acc[i + u][e];
+                            v[u] = __builtin_bit_cast(u32x2, b);
+                        }
+                        if constexpr (TP == 2)
+                            __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[0][0], v[0][1], v[1][0], v[1][1]}, ob, at, 0, 0);
+                        else
+                            __builtin_amdgcn_raw_buffer_store_b64(v[0], ob, at, 0, 0);
+                    }
                 }
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int col0 = sizeof(T) == 2 ? 4 * NV * (m & 3) + 4 * i : 4 * NV * (m >> 2) + 4 * i + (m & 3);
-                    const Frag zf = X::load_t(s.z, LZ, js * JS, col0);
-#pragma unroll
-                    for (int u = 0; u < PP; ++u) acc[i] = X::mma(zf, pf[u], acc[i]);
-                }
-            }
-            // ---- out: 4 NV consecutive channels of one step
-            if (tt < a.T) {
-                T* o = static_cast<T*>(op.out) + (rows + tt) * a.nd + blk * VB + 4 * NV * g;
-                const bool ok = tt < n;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) st4<T>(o + 4 * i, ok ? acc[i] : zero4());
-            }
-            if constexpr (DG) {
-                if (op.role == 1) {
-                    dot = sum_lane_groups(dot);
-                    if (g == 0 && tt < n) op.dots[((long)blk * a.BH + bh) * a.T + tt] = dot;
-                } else {
-                    dot = sum_lane_groups(dot + col);
+                if constexpr (DG) {
+                    dot = sum_lane_groups(op.role == 1 ? dot : dot + col);
+                    put_dot(c, op.role == 1 && g == 0 ? row_at(trow, 1) / (int)sizeof(T) * 4 : kNowhere, dot);
                     if (g == 0) s.colb[trow] = dot;
                 }
-            }
-        }
-        // ---- state
-        if (owns) {
-            const float et = s.etot[par];
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) S[ct] = S[ct] * et;
-#pragma unroll
-            for (int js = 0; js < kLinC / JS; ++js) {
-                const Frag zf = X::load_t(s.z, LZ, js * JS, 16 * vt + (sizeof(T) == 2 ? 4 * (m & 3) : m));
-                Frag zw[sizeof(T) == 2 ? 3 : 1];
-#pragma unroll
-                for (int q = 0; q < E / 4; ++q) {
-                    const f32x4 ww = *reinterpret_cast<const f32x4*>(&s.ew[par][js * JS + 16 * q + 4 * g]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float v = to_f(zf[4 * q + i]) * ww[i];
-                        if constexpr (sizeof(T) == 2) {
-                            bf16 u0, u1, u2;
-                            split3(v, u0, u1, u2);
-                            zw[0][4 * q + i] = u0, zw[1][4 * q + i] = u1, zw[2][4 * q + i] = u2;
-                        } else {
-                            zw[0][i] = v;
-                        }
-                    }
+            } else if (owns) {
+                // ---- state
+                if constexpr (DG) {   // the states the gate's gradient is summed from
+                    const int e = c / a.snap;
+                    if (snap && (rev ? (c + 1) % a.snap == 0 || ci == 0 : c % a.snap == 0) && !(a.nseg > 1 && e == ent0))
+                        store_state(snap + e * se, 1.f);
                 }
+                const float et = s.etot;
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    const Frag yf = X::load_t(s.y, LY, js * JS, 16 * (ct0 + ct) + (sizeof(T) == 2 ? 4 * (m & 3) : m));
-                    S[ct] = X::mma(yf, zw[0], S[ct]);
-                    if constexpr (sizeof(T) == 2) {
-                        if (a.gate != kLinNone) {   // without a gate the first part is all of z
-                            S[ct] = X::mma(yf, zw[1], S[ct]);
-                            S[ct] = X::mma(yf, zw[2], S[ct]);
+                for (int ct = 0; ct < CT; ++ct) S[ct] = S[ct] * et;
+#pragma unroll
+                for (int js = 0; js < kLinC / JS; ++js) {
+                    const Frag zf = X::load_t(s.z, LZ, js * JS, 16 * vt + (sizeof(T) == 2 ? 4 * (m & 3) : m));
+                    constexpr int ZP = sizeof(T) == 2 ? 3 : 1;   // parts of z e^{..}
+                    Frag zw[ZP];
+                    if constexpr (ZP == 3) {
+                        u32x4 part[ZP];
+#pragma unroll
+                        for (int e = 0; e < E; e += 2) {
+                            const float* ww = &s.ew[js * JS + 16 * (e / 4) + 4 * g + (e & 3)];
+                            float u = to_f(zf[e]) * ww[0], v = to_f(zf[e + 1]) * ww[1];
+#pragma unroll
+                            for (int p = 0; p < ZP; ++p) part[p][e / 2] = take_bf16(u, v);
                         }
+#pragma unroll
+                        for (int p = 0; p < ZP; ++p) zw[p] = __builtin_bit_cast(Frag, part[p]);
+                    } else {
+                        const f32x4 ww = *reinterpret_cast<const f32x4*>(&s.ew[js * JS + 4 * g]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) zw[0][i] = zf[i] * ww[i];
                     }
+                    Frag yf[CT];
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        yf[ct] = X::load_t(s.y, LY, js * JS, 16 * (ct0 + ct) + (sizeof(T) == 2 ? 4 * (m & 3) : m));
+#pragma unroll
+                    for (int p = 0; p < ZP; ++p)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) S[ct] = X::mma(yf[ct], zw[p], S[ct]);
+                }
+            }
+            if (gates && ci + 1 < count) form_gates(lin_log2(gn, n, time_of(next, l), rev));
+            __syncthreads();
+            if (gates) put_gates();
+            put_tiles();
+            if constexpr (OUT && !O) put_state();
+            if constexpr (DG && O) {
+                if (wave == 0) {
+                    float d = -s.colb[l];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) d += u >= l / 16 ? s.rowe[u][l] : 0.f;
+                    put_dot(c, op.role == 2 ? row_at(l, 1) / (int)sizeof(T) * 4 : kNowhere, d);
                 }
             }
         }
-        if (w == 0 && more) put_gates(gn, par ^ 1);
-        __syncthreads();
-        if constexpr (DG) {
-            const int row = tid, tt = time_of(c, row & (kLinC - 1));
-            if (op.role == 2 && row < kLinC && tt < n) {
-                float d = -s.colb[row];
-                for (int u = row / 16; u < 4; ++u) d += s.rowe[u][row];
-                op.dots[((long)blk * a.BH + bh) * a.T + tt] = d;
-            }
-        }
-        if (more) {
-            put_tiles(c + step);
-            put_state();
-        }
-    }
 
-    // ---- what is left: steps past the length, the last state, the segment's factor
-    if constexpr (OUT) {
-        T* o = static_cast<T*>(op.out) + rows * a.nd + blk * VB;
-        const int from = max(c0, cv) * kLinC, to = min(a.T, c1 * kLinC);
-        for (int t = from + tid / PZ; t < to; t += kLinThreads / PZ)
-            *reinterpret_cast<uint4*>(o + (long)t * a.nd + (tid % PZ) * E) = make_uint4(0u, 0u, 0u, 0u);
-        if (rev ? seg == 0 : seg == a.nseg - 1) {
-            if (DG && !rev && snap) store_state(snap + a.nent * se, 1.f);
-            if (op.fin) {   // rev: back through the first step's gate
-                const float g0 = !rev || n == 0 || a.gate == kLinNone ? 0.f : a.gate == kLinHead ? a.g[h] : a.g[rows];
-                store_state(op.fin + bh * se, expf(g0));
+        // ---- the last state, the segment's own state and factor
+        if constexpr (!O) {
+            if (!OUT) {
+                store_state(snap + ent0 * se, 1.f);
+                if (tid == 0 && blk == 0) a.segdec[((long)oi * a.BH + bh) * a.nseg + seg] = exp2_hw((float)dec);
+            } else if (rev ? seg == 0 : seg == a.nseg - 1) {
+                if (DG && snap) store_state(snap + a.nent * se, 1.f);
+                if (op.fin) {   // rev: back through the first step's gate
+                    const float g0 = !rev || n == 0 || a.gate == kLinNone ? 0.f : a.gate == kLinHead ? a.g[h] : a.g[rows];
+                    store_state(op.fin + bh * se, expf(g0));
+                }
             }
         }
+    };
+    if constexpr (OUT) {
+        if (wave < 4)
+            run(std::true_type{});
+        else
+            run(std::false_type{});
+        // steps past the length
+        T* o = static_cast<T*>(op.out) + rows * a.nd + blk * VB;
+        const int from = max(c0 * kLinC, n), to = min(a.T, c1 * kLinC);
+        for (int t = from + tid / PZ; t < to; t += TH / PZ)
+            *reinterpret_cast<uint4*>(o + (long)t * a.nd + (tid % PZ) * E) = make_uint4(0u, 0u, 0u, 0u);
     } else {
-        store_state(snap + ent0 * se, 1.f);
-        if (tid == 0 && blk == 0) a.segdec[((long)oi * a.BH + bh) * a.nseg + seg] = exp2_hw((float)dec);
+        run(std::false_type{});
     }
 }
 
 template <typename T, int KD, int NV> hipError_t lin_launch_nv(const LinArgs& a, int mode, hipStream_t s) {
     const long units = ((long)a.BH * a.nseg + kXcds - 1) / kXcds * kXcds;
-    const dim3 grid((unsigned)(units * a.nops * a.nblk)), block(kLinThreads);
+    const dim3 grid((unsigned)(units * a.nops * a.nblk)), block(lin_threads(mode));
     switch (mode) {
         case kLinState: hipLaunchKernelGGL((lin_kernel<T, KD, NV, kLinState>), grid, block, 0, s, a); break;
         case kLinOut: hipLaunchKernelGGL((lin_kernel<T, KD, NV, kLinOut>), grid, block, 0, s, a); break;
