@@ -91,13 +91,16 @@ __device__ __forceinline__ unsigned take_bf16(float& a, float& b) {
     return u;
 }
 
-template <typename T, int KD, int NV, bool DG> struct LinLds {
-    static constexpr int VB = 16 * NV, PAD = 16 / sizeof(T);
-    static constexpr int LY = KD + PAD, LZ = VB + PAD;
-    static constexpr int NS = DG && sizeof(T) == 2 ? 3 : 1;   // parts of the state operand
+// LDS rows of y and z are padded for the transposed reads, which take four rows of 32
+// bytes at once (bf16: rows 8 dwords apart modulo 64, or a permutation of that).
+template <typename T, int KD, int NV, int MODE> struct LinLds {
+    static constexpr bool DG = MODE == kLinDots;
+    static constexpr int VB = 16 * NV, E = 16 / sizeof(T), PAD = sizeof(T) == 2 ? 2 * E : E;
+    static constexpr int LY = KD + PAD, LZ = VB + PAD, LS = KD + E;
+    static constexpr int NS = MODE == kLinState ? 0 : DG && sizeof(T) == 2 ? 3 : 1;   // parts of the state operand
     T y[kLinC * LY];
     T z[kLinC * LZ];
-    T s[NS][VB * LY];
+    T s[NS > 0 ? NS : 1][NS > 0 ? VB * LS : 1];
     // R: G from the first step of the row's 16 (two floats); e^{G_63 - G};
     // e^{G_16w - G_j} of the rows j before 16 w, w = 1, 2, 3; e^{G_16w}; the chunk's factor
     float hi[kLinC], lo[kLinC], ew[kLinC], tab[3][kLinC], eref[4], etot;
@@ -124,8 +127,8 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
     constexpr int TH = lin_threads(MODE);
     using X = LinT<T>;
     using Frag = typename X::Frag;
-    using L = LinLds<T, KD, NV, DG>;
-    constexpr int E = X::E, JS = X::JS, VB = 16 * NV, LY = L::LY, LZ = L::LZ, NS = L::NS;
+    using L = LinLds<T, KD, NV, MODE>;
+    constexpr int E = X::E, JS = X::JS, VB = 16 * NV, LY = L::LY, LZ = L::LZ, LS = L::LS, NS = L::NS;
     constexpr int XF = KD / (4 * E);                         // fragments of an x row
     constexpr int WV = 4 / NV;                               // waves that share a state tile column
     constexpr int CT = KD / 16 / WV > 0 ? KD / 16 / WV : 1;  // state tiles of a wave
@@ -299,7 +302,7 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
             if (!owns) return;
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                const int at = (16 * vt + m) * LY + 16 * (ct0 + ct) + 4 * g;
+                const int at = (16 * vt + m) * LS + 16 * (ct0 + ct) + 4 * g;
                 if constexpr (NS == 1) {
                     st4<T>(&s.s[0][at], S[ct]);
                 } else {
@@ -370,7 +373,7 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
                     for (int p = 0; p < NS; ++p)
 #pragma unroll
                         for (int i = 0; i < NV; ++i) {   // consecutive steps: different accumulators
-                            const int at = out_col(i, m >> 2, m & 3) * LY + 4 * E * f + E * g;
+                            const int at = out_col(i, m >> 2, m & 3) * LS + 4 * E * f + E * g;
                             acc[i] = X::mma(*reinterpret_cast<const Frag*>(&s.s[p][at]), x[f], acc[i]);
                         }
                 // The factors of a step's row: e^{G_16w} and e^{R}; pairs with the 16-step blocks before
