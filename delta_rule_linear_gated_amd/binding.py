@@ -31,7 +31,8 @@ DN_NOALLOC_SCRATCH_BYTES = 64 << 20
 EXPORTS = ("dn_states_bytes", "dn_states_layout", "dn_workspace_bytes", "dn_workspace_layout", "dn_chunk_fwd",
            "dn_chunk_fwd_noalloc", "dn_chunk_bwd", "dn_recurrent_fwd", "dn_recurrent_phase_fwd", "dn_phase_states_bytes",
            "dn_phase_workspace_bytes", "dn_chunk_phase_fwd", "dn_chunk_phase_bwd", "dn_linear_workspace_bytes",
-           "dn_linear_fwd", "dn_linear_bwd", "dn_linear_recurrent_fwd", "dn_status_string", "dn_last_error",
+           "dn_linear_fwd", "dn_linear_bwd", "dn_linear_recurrent_fwd", "dn_tree_fwd", "dn_tree_commit",
+           "dn_status_string", "dn_last_error",
            "dn_profile_enable", "dn_profile_collect")
 
 
@@ -95,6 +96,10 @@ def lib():
     L.dn_linear_bwd.restype = i32
     L.dn_linear_recurrent_fwd.argtypes = [sp] + [vp] * 7
     L.dn_linear_recurrent_fwd.restype = i32
+    L.dn_tree_fwd.argtypes = [sp] + [vp] * 11
+    L.dn_tree_fwd.restype = i32
+    L.dn_tree_commit.argtypes = [sp] + [vp] * 7
+    L.dn_tree_commit.restype = i32
     L.dn_status_string.argtypes = [i32]
     L.dn_status_string.restype = ctypes.c_char_p
     L.dn_last_error.argtypes = []
@@ -273,6 +278,18 @@ def dn_linear_recurrent_fwd(shape, q, k, v, g, state, o, stream=None) -> int:
     """Raw call; returns the dn_status (no exception)."""
     return lib().dn_linear_recurrent_fwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(state), _ptr(o),
                                          _stream(stream))
+
+
+def dn_tree_fwd(shape, q, k, v, beta, g, parent, counts, state, o, u, stream=None) -> int:
+    """Raw call; returns the dn_status (no exception)."""
+    return lib().dn_tree_fwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(g), _ptr(parent),
+                             _ptr(counts), _ptr(state), _ptr(o), _ptr(u), _stream(stream))
+
+
+def dn_tree_commit(shape, k, u, g, parent, accept, state, stream=None) -> int:
+    """Raw call; returns the dn_status (no exception)."""
+    return lib().dn_tree_commit(ctypes.byref(shape), _ptr(k), _ptr(u), _ptr(g), _ptr(parent), _ptr(accept), _ptr(state),
+                                _stream(stream))
 
 
 # ------------------------------------------------------------------ convenience
@@ -617,3 +634,50 @@ class LinearAttention(torch.autograd.Function):
         gr = linear_bwd(q, k, v, g, h0, do.contiguous(), None if dhT is None else dhT.contiguous(), lens=lens,
                         want_dh0=h0 is not None)
         return gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["dh0"], None
+
+
+# ------------------------------------------------------------------ trees of drafted tokens
+
+
+def tree_fwd(q, k, v, beta, g, parent, state, counts=None, want_u=True, stream=None, kaczmarz_eps=None):
+    """Every node of a tree of drafted tokens read from ``state`` (fp32 [B,H,dv,dk], unchanged) as if its
+    path had been decoded: q, k [B,H,N,dk], v [B,H,N,dv], N <= 64; ``beta`` [B,H,N] (None: linear
+    attention; eta with ``kaczmarz_eps``); ``g`` None, [H], [B,H,N] or [B,H,N,dk]; ``parent`` int32 [B,N],
+    an earlier node or -1 (the root); ``counts`` int32 [B], the nodes of each batch element.
+    Returns (o [B,H,N,dv], u): u, fp32 [B,H,N,dv] (None unless wanted), is what tree_commit takes."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"q must be [B,H,N,dk] and v [B,H,N,dv], got shapes {tuple(q.shape)}, {tuple(v.shape)}")
+    B, H, N, dk = q.shape
+    dv = v.shape[3]
+    if q.dtype not in _IO_DTYPES:
+        raise ValueError(f"q must be float32 or bfloat16, got {q.dtype}")
+    kind, gshape = _linear_gate(g, B, H, N, dk)
+    f32, i32 = torch.float32, torch.int32
+    _check_tensors(q, {"q": (q, q.dtype, (B, H, N, dk)), "k": (k, q.dtype, (B, H, N, dk)),
+                       "v": (v, q.dtype, (B, H, N, dv)), "beta": (beta, f32, (B, H, N)), "g": (g, f32, gshape),
+                       "parent": (parent, i32, (B, N)), "counts": (counts, i32, (B,)),
+                       "state": (state, f32, (B, H, dv, dk))})
+    sh = make_shape(B, H, N, dk, dv, 64, q.dtype, kind, kaczmarz_eps)
+    o = torch.empty_like(v)
+    u = torch.empty(B, H, N, dv, dtype=f32, device=q.device) if want_u else None
+    _check(dn_tree_fwd(sh, q, k, v, beta, g, parent, counts, state, o, u, stream))
+    return o, u
+
+
+def tree_commit(k, u, g, parent, accept, state, stream=None):
+    """Move ``state`` (fp32 [B,H,dv,dk], in place) along the path that ends at node ``accept`` (int32 [B];
+    -1 accepts nothing) of the tree that tree_fwd read; ``u`` is what it returned.  Returns state."""
+    if k.dim() != 4 or u.dim() != 4:
+        raise ValueError(f"k must be [B,H,N,dk] and u [B,H,N,dv], got shapes {tuple(k.shape)}, {tuple(u.shape)}")
+    B, H, N, dk = k.shape
+    dv = u.shape[3]
+    if k.dtype not in _IO_DTYPES:
+        raise ValueError(f"k must be float32 or bfloat16, got {k.dtype}")
+    kind, gshape = _linear_gate(g, B, H, N, dk)
+    f32, i32 = torch.float32, torch.int32
+    _check_tensors(k, {"k": (k, k.dtype, (B, H, N, dk)), "u": (u, f32, (B, H, N, dv)), "g": (g, f32, gshape),
+                       "parent": (parent, i32, (B, N)), "accept": (accept, i32, (B,)),
+                       "state": (state, f32, (B, H, dv, dk))})
+    sh = make_shape(B, H, N, dk, dv, 64, k.dtype, kind)
+    _check(dn_tree_commit(sh, k, u, g, parent, accept, state, stream))
+    return state

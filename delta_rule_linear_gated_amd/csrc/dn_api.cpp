@@ -14,6 +14,7 @@
 #include "dn.h"
 #include "dn_internal.h"
 #include "dn_linear_api.h"
+#include "dn_tree.h"
 
 namespace {
 
@@ -840,6 +841,120 @@ dn_status dn_linear_recurrent_fwd(const dn_shape* shape, const void* q, const vo
                           {"state", state, ns, true},
                           {"o", o, nv, true}}));
     const hipError_t e = dn::launch_linear_recurrent(pr, q, k, v, g, state, o, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return DN_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+dn_status tree_shape(const dn_shape* s, dn::TreeArgs* a, Dims* d) {
+    if (!s) return fail(DN_ERR_INVALID, "shape is NULL");
+    if (s->B < 0 || s->H < 0 || s->T < 0) return fail(DN_ERR_SHAPE, "B, H, T must be >= 0");
+    if (s->dtype != DN_F32 && s->dtype != DN_BF16) return fail(DN_ERR_DTYPE, "unknown dtype %d", s->dtype);
+    if (s->gate < DN_GATE_NONE || s->gate > DN_GATE_HEAD) return fail(DN_ERR_INVALID, "unknown gate %d", s->gate);
+    DN_TRY(check_flags(s));
+    if (s->T > dn::kTreeMax) return fail(DN_ERR_UNSUPPORTED, "a tree has at most %d nodes", dn::kTreeMax);
+    if (s->dk != 16 && s->dk != 32 && s->dk != 64 && s->dk != 128)
+        return fail(DN_ERR_UNSUPPORTED, "dk must be 16, 32, 64 or 128");
+    if (s->dv <= 0 || s->dv % 16 != 0) return fail(DN_ERR_UNSUPPORTED, "dv must be a positive multiple of 16");
+    if ((long long)s->B * s->H * ((s->dv + 63) / 64) > 0x7fffffffLL)
+        return fail(DN_ERR_UNSUPPORTED, "B*H*ceil(dv/64) too large");
+    *a = dn::TreeArgs{};
+    a->B = s->B;
+    a->H = s->H;
+    a->N = s->T;
+    a->dk = s->dk;
+    a->dv = s->dv;
+    a->bf16 = s->dtype == DN_BF16;
+    a->gate = s->gate;
+    a->kz = (s->flags & DN_FLAG_KACZMARZ) ? 1 : 0;
+    a->eps = s->eps;
+    *d = Dims{};
+    d->BH = (size_t)s->B * s->H;
+    d->T = (size_t)s->T;
+    d->dk = (size_t)s->dk;
+    d->dv = (size_t)s->dv;
+    d->E = a->bf16 ? 2 : 4;
+    return DN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dn_status dn_tree_fwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* beta,
+                      const float* g, const int32_t* parent, const int32_t* counts, const float* state, void* o,
+                      float* u, void* stream) {
+    g_err[0] = '\0';
+    dn::TreeArgs a;
+    Dims d;
+    DN_TRY(tree_shape(shape, &a, &d));
+    if (a.kz && !beta && d.BH * d.T > 0) return fail(DN_ERR_INVALID, "the Kaczmarz step needs eta in beta");
+    const size_t nk = d.BH * d.T * d.dk * d.E, nv = d.BH * d.T * d.dv * d.E, nb = d.BH * d.T * 4;
+    const size_t ng = d.T ? gate_bytes(shape, d) : 0, ns = d.BH * d.dv * d.dk * 4, np = (size_t)shape->B * d.T * 4;
+    if (shape->gate == DN_GATE_NONE && g) return fail(DN_ERR_INVALID, "g must be NULL without a gate");
+    DN_TRY(need(q, nk, "q"));
+    DN_TRY(need(k, nk, "k"));
+    DN_TRY(need(v, nv, "v"));
+    DN_TRY(need(g, ng, "g"));
+    DN_TRY(need(parent, np, "parent"));
+    DN_TRY(need(state, ns, "state"));
+    DN_TRY(need(o, nv, "o"));
+    DN_TRY(check_buffers({{"q", q, nk, false},
+                          {"k", k, nk, false},
+                          {"v", v, nv, false},
+                          {"beta", beta, nb, false},
+                          {"g", g, ng, false},
+                          {"parent", parent, np, false},
+                          {"counts", counts, (size_t)shape->B * 4, false},
+                          {"state", state, ns, false},
+                          {"o", o, nv, true},
+                          {"u", u, d.BH * d.T * d.dv * 4, true}}));
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.beta = beta;
+    a.g = g;
+    a.parent = parent;
+    a.counts = counts;
+    a.state = const_cast<float*>(state);
+    a.o = o;
+    a.u = u;
+    const hipError_t e = dn::launch_tree_fwd(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return DN_OK;
+}
+
+dn_status dn_tree_commit(const dn_shape* shape, const void* k, const float* u, const float* g, const int32_t* parent,
+                         const int32_t* accept, float* state, void* stream) {
+    g_err[0] = '\0';
+    dn::TreeArgs a;
+    Dims d;
+    DN_TRY(tree_shape(shape, &a, &d));
+    const size_t nk = d.BH * d.T * d.dk * d.E, nu = d.BH * d.T * d.dv * 4, np = (size_t)shape->B * d.T * 4;
+    const size_t ng = d.T ? gate_bytes(shape, d) : 0, ns = d.BH * d.dv * d.dk * 4, na = (size_t)shape->B * 4;
+    if (shape->gate == DN_GATE_NONE && g) return fail(DN_ERR_INVALID, "g must be NULL without a gate");
+    DN_TRY(need(k, nk, "k"));
+    DN_TRY(need(u, nu, "u"));
+    DN_TRY(need(g, ng, "g"));
+    DN_TRY(need(parent, np, "parent"));
+    DN_TRY(need(accept, na, "accept"));
+    DN_TRY(need(state, ns, "state"));
+    DN_TRY(check_buffers({{"k", k, nk, false},
+                          {"u", u, nu, false},
+                          {"g", g, ng, false},
+                          {"parent", parent, np, false},
+                          {"accept", accept, na, false},
+                          {"state", state, ns, true}}));
+    a.k = k;
+    a.u = const_cast<float*>(u);
+    a.g = g;
+    a.parent = parent;
+    a.accept = accept;
+    a.state = state;
+    const hipError_t e = dn::launch_tree_commit(a, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
     return DN_OK;
 }

@@ -1,0 +1,348 @@
+// dn_tree_kernels.h -- the nodes of a tree of drafted tokens read from one state.
+//
+// Node n hangs on parent p(n) < n or on the root, whose state S is the sequence's.
+// With Gam_n the log-decays summed along the path to n and "anc" the nodes on that path
+// before n, the states of all nodes unroll to
+//     u_n = beta_n (v_n - S e^{Gam_n} k_n - sum_{m anc n} u_m (k_m . e^{Gam_n - Gam_m} k_n))
+//     o_n = S e^{Gam_n} q_n + sum_{m anc n or m = n} u_m (k_m . e^{Gam_n - Gam_m} q_n)
+// (linear attention: u_n = v_n): one triangular system whose mask is the tree's, so the
+// state is read once whatever the number of branches, and never copied.
+//
+// A workgroup takes one (b, h) and a block of state rows (16 a wave).  Everything is held
+// and multiplied in fp32 (fp32 matrix-core steps, operands straight from the state's own
+// rows): u is an fp32 output from which states are continued, and at 16 nodes the
+// products take under half of the time that reading the states takes.  A wave keeps its
+// columns of u in accumulators from the first product to the last: accumulator row
+// 4 g + i is K slot g of step i of the next product, so the chain X -> R -> u -> o needs
+// no LDS besides the node-by-node matrices.  The system is solved by 16-node blocks, the
+// diagonal ones inverted by substitution, one lane a column.
+#pragma once
+
+#include "dn.h"
+#include "dn_device.h"
+#include "dn_tree.h"
+
+namespace dn {
+
+__device__ __forceinline__ f32x4 tree_mma(f32x4 a, f32x4 b, f32x4 c) {   // K over 4 g + i
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+    return c;
+}
+
+// Gates below -1000 are a factor of zero whatever follows, and their sums stay finite.
+__device__ __forceinline__ float tree_clamp(float g) { return g < -1000.f ? -1000.f : g; }
+
+// Lane n: the node's parent (-1: the root; an index that is no earlier node counts as the
+// root), by the first n nodes of the tree.
+__device__ __forceinline__ int tree_parent(const int* parent, int count, int n) {
+    const int p = n < count ? parent[n] : -1;
+    return p >= 0 && p < n ? p : -1;
+}
+// Lane n of a whole wave: the nodes on its path (itself included) as bits, and x summed
+// along it, by pointer doubling.
+__device__ __forceinline__ unsigned long long tree_path(int p, int n, double& x) {
+    unsigned long long on = 1ull << n;
+#pragma unroll
+    for (int r = 0; r < 6; ++r) {
+        const int from = p < 0 ? n : p;
+        const unsigned long long o = __shfl(on, from);
+        const double y = __shfl(x, from);
+        const int pp = __shfl(p, from);
+        if (p >= 0) {
+            on |= o;
+            x += y;
+            p = pp;
+        }
+    }
+    return on;
+}
+
+template <int DK, int NP, bool VEC> struct TreeLds {
+    static constexpr int LD = DK + 4, LN = NP + 4;
+    float kx[NP][LD], qx[NP][LD];        // k, q; per channel gate: times e^{Gam}
+    float km[VEC ? NP : 1][VEC ? LD : 1];   // k e^{-Gam}, or the gates where that would overflow
+    float A[NP][LN], P[NP][LN];          // the system's matrix (its diagonal blocks inverted in place), the outputs'
+    unsigned long long on[NP];
+    double gam[NP];                      // Gam of a gate per step or head
+    float beta[NP];
+    int parent[NP];
+    float low[8];                        // the lowest Gam of any channel, by wave
+};
+
+template <typename T, int DK, int NP, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW) void tree_kernel(TreeArgs a) {
+    using L = TreeLds<DK, NP, VEC>;
+    constexpr int TH = 64 * NW, NT = NP / 16, F = DK / 16, Q = DK / 4;
+    __shared__ __align__(16) L s;
+    const int nblk = (a.dv / 16 + NW - 1) / NW;
+    const int BH = a.B * a.H;
+    int bh, blk;   // blocks of a head: ids equal mod 8 (one XCD, whose L2 holds its rows)
+    head_and_block(nblk, BH, bh, blk);
+    const int b = bh / a.H, h = bh % a.H, N = a.N;
+    const int tid = threadIdx.x, l = lane_id(), g = l >> 4, m = l & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int cnt = a.counts ? a.counts[b] : N;
+    cnt = __builtin_amdgcn_readfirstlane(cnt < 0 ? 0 : cnt > N ? N : cnt);
+    const bool delta = a.beta != nullptr;
+    const int tile = blk * NW + wave;
+    const bool active = 16 * tile < a.dv;
+    const long rows = (long)bh * N;
+
+    // ---- the state's rows of this wave, in the order its products take them
+    f32x4 S[F];
+    const int vrow = 16 * tile + m;
+#pragma unroll
+    for (int f = 0; f < F; ++f)
+        S[f] = active ? *reinterpret_cast<const f32x4*>(a.state + ((long)bh * a.dv + vrow) * DK + 16 * f + 4 * g) : zero4();
+    float vin[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = 16 * t + 4 * g + i;
+            vin[t][i] = active && n < cnt ? to_f(static_cast<const T*>(a.v)[(rows + n) * a.dv + vrow]) : 0.f;
+        }
+
+    // ---- the tree: paths and their decays
+    if (wave == 0) {
+        const int p = l < NP ? tree_parent(a.parent + (long)b * N, cnt, l) : -1;
+        double x = 0.0;
+        if (l < cnt && a.gate == DN_GATE_SCALAR) x = tree_clamp(a.g[rows + l]);
+        if (l < cnt && a.gate == DN_GATE_HEAD) x = tree_clamp(a.g[h]);
+        const unsigned long long on = tree_path(p, l, x);
+        if (l < NP) {
+            s.on[l] = on;
+            s.gam[l] = x;
+            s.parent[l] = p;
+        }
+    }
+    if constexpr (VEC) {
+        for (int id = tid; id < NP * Q; id += TH) {
+            const int n = id / Q, c = 4 * (id % Q);
+            f32x4 x = zero4();
+            if (n < cnt) x = *reinterpret_cast<const f32x4*>(a.g + (rows + n) * DK + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s.km[n][c + i] = tree_clamp(x[i]);
+        }
+        __syncthreads();
+        // path sums of a channel, a thread each; parents come before their children
+        float low = 0.f;
+        for (int c = tid; c < DK; c += TH)
+            for (int n = 0; n < cnt; ++n) {
+                const int p = s.parent[n];
+                const float x = s.km[n][c] + (p >= 0 ? s.qx[p][c] : 0.f);
+                s.qx[n][c] = x;
+                low = fminf(low, x);
+            }
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) low = fminf(low, __shfl_xor(low, d));
+        if (l == 0) s.low[wave] = low;
+        __syncthreads();
+    }
+    // e^{-Gam} is finite down to -87: below, the pairs' decays are formed one by one
+    bool deep = false;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int u = 0; u < NW; ++u) deep |= s.low[u] < -80.f;
+    }
+
+    // ---- keys and queries, four channels a thread; the keys' square norms for Kaczmarz steps
+    for (int id = tid; id < NP * Q; id += TH) {
+        const int n = id / Q, c = 4 * (id % Q);
+        f32x4 kk = zero4(), qq = zero4();
+        if (n < cnt) {
+            kk = ld4<T>(static_cast<const T*>(a.k) + (rows + n) * DK + c);
+            qq = ld4<T>(static_cast<const T*>(a.q) + (rows + n) * DK + c);
+        }
+        const float norm = group_sum<Q>(kk[0] * kk[0] + kk[1] * kk[1] + kk[2] * kk[2] + kk[3] * kk[3]);
+        if (c == 0) {
+            float bt = delta && n < cnt ? a.beta[rows + n] : 0.f;
+            if (a.kz && n < cnt) bt /= norm + a.eps;
+            s.beta[n] = bt;
+        }
+        if constexpr (VEC) {
+            f32x4 e = zero4(), r = zero4();
+            if (n < cnt) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = s.qx[n][c + i];
+                    e[i] = expf(x);
+                    r[i] = deep ? s.km[n][c + i] : kk[i] * expf(-x);
+                }
+            }
+            *reinterpret_cast<f32x4*>(&s.km[n][c]) = r;
+            kk = kk * e;
+            qq = qq * e;
+        }
+        *reinterpret_cast<f32x4*>(&s.kx[n][c]) = kk;
+        *reinterpret_cast<f32x4*>(&s.qx[n][c]) = qq;
+    }
+    __syncthreads();
+
+    // ---- S k_n and S q_n of every node, rows n, columns the wave's state rows
+    f32x4 X[NT], o[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) X[t] = zero4(), o[t] = zero4();
+    if (active) {
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                o[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.qx[16 * t + m][16 * f + 4 * g]), S[f], o[t]);
+                if (delta) X[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.kx[16 * t + m][16 * f + 4 * g]), S[f], X[t]);
+            }
+        }
+    }
+
+    // ---- node by node: A = beta (k_n . e^{..} k_m) for m before n on its path, P with q_n, m = n too
+    constexpr int TRI = NT * (NT + 1) / 2;
+    if (!deep) {
+        for (int id = wave; id < 2 * TRI; id += NW) {
+            const bool isP = id < TRI;
+            if (!isP && !delta) break;
+            int tn = 0, tm = isP ? id : id - TRI;
+            while (tm > tn) tm -= ++tn;
+            f32x4 acc = zero4();
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const float* nr = isP ? &s.qx[16 * tn + m][0] : &s.kx[16 * tn + m][0];
+                const float* mr = VEC ? &s.km[16 * tm + m][0] : &s.kx[16 * tm + m][0];
+                acc = tree_mma(*reinterpret_cast<const f32x4*>(nr + 16 * f + 4 * g),
+                               *reinterpret_cast<const f32x4*>(mr + 16 * f + 4 * g), acc);
+            }
+            const int mm = 16 * tm + m;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = 16 * tn + 4 * g + i;
+                const bool on = (s.on[n] >> mm & 1) && (isP || mm != n);
+                float w = 1.f;
+                if (!VEC) w = __builtin_amdgcn_exp2f((float)((s.gam[n] - s.gam[mm]) * 1.4426950408889634));
+                const float x = on ? acc[i] * w : 0.f;
+                if (isP) s.P[n][mm] = x;
+                else s.A[n][mm] = x * s.beta[n];
+            }
+        }
+    } else if constexpr (VEC) {
+        // Up each node's path with the decay of the nodes passed, a wave a node.
+        for (int id = tid; id < NP * NP; id += TH) s.A[id / NP][id % NP] = 0.f, s.P[id / NP][id % NP] = 0.f;
+        __syncthreads();
+        constexpr int C = (DK + 63) / 64;
+        for (int n = wave; n < cnt; n += NW) {
+            float kn[C], qn[C], w[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const bool in = l + 64 * c < DK;
+                const long at = (rows + n) * DK + (in ? l + 64 * c : 0);
+                kn[c] = in ? to_f(static_cast<const T*>(a.k)[at]) : 0.f;
+                qn[c] = in ? to_f(static_cast<const T*>(a.q)[at]) : 0.f;
+                w[c] = 0.f;
+            }
+            const float bn = s.beta[n];
+            for (int mm = n; mm >= 0; mm = s.parent[mm]) {
+                float pk = 0.f, pq = 0.f;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int ch = l + 64 * c < DK ? l + 64 * c : 0;
+                    const float x = to_f(static_cast<const T*>(a.k)[(rows + mm) * DK + ch]) * expf(w[c]);
+                    pk += x * kn[c];
+                    pq += x * qn[c];
+                    w[c] += s.km[mm][ch];
+                }
+#pragma unroll
+                for (int d = 1; d < 64; d *= 2) pk += __shfl_xor(pk, d), pq += __shfl_xor(pq, d);
+                if (l == 0) {
+                    s.P[n][mm] = pq;
+                    if (mm != n && delta) s.A[n][mm] = bn * pk;
+                }
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- diagonal blocks of I + A inverted in place: lane j a column, by substitution
+    if (delta) {
+        if (tid < NP) {
+            const int r0 = tid & ~15, j = tid & 15;
+            float t[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float x = i == j ? 1.f : 0.f;
+#pragma unroll
+                for (int q = 0; q < i; ++q) x -= s.A[r0 + i][r0 + q] * t[q];
+                t[i] = x;
+            }
+            __builtin_amdgcn_wave_barrier();   // every lane of the block has read it
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s.A[r0 + i][r0 + j] = t[i];
+        }
+        __syncthreads();
+    }
+    if (!active) return;
+
+    // ---- R = beta (v - S e^{Gam} k), u block by block, then the outputs
+    f32x4 u[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        f32x4 eg, r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = 16 * t + 4 * g + i;
+            eg[i] = VEC ? 1.f : __builtin_amdgcn_exp2f((float)(s.gam[n] * 1.4426950408889634));
+            r[i] = delta ? s.beta[n] * (vin[t][i] - eg[i] * X[t][i]) : vin[t][i];
+        }
+        o[t] = o[t] * eg;
+        if (delta) {
+            f32x4 sub = zero4();
+#pragma unroll
+            for (int q = 0; q < t; ++q) sub = tree_mma(*reinterpret_cast<const f32x4*>(&s.A[16 * t + m][16 * q + 4 * g]), u[q], sub);
+            r = r - sub;
+            u[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.A[16 * t + m][16 * t + 4 * g]), r, zero4());
+        } else {
+            u[t] = r;
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int q = 0; q <= t; ++q) o[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.P[16 * t + m][16 * q + 4 * g]), u[q], o[t]);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = 16 * t + 4 * g + i;
+            if (n >= N) continue;
+            const long at = (rows + n) * a.dv + vrow;
+            static_cast<T*>(a.o)[at] = from_f<T>(n < cnt ? o[t][i] : 0.f);
+            if (a.u) a.u[at] = n < cnt ? u[t][i] : 0.f;
+        }
+}
+
+template <typename T, int DK, int NP, int NW> hipError_t tree_launch_np(const TreeArgs& a, hipStream_t s) {
+    const int nblk = (a.dv / 16 + NW - 1) / NW;
+    const dim3 grid((unsigned)((long)a.B * a.H * nblk)), block(64 * NW);
+    if (a.gate == DN_GATE_VECTOR)
+        hipLaunchKernelGGL((tree_kernel<T, DK, NP, NW, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((tree_kernel<T, DK, NP, NW, false>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+// 64 nodes: eight waves share the node-by-node products, which then weigh as much as the state's.
+template <typename T, int DK> hipError_t tree_launch_dk(const TreeArgs& a, hipStream_t s) {
+    if (a.N <= 16) return tree_launch_np<T, DK, 16, 4>(a, s);
+    if (a.N <= 32) return tree_launch_np<T, DK, 32, 4>(a, s);
+    return tree_launch_np<T, DK, 64, 8>(a, s);
+}
+
+template <typename T> hipError_t tree_launch(const TreeArgs& a, hipStream_t s) {
+    switch (a.dk) {
+        case 16: return tree_launch_dk<T, 16>(a, s);
+        case 32: return tree_launch_dk<T, 32>(a, s);
+        case 64: return tree_launch_dk<T, 64>(a, s);
+        case 128: return tree_launch_dk<T, 128>(a, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace dn

@@ -352,6 +352,37 @@ dn_status dn_linear_bwd(const dn_shape* shape, const void* q, const void* k, con
 dn_status dn_linear_recurrent_fwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* g,
                                   float* state, void* o, void* stream);
 
+/*
+ * A tree of drafted tokens (speculative decoding) on the recurrent state: the reading of
+ * every node as if the tokens on its path from the root had been decoded one after the
+ * other from `state` (the recurrence of dn_recurrent_fwd, or of dn_linear_recurrent_fwd
+ * when beta is NULL), without a copy of the state for each branch.  Node n hangs on node
+ * parent[b][n], an earlier node of the same batch element, or on the root (any value that
+ * is no earlier node, e.g. -1); a chain is parent[n] = n - 1.
+ *   dn_tree_fwd    reads the nodes: o, and u, what each node writes into the state
+ *                  (u_n k_n^T; for linear attention u_n = v_n).  The state is not changed.
+ *   dn_tree_commit moves `state` along the path that ends at node accept[b] (in place),
+ *                  from the u of dn_tree_fwd; any accept[b] outside 0 .. T - 1 (e.g. -1)
+ *                  leaves that batch element's states as they are, unread.
+ *   shape  : T = nodes per batch element, 0 .. 64; dk in {16, 32, 64, 128}; dv a positive
+ *            multiple of 16; dtype (q, k, v, o); gate: any dn_gate (g [B][H][T],
+ *            [B][H][T][dk] or [H]); flags: DN_FLAG_KACZMARZ (dn_tree_fwd with beta, which
+ *            then carries eta; dn_tree_commit ignores it), DN_FLAG_NO_SCAN is ignored; C
+ *            unused.  B*H*ceil(dv/64) <= 2^31 - 1
+ *   inputs : q, k, v, beta (NULL: linear attention), g (NULL iff no gate) as for
+ *            dn_recurrent_fwd, the nodes in the place of the steps; parent int32 [B][T];
+ *            counts int32 [B] or NULL: the nodes of each batch element (clamped to
+ *            0 .. T), o and u are zero from there on; accept int32 [B]; state fp32
+ *            [B][H][dv][dk].  Gates below -1000 act as -1000 (a factor of zero).
+ *   outputs: o (io) and u fp32, both [B][H][T][dv] (u NULL = not wanted); fp32 arithmetic
+ * Validation and errors as for dn_recurrent_fwd; no workspace.
+ */
+dn_status dn_tree_fwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* beta,
+                      const float* g, const int32_t* parent, const int32_t* counts, const float* state, void* o,
+                      float* u, void* stream);
+dn_status dn_tree_commit(const dn_shape* shape, const void* k, const float* u, const float* g, const int32_t* parent,
+                         const int32_t* accept, float* state, void* stream);
+
 /* Static description of a status code. */
 const char* dn_status_string(dn_status status);
 
