@@ -32,13 +32,10 @@ struct LinOp {
     long snap_bh;        // floats of one (b, h) there
     int sn, sk;          // strides of state element (z channel, y channel) in init, fin, snap
     int rev;
-    // Gate gradient (role 0: none): r is laid out like z, one row for each output row.
-    //   role 1: dots[blk][BH][T] = r_i . (out_i's part from earlier chunks)
-    //   role 2: with E_ji = w_ij (x_i . y_j) (r_i . z_j) over the chunk's pairs,
-    //           dots_i = sum_j E_ij - sum_j E_ji - r_i . (out_i's part from later steps)
+    // Gate gradient: rows r laid out like z; dots[2][blk][BH][T] = r_i . out_i, over the block's
+    // channels and before its rounding: the part from earlier chunks, then from all steps before
     const void* r;
     float* dots;
-    int role;
 };
 
 // State entries: forward, entry e = the state before chunk e * snap; rev, entry e = the
@@ -74,12 +71,21 @@ __device__ __forceinline__ int lin_len(const int* lens, int b, int T) {
 }
 
 enum LinMode { kLinState = 0, kLinOut = 1, kLinDots = 2 };
+// Output tiles (16 channels) whose 16-byte pieces a lane stores at once.
+__host__ __device__ constexpr int lin_pair(bool bf16, int nv) { return bf16 && nv > 1 ? 2 : 1; }
+// The gate's gradient leaves room for one workgroup on a compute unit (three parts of the
+// state in LDS): eight waves form its outputs, each half of the channels, so that matrix,
+// vector and LDS work of more waves overlap.
+__host__ __device__ constexpr int lin_halves(int mode, bool bf16, int nv) {
+    return mode == kLinDots && nv / lin_pair(bf16, nv) > 1 ? 2 : 1;
+}
+// Four waves carry the state; four for each share of the channels form the outputs.
+__host__ __device__ constexpr int lin_threads(int mode, bool bf16, int nv) {
+    return mode == kLinState ? 256 : 256 + 256 * lin_halves(mode, bf16, nv);
+}
 // Waves a SIMD holds at once: the registers of fp32 rows and of the gate's gradient leave
-// room for two (the latter in 128 registers spills 70 and takes 825 us where 256 take 660
-// at 8 x 16 heads, 4096 steps).
+// room for few.
 __host__ __device__ constexpr int lin_waves(int mode, bool bf16) { return mode == kLinOut && bf16 ? 4 : 2; }
-// Four waves carry the state; four more form the outputs.
-__host__ __device__ constexpr int lin_threads(int mode) { return mode == kLinState ? 256 : 512; }
 typedef hipError_t (*LinLaunch)(const LinArgs& a, int nv, int mode, hipStream_t s);
 hipError_t lin_bf16_k32(const LinArgs&, int, int, hipStream_t);
 hipError_t lin_bf16_k64(const LinArgs&, int, int, hipStream_t);

@@ -10,6 +10,8 @@ namespace dn {
 
 namespace {
 
+constexpr int kLinMaxSeg = 64;   // parallel segments of a sequence
+
 // Boundary states of the parallel segments: entry s of snap holds segment s's own
 // contribution (from a zero state) and gets the state the segment starts from,
 //     start_{s+1} = dec_s start_s + end_s,
@@ -24,7 +26,9 @@ __global__ __launch_bounds__(256) void lin_join_kernel(LinArgs a) {
     const LinOp& op = a.op[oi];
     const long se = (long)a.kd * a.nd;
     float* base = op.snap + bh * op.snap_bh + 4 * at;
-    const float* dec = a.segdec + ((long)oi * a.BH + bh) * a.nseg;
+    // one factor a lane: loaded once, not waited for at every entry
+    static_assert(kLinMaxSeg <= 64, "a factor of each segment in a lane");
+    const float dec = a.segdec[((long)oi * a.BH + bh) * a.nseg + min(lane_id(), a.nseg - 1)];
     f32x4 cur = op.init ? *reinterpret_cast<const f32x4*>(op.init + bh * se + 4 * at) : zero4();
     auto slot = [&](int i) {   // i-th segment walked -> its entry
         const int s = op.rev ? a.nseg - 1 - i : i;
@@ -40,18 +44,20 @@ __global__ __launch_bounds__(256) void lin_join_kernel(LinArgs a) {
         for (int i = 0; i < AHEAD; ++i) {
             if (i0 + i >= a.nseg) break;
             *slot(i0 + i) = cur;   // the last segment's own part is nowhere formed, nor used
-            if (i0 + i + 1 < a.nseg) cur = cur * dec[op.rev ? a.nseg - 1 - (i0 + i) : i0 + i] + own[i];
+            if (i0 + i + 1 < a.nseg) cur = cur * __shfl(dec, op.rev ? a.nseg - 1 - (i0 + i) : i0 + i) + own[i];
         }
     }
 }
 
 // Gate gradient of the steps t0 .. t1 - 1 that one kept state covers:
 //     dg_t = B1 + sum_{t <= s < t1} (a_s - b_s),   B(t) = dg_t = e^{g_t} <S_{t - 1}, D_t>
-// (the pairs that straddle t), a_s - b_s summed over the channel blocks of the two
-// evaluations that wrote them.  Both ends are known from the kept states, so that the
-// rounding of the differences adds up over one stretch only, and what it adds up to
-// there, B0 less the sum's own value at t0, is taken off evenly along the stretch
-// (1.3e-6 -> 0.7e-6 of the gradient's norm at 4096 steps).  Sums in 64 bits.
+// (the pairs that straddle t), a_s = q_s . dq_s and b_s = v_s . dv_s (= k_s . dk_s),
+// summed over the channel blocks that wrote them, the pair of a step with itself left
+// out.  The rounding of the differences would add up over the sequence (gradients of
+// 4096 steps were off by 1e-5 of their norm).  Three things hold it down: both ends of
+// a stretch are known from the kept states, and what the sum misses at t0 is taken off
+// evenly along it; the pairs inside a chunk sum to zero over it, and what they sum to
+// is taken off evenly along the chunk.  Sums in 64 bits.  A thread owns four steps.
 __device__ __forceinline__ double block_sum(double x, double* part) {
     part[threadIdx.x] = x;
     __syncthreads();
@@ -93,16 +99,34 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* 
                                last ? n : t1);
     // the first step's gate decays h0, and nothing without one
     const double B0 = straddle(e > 0 ? sk + e * se : h0 ? h0 + bh * se : nullptr, dk + (e > 0 ? e - 1 : a.nent) * se, t0);
-    // each thread: a run of consecutive steps, then the sums of the runs after it
-    const int per = (t1 - t0 + 255) / 256, ta = t0 + tid * per, tb = min(ta + per, t1);
-    auto term = [&](int t) {
-        double d = 0.0;
-        for (int i = 0; i < n1; ++i) d += dots1[((long)i * a.BH + bh) * a.T + t];
-        for (int i = 0; i < n2; ++i) d += dots2[((long)i * a.BH + bh) * a.T + t];
-        return d;
-    };
+    const long nt = (long)a.BH * a.T;
+    const int ta = t0 + 4 * tid, tb = min(ta + 4, t1);
+    double inter[4], pairs[4], off = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        inter[i] = pairs[i] = 0.0;
+        if (ta + i >= tb) continue;
+        for (int b = 0; b < n1; ++b) {
+            const float* d = dots1 + b * nt + row + ta + i;
+            inter[i] += d[0];
+            pairs[i] += (double)d[n1 * nt] - d[0];
+        }
+        for (int b = 0; b < n2; ++b) {
+            const float* d = dots2 + b * nt + row + ta + i;
+            inter[i] -= d[0];
+            pairs[i] -= (double)d[n2 * nt] - d[0];
+        }
+        off += pairs[i];
+    }
+#pragma unroll
+    for (int d = 1; d < kLinC / 4; d *= 2) off += __shfl_xor(off, d);   // the 16 threads of a chunk
+    const int c0 = t0 + (tid / (kLinC / 4)) * kLinC, live = min(c0 + kLinC, t1) - c0;
     double own = 0.0;
-    for (int t = ta; t < tb; ++t) own += term(t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (ta + i < tb) inter[i] += pairs[i] - off / live;
+        own += inter[i];
+    }
     part[tid] = own;
     __syncthreads();
     for (int d = 1; d < 256; d *= 2) {   // suffix sums
@@ -113,8 +137,11 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* 
     }
     const double slope = (B0 - (B1 + part[0])) / (t1 - t0);
     double acc = B1 + (tid < 255 ? part[tid + 1] : 0.0);
-    for (int t = tb - 1; t >= ta; --t) {
-        acc += term(t);
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+        const int t = ta + i;
+        if (t >= tb) continue;
+        acc += inter[i];
         dg[row + t] = t == t0 ? (float)B0 : (float)(acc + slope * (t1 - t));
     }
     for (int t = t1 + tid; t < tend; t += 256) dg[row + t] = 0.f;
@@ -200,10 +227,10 @@ int blocks_of(int nd, int bf16) { return nd / lin_vb(nd, bf16 != 0); }
 LinPlan lin_plan(const LinProblem& pr, int nops, bool dots) {
     const int NT = ceil_div(pr.T, kLinC);
     const long wgs = (long)pr.B * pr.H * blocks_of(pr.dv, pr.bf16) * nops;
-    constexpr long kWant = 512, kMinLen = 4, kMaxSeg = 64;   // two workgroups on each compute unit
+    constexpr long kWant = 1024, kFull = 256, kMinLen = 4;
     long ns = wgs > 0 ? kWant / wgs : 1;
-    if (pr.no_scan || 2 * wgs >= kWant) ns = 1;
-    if (ns > kMaxSeg) ns = kMaxSeg;
+    if (pr.no_scan || wgs >= kFull) ns = 1;
+    if (ns > kLinMaxSeg) ns = kLinMaxSeg;
     if (ns > NT / kMinLen) ns = NT / kMinLen;
     if (ns < 1) ns = 1;
     LinPlan p;
@@ -274,9 +301,9 @@ LinWs lin_ws(const LinProblem& pr, int pass) {
     w.segdec = off;
     off += p.nseg > 1 ? al256((bwd ? 2 : 1) * BH * p.nseg * 4) : 0;
     w.dots1 = off;
-    off += dots ? al256((size_t)blocks_of(pr.dk, pr.bf16) * BH * pr.T * 4) : 0;
+    off += dots ? al256(2 * (size_t)blocks_of(pr.dk, pr.bf16) * BH * pr.T * 4) : 0;
     w.dots2 = off;
-    off += dots ? al256((size_t)blocks_of(pr.dv, pr.bf16) * BH * pr.T * 4) : 0;
+    off += dots ? al256(2 * (size_t)blocks_of(pr.dv, pr.bf16) * BH * pr.T * 4) : 0;
     w.total = off;
     return w;
 }
@@ -344,8 +371,8 @@ hipError_t launch_linear_bwd(const LinProblem& pr, const LinBwd& f, char* ws, hi
         if ((e = launch_boundaries(pr, a, s)) != hipSuccess) return e;
     }
     if (dots) {
-        dq.r = f.q, dq.role = 1, dq.dots = reinterpret_cast<float*>(ws + w.dots1);
-        dv.r = f.v, dv.role = 2, dv.dots = reinterpret_cast<float*>(ws + w.dots2);
+        dq.r = f.q, dq.dots = reinterpret_cast<float*>(ws + w.dots1);
+        dv.r = f.v, dv.dots = reinterpret_cast<float*>(ws + w.dots2);
     }
     // evaluations of the same widths and mode share a launch (and their rows in L2)
     auto run = [&](const LinOp* ops, int n, int kd, int nd, int mode) {

@@ -104,7 +104,8 @@ template <typename T, int KD, int NV, int MODE> struct LinLds {
     // R: G from the first step of the row's 16 (two floats); e^{G_63 - G};
     // e^{G_16w - G_j} of the rows j before 16 w, w = 1, 2, 3; e^{G_16w}; the chunk's factor
     float hi[kLinC], lo[kLinC], ew[kLinC], tab[3][kLinC], eref[4], etot;
-    float rowe[DG ? 4 : 1][DG ? kLinC : 1], colb[DG ? kLinC : 1];
+    static constexpr int HV = lin_halves(MODE, sizeof(T) == 2, NV);
+    float dot[2][HV][HV > 1 ? kLinC : 1];
 };
 
 // Gate that the state takes when step t is entered: the step's own, or with rev that of
@@ -122,13 +123,14 @@ __device__ __forceinline__ double lin_log2(float g, int n, int t, int rev) {
 }
 
 template <typename T, int KD, int NV, int MODE>
-__global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2)) void lin_kernel(LinArgs a) {
+__global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MODE, sizeof(T) == 2)) void lin_kernel(LinArgs a) {
     constexpr bool OUT = MODE != kLinState, DG = MODE == kLinDots;
-    constexpr int TH = lin_threads(MODE);
+    constexpr int TH = lin_threads(MODE, sizeof(T) == 2, NV), HV = lin_halves(MODE, sizeof(T) == 2, NV);
     using X = LinT<T>;
     using Frag = typename X::Frag;
     using L = LinLds<T, KD, NV, MODE>;
     constexpr int E = X::E, JS = X::JS, VB = 16 * NV, LY = L::LY, LZ = L::LZ, LS = L::LS, NS = L::NS;
+    constexpr int NVW = NV / HV;                             // output tiles of a wave
     constexpr int XF = KD / (4 * E);                         // fragments of an x row
     constexpr int WV = 4 / NV;                               // waves that share a state tile column
     constexpr int CT = KD / 16 / WV > 0 ? KD / 16 / WV : 1;  // state tiles of a wave
@@ -137,7 +139,7 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
     __shared__ __align__(16) L s;
     // z channel of accumulator element i of lane group q in output tile `tile`: a lane's
     // elements of TP tiles are 16 bytes of a row, and the four groups' follow each other
-    constexpr int TP = sizeof(T) == 2 && NV > 1 ? 2 : 1;
+    constexpr int TP = lin_pair(sizeof(T) == 2, NV);
     auto out_col = [](int tile, int q, int i) { return 16 * TP * (tile / TP) + 4 * TP * q + 4 * (tile % TP) + i; };
 
     // Workgroups go to the 8 XCDs in turn: the blocks and evaluations of one (b, h) and
@@ -152,7 +154,8 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
     const int rev = op.rev;
     if (!OUT && (rev ? seg == 0 : seg == a.nseg - 1)) return;   // nothing starts from its end
 
-    // waves 0 .. 3 form the outputs (16 steps each), the others the state
+    // waves 0 .. 4 HV - 1 form the outputs (16 steps each, HV shares of the channels), the
+    // others the state
     const int tid = threadIdx.x, l = lane_id(), g = l >> 4, m = l & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), w = wave & 3;   // uniform: branches on it are scalar
     const int h = bh % a.H, n = __builtin_amdgcn_readfirstlane(lin_len(a.lens, bh / a.H, a.T));
@@ -178,9 +181,11 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
     // registers for one of them only.
     auto run = [&](auto outs) {
         constexpr bool O = decltype(outs)::value;
+        const int half = O ? wave >> 2 : 0, tile0 = half * NVW;   // this wave's output tiles
         // ---- tiles of a chunk: 16-byte pieces, places in bytes from the chunk's first row
         u32x4 yr[NY], zr[NZ];
         Frag xn[O ? XF : 1], x[O ? XF : 1];
+        T rn[O && DG ? 4 * NVW : 1], r[O && DG ? 4 * NVW : 1];
         auto row_at = [&](int row, int width) { return (rev ? kLinC - 1 - row : row) * width * (int)sizeof(T); };
         int yo[NY], zo[NZ];
 #pragma unroll
@@ -209,6 +214,24 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
                     xn[f] = __builtin_bit_cast(
                         Frag, load16(xb, KD > 32 || 4 * E * f + E * g < a.kd ? xo + 64 * f : kNowhere));
             }
+            if constexpr (O && DG) {   // rows of the other factor of the gate's gradient, the lane's output channels
+                const auto rb = lin_range(static_cast<const T*>(op.r) + (rows + row0) * a.nd + blk * VB,
+                                          (min(n - row0, kLinC) * a.nd - blk * VB) * (int)sizeof(T));
+#pragma unroll
+                for (int i = 0; i < NVW; i += TP) {
+                    const int at = row_at(trow, a.nd) + out_col(tile0 + i, g, 0) * (int)sizeof(T);
+                    if constexpr (TP * 4 * sizeof(T) == 16) {
+                        const Frag v = __builtin_bit_cast(Frag, load16(rb, at));
+#pragma unroll
+                        for (int e = 0; e < E; ++e) rn[4 * i + e] = v[e];
+                    } else {
+                        typedef typename Vec4<T>::type V4;
+                        const V4 v = __builtin_bit_cast(V4, __builtin_amdgcn_raw_buffer_load_b64(rb, at, 0, 0));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) rn[4 * i + e] = v[e];
+                    }
+                }
+            }
         };
         auto put_tiles = [&]() {
 #pragma unroll
@@ -226,6 +249,10 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
             if constexpr (O) {
 #pragma unroll
                 for (int f = 0; f < XF; ++f) x[f] = xn[f];
+            }
+            if constexpr (O && DG) {
+#pragma unroll
+                for (int e = 0; e < 4 * NVW; ++e) r[e] = rn[e];
             }
         };
         // ---- running log-decay of a chunk: lane = row, sums in 64 bits.  One wave forms it
@@ -261,11 +288,18 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
                 for (int u = 1; u < 4; ++u) s.tab[u - 1][l] = gtab[u];
             }
         };
-        auto put_dot = [&](int c, int at, float d) {
-            if constexpr (DG) {
-                const auto db = lin_range(op.dots + ((long)blk * a.BH + bh) * a.T + c * kLinC, min(n - c * kLinC, kLinC) * 4);
-                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, d), db, at, 0, 0);
-            }
+        auto put_dot = [&](int which, int c, int at, float d) {
+            const auto db = lin_range(op.dots + (((long)which * a.nblk + blk) * a.BH + bh) * a.T + c * kLinC,
+                                      min(n - c * kLinC, kLinC) * 4);
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, d), db, at, 0, 0);
+        };
+        auto rdot = [&](const auto& acc, const auto& r) {   // over the lane's channels
+            float d = 0.f;
+#pragma unroll
+            for (int i = 0; i < NVW; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d += acc[i][e] * to_f(r[4 * i + e]);
+            return d;
         };
         // ---- state block: element pieces of this lane in global memory and in LDS
         f32x4 S[O ? 1 : CT];
@@ -341,39 +375,18 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
             const float gn = lin_gate(a, gp, n, time_of(next, l), rev);
             load(next);
             if constexpr (O) {
-                f32x4 acc[NV];
+                f32x4 acc[NVW];
                 const int row0 = c * kLinC;
-                // rows of the other factor of the gate's gradient, the lane's output channels
-                T r[DG ? 4 * NV : 1];
-                float dot = 0.f, col = 0.f;
-                if constexpr (DG) {
-                    const auto rb = lin_range(static_cast<const T*>(op.r) + (rows + row0) * a.nd + blk * VB,
-                                              (min(n - row0, kLinC) * a.nd - blk * VB) * (int)sizeof(T));
 #pragma unroll
-                    for (int i = 0; i < NV; i += TP) {
-                        const int at = row_at(trow, a.nd) + out_col(i, g, 0) * (int)sizeof(T);
-                        if constexpr (TP * 4 * sizeof(T) == 16) {
-                            const Frag v = __builtin_bit_cast(Frag, load16(rb, at));
-#pragma unroll
-                            for (int e = 0; e < E; ++e) r[4 * i + e] = v[e];
-                        } else {
-                            typedef typename Vec4<T>::type V4;
-                            const V4 v = __builtin_bit_cast(V4, __builtin_amdgcn_raw_buffer_load_b64(rb, at, 0, 0));
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) r[4 * i + e] = v[e];
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < NV; ++i) acc[i] = zero4();
+                for (int i = 0; i < NVW; ++i) acc[i] = zero4();
                 // ---- from earlier chunks
 #pragma unroll
                 for (int f = 0; f < XF; ++f)
 #pragma unroll
                     for (int p = 0; p < NS; ++p)
 #pragma unroll
-                        for (int i = 0; i < NV; ++i) {   // consecutive steps: different accumulators
-                            const int at = out_col(i, m >> 2, m & 3) * LS + 4 * E * f + E * g;
+                        for (int i = 0; i < NVW; ++i) {   // consecutive steps: different accumulators
+                            const int at = out_col(tile0 + i, m >> 2, m & 3) * LS + 4 * E * f + E * g;
                             acc[i] = X::mma(*reinterpret_cast<const Frag*>(&s.s[p][at]), x[f], acc[i]);
                         }
                 // The factors of a step's row: e^{G_16w} and e^{R}; pairs with the 16-step blocks before
@@ -381,14 +394,9 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
                 // for each pair.
                 const float er = s.eref[w], hi = s.hi[trow], lo = s.lo[trow], es = exp2_hw(hi + lo);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    acc[i] = acc[i] * er;
-                    if constexpr (DG) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) dot += acc[i][e] * to_f(r[4 * i + e]);
-                    }
-                }
-                if constexpr (DG) dot *= es;
+                for (int i = 0; i < NVW; ++i) acc[i] = acc[i] * er;
+                float dot0 = 0.f, dot1 = 0.f, pd = 0.f;   // r . out from earlier chunks, from all steps before; P's diagonal
+                if constexpr (DG) dot0 = rdot(acc, r) * es;
                 // ---- pairs of the chunk
                 constexpr int NP = JS / 16;
                 auto block = [&](int js, auto diagonal) {   // steps JS js .., the last of them w's own
@@ -418,45 +426,18 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
                             for (int i = 0; i < 4; ++i) {
                                 const int j = 16 * jt + 4 * g + i;
                                 const float d = (hi - hj[i]) + (lo - lj[i]);
-                                p[u][i] = pa[u][i] * exp2_hw(j <= trow ? d : -INFINITY);
-                            }
-                        }
-                        if constexpr (DG) {
-                            if (op.role == 2) {   // E = P o (r z^T), summed along both axes
-                                f32x4 q = zero4();
-                                const T* zj = &s.z[(16 * jt + m) * LZ];
-                                if constexpr (4 * NV >= E) {
-#pragma unroll
-                                    for (int f = 0; f < 4 * NV / E; ++f) {
-                                        Frag rb;
-#pragma unroll
-                                        for (int e = 0; e < E; ++e) rb[e] = r[E * f + e];
-                                        q = X::mma(*reinterpret_cast<const Frag*>(zj + 4 * E * f + E * g), rb, q);
-                                    }
-                                } else {   // 16 channels of bf16: half of the K slots are zero
-                                    Frag za, rb;
-                                    const typename Vec4<T>::type v = *reinterpret_cast<const typename Vec4<T>::type*>(zj + 4 * g);
-#pragma unroll
-                                    for (int e = 0; e < E; ++e) {
-                                        za[e] = e < 4 ? (T)v[e & 3] : (T)0.f;
-                                        rb[e] = e < 4 ? r[e & 3] : (T)0.f;
-                                    }
-                                    q = X::mma(za, rb, q);
-                                }
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int j = 16 * jt + 4 * g + i;
-                                    const float e = j == trow ? 0.f : p[u][i] * q[i] * (D ? 1.f : es);   // the diagonal cancels
-                                    col += e;
-                                    const float rs = row16_sum(e);
-                                    if (m == 0) s.rowe[w][j] = rs;
+                                if constexpr (DG) {   // the diagonal apart: it is no part of the gate's gradient
+                                    if (j == trow) pd += pa[u][i];
+                                    p[u][i] = pa[u][i] * exp2_hw(j < trow ? d : -INFINITY);
+                                } else {
+                                    p[u][i] = pa[u][i] * exp2_hw(j <= trow ? d : -INFINITY);
                                 }
                             }
                         }
                     }
-                    constexpr int PP = sizeof(T) == 2 ? 2 : 1;   // parts of P
+                    constexpr int PP = sizeof(T) == 4 ? 1 : DG ? 3 : 2;   // parts of P
                     Frag pf[PP];
-                    if constexpr (PP == 2) {
+                    if constexpr (PP > 1) {
                         u32x4 part[PP];
 #pragma unroll
                         for (int e = 0; e < E; e += 2)
@@ -468,30 +449,51 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
 #pragma unroll
                         for (int e = 0; e < E; ++e) pf[0][e] = from_f<T>(p[0][e]);
                     }
-                    Frag zf[NV];
+                    Frag zf[NVW];
 #pragma unroll
-                    for (int i = 0; i < NV; ++i) {
-                        const int col0 = sizeof(T) == 2 ? out_col(i, m & 3, 0) : out_col(i, m >> 2, m & 3);
+                    for (int i = 0; i < NVW; ++i) {
+                        const int col0 = sizeof(T) == 2 ? out_col(tile0 + i, m & 3, 0) : out_col(tile0 + i, m >> 2, m & 3);
                         zf[i] = X::load_t(s.z, LZ, js * JS, col0);
                     }
 #pragma unroll
                     for (int u = 0; u < PP; ++u)
 #pragma unroll
-                        for (int i = 0; i < NV; ++i) acc[i] = X::mma(zf[i], pf[u], acc[i]);
+                        for (int i = 0; i < NVW; ++i) acc[i] = X::mma(zf[i], pf[u], acc[i]);
                 };
 #pragma unroll
                 for (int js = 0; js < kLinC / JS; ++js) {   // whole blocks before w's own, then the rest
                     if ((js + 1) * NP <= w) block(js, std::false_type{});
                 }
 #pragma unroll
-                for (int i = 0; i < NV; ++i) acc[i] = acc[i] * es;
+                for (int i = 0; i < NVW; ++i) acc[i] = acc[i] * es;
                 block(w / NP, std::true_type{});
+                if constexpr (DG) {
+                    dot1 = rdot(acc, r);
+                    pd = sum_lane_groups(pd);
+#pragma unroll
+                    for (int i = 0; i < NVW; ++i) {
+                        const typename Vec4<T>::type z =
+                            *reinterpret_cast<const typename Vec4<T>::type*>(&s.z[trow * LZ + out_col(tile0 + i, g, 0)]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][e] += pd * to_f(z[e]);
+                    }
+                    dot0 = sum_lane_groups(dot0);
+                    dot1 = sum_lane_groups(dot1);
+                    if constexpr (HV == 1) {
+                        const int at = g == 0 ? row_at(trow, 1) / (int)sizeof(T) * 4 : kNowhere;
+                        put_dot(0, c, at, dot0);
+                        put_dot(1, c, at, dot1);
+                    } else if (g == 0) {
+                        s.dot[0][half][trow] = dot0;
+                        s.dot[1][half][trow] = dot1;
+                    }
+                }
                 // ---- out: 16-byte pieces, 64 consecutive bytes of a step for the four lanes that share it
                 const auto ob = lin_range(static_cast<T*>(op.out) + (rows + row0) * a.nd + blk * VB,
                                           (min(n - row0, kLinC) * a.nd - blk * VB) * (int)sizeof(T));
 #pragma unroll
-                for (int i = 0; i < NV; i += TP) {
-                    const int at = row_at(trow, a.nd) + out_col(i, g, 0) * (int)sizeof(T);
+                for (int i = 0; i < NVW; i += TP) {
+                    const int at = row_at(trow, a.nd) + out_col(tile0 + i, g, 0) * (int)sizeof(T);
                     if constexpr (sizeof(T) == 4) {
                         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i]), ob, at, 0, 0);
                     } else {
@@ -508,11 +510,6 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
                         else
                             __builtin_amdgcn_raw_buffer_store_b64(v[0], ob, at, 0, 0);
                     }
-                }
-                if constexpr (DG) {
-                    dot = sum_lane_groups(op.role == 1 ? dot : dot + col);
-                    put_dot(c, op.role == 1 && g == 0 ? row_at(trow, 1) / (int)sizeof(T) * 4 : kNowhere, dot);
-                    if (g == 0) s.colb[trow] = dot;
                 }
             } else if (owns) {
                 // ---- state
@@ -560,13 +557,8 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
             if (gates) put_gates();
             put_tiles();
             if constexpr (OUT && !O) put_state();
-            if constexpr (DG && O) {
-                if (wave == 0) {
-                    float d = -s.colb[l];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) d += u >= l / 16 ? s.rowe[u][l] : 0.f;
-                    put_dot(c, op.role == 2 ? row_at(l, 1) / (int)sizeof(T) * 4 : kNowhere, d);
-                }
+            if constexpr (DG && O && HV > 1) {   // the halves of a step's dot
+                if (wave < 2) put_dot(wave, c, row_at(l, 1) / (int)sizeof(T) * 4, s.dot[wave][0][l] + s.dot[wave][1][l]);
             }
         }
 
@@ -585,14 +577,14 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
         }
     };
     if constexpr (OUT) {
-        if (wave < 4)
+        if (wave < 4 * HV)
             run(std::true_type{});
         else
             run(std::false_type{});
         // steps past the length
         T* o = static_cast<T*>(op.out) + rows * a.nd + blk * VB;
         const int from = max(c0 * kLinC, n), to = min(a.T, c1 * kLinC);
-        for (int t = from + tid / PZ; t < to; t += TH / PZ)
+        for (int t = from + tid / PZ; tid < TH / PZ * PZ && t < to; t += TH / PZ)
             *reinterpret_cast<uint4*>(o + (long)t * a.nd + (tid % PZ) * E) = make_uint4(0u, 0u, 0u, 0u);
     } else {
         run(std::false_type{});
@@ -601,7 +593,7 @@ __global__ __launch_bounds__(lin_threads(MODE), lin_waves(MODE, sizeof(T) == 2))
 
 template <typename T, int KD, int NV> hipError_t lin_launch_nv(const LinArgs& a, int mode, hipStream_t s) {
     const long units = ((long)a.BH * a.nseg + kXcds - 1) / kXcds * kXcds;
-    const dim3 grid((unsigned)(units * a.nops * a.nblk)), block(lin_threads(mode));
+    const dim3 grid((unsigned)(units * a.nops * a.nblk)), block(lin_threads(mode, sizeof(T) == 2, NV));
     switch (mode) {
         case kLinState: hipLaunchKernelGGL((lin_kernel<T, KD, NV, kLinState>), grid, block, 0, s, a); break;
         case kLinOut: hipLaunchKernelGGL((lin_kernel<T, KD, NV, kLinOut>), grid, block, 0, s, a); break;
