@@ -15,14 +15,14 @@ namespace {
 // on their way.  A sequence that accepts nothing is neither read nor written.
 constexpr int kCommitThreads = 256, kCommitRows = 64;
 
-template <typename T, int DK>
+template <typename T, int DK, int NP>
 __global__ __launch_bounds__(kCommitThreads) void tree_commit_kernel(TreeArgs a) {
     constexpr int E = DK / 16, R = kCommitRows / 16, LU = kCommitRows + 4;
-    __shared__ __align__(16) float kd[kTreeMax][DK];
-    __shared__ __align__(16) float us[kTreeMax][LU];
+    __shared__ __align__(16) float kd[NP][DK];
+    __shared__ __align__(16) float us[NP][LU];
     __shared__ float end[DK];       // e^{Gam_a} of each channel
-    __shared__ float wt[kTreeMax];  // e^{Gam_a - Gam_m} of a gate per step or head
-    __shared__ int path[kTreeMax];  // the path, root first
+    __shared__ float wt[NP];        // e^{Gam_a - Gam_m} of a gate per step or head
+    __shared__ int path[NP];        // the path, root first
     const int nblk = (a.dv + kCommitRows - 1) / kCommitRows;
     int bh, blk;
     head_and_block(nblk, a.B * a.H, bh, blk);
@@ -31,23 +31,23 @@ __global__ __launch_bounds__(kCommitThreads) void tree_commit_kernel(TreeArgs a)
     if (at < 0 || at >= N) return;
     const long rows = (long)bh * N;
 
-    // ---- state rows r = 16 i + tid / 16 of the block
+    // ---- the tree's loads, then state rows r = 16 i + tid / 16 of the block
+    const int p = tree_parent(a.parent + (long)b * N, N, l);
+    double x = 0.0;
+    if (l < N && a.gate == DN_GATE_SCALAR) x = tree_clamp(a.g[rows + l]);
+    if (l < N && a.gate == DN_GATE_HEAD) x = tree_clamp(a.g[h]);
     float s[R][E];
     float* base = a.state + ((long)bh * a.dv + blk * kCommitRows) * DK + j * E;
     const int left = a.dv - blk * kCommitRows;   // rows of the block
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int r = 16 * i + (tid >> 4);
+        const int r = min(16 * i + (tid >> 4), left - 1);
 #pragma unroll
-        for (int e = 0; e < E; ++e) s[i][e] = r < left ? base[(long)r * DK + e] : 0.f;
+        for (int e = 0; e < E; ++e) s[i][e] = base[(long)r * DK + e];
     }
 
     // ---- the path (every wave for itself; wave 0 writes it down)
-    const int p = tree_parent(a.parent + (long)b * N, N, l);
-    double x = 0.0;
-    if (l < N && a.gate == DN_GATE_SCALAR) x = tree_clamp(a.g[rows + l]);
-    if (l < N && a.gate == DN_GATE_HEAD) x = tree_clamp(a.g[h]);
-    const unsigned long long all = tree_path(p, l, x);
+    const unsigned long long all = tree_path<NP>(p, l, x);
     const unsigned long long on = __shfl(all, at);
     const double xe = __shfl(x, at);
     const int len = __popcll(on);
@@ -106,17 +106,25 @@ __global__ __launch_bounds__(kCommitThreads) void tree_commit_kernel(TreeArgs a)
     }
 }
 
-template <typename T> hipError_t commit_launch(const TreeArgs& a, hipStream_t s) {
+template <typename T, int DK> hipError_t commit_dk(const TreeArgs& a, hipStream_t s) {
     const int nblk = (a.dv + kCommitRows - 1) / kCommitRows;
     const dim3 grid((unsigned)((long)a.B * a.H * nblk)), block(kCommitThreads);
+    // LDS for 64 nodes leaves three workgroups on a compute unit, for 16 nodes eight
+    if (a.N <= 16)
+        hipLaunchKernelGGL((tree_commit_kernel<T, DK, 16>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((tree_commit_kernel<T, DK, kTreeMax>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t commit_launch(const TreeArgs& a, hipStream_t s) {
     switch (a.dk) {
-        case 16: hipLaunchKernelGGL((tree_commit_kernel<T, 16>), grid, block, 0, s, a); break;
-        case 32: hipLaunchKernelGGL((tree_commit_kernel<T, 32>), grid, block, 0, s, a); break;
-        case 64: hipLaunchKernelGGL((tree_commit_kernel<T, 64>), grid, block, 0, s, a); break;
-        case 128: hipLaunchKernelGGL((tree_commit_kernel<T, 128>), grid, block, 0, s, a); break;
+        case 16: return commit_dk<T, 16>(a, s);
+        case 32: return commit_dk<T, 32>(a, s);
+        case 64: return commit_dk<T, 64>(a, s);
+        case 128: return commit_dk<T, 128>(a, s);
         default: return hipErrorInvalidValue;
     }
-    return hipGetLastError();
 }
 
 }  // namespace

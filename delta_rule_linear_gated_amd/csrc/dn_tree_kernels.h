@@ -41,10 +41,10 @@ __device__ __forceinline__ int tree_parent(const int* parent, int count, int n) 
 }
 // Lane n of a whole wave: the nodes on its path (itself included) as bits, and x summed
 // along it, by pointer doubling.
-__device__ __forceinline__ unsigned long long tree_path(int p, int n, double& x) {
+template <int NP> __device__ __forceinline__ unsigned long long tree_path(int p, int n, double& x) {
     unsigned long long on = 1ull << n;
 #pragma unroll
-    for (int r = 0; r < 6; ++r) {
+    for (int r = 1; r < NP; r *= 2) {   // NP nodes: a path of at most NP
         const int from = p < 0 ? n : p;
         const unsigned long long o = __shfl(on, from);
         const double y = __shfl(x, from);
@@ -71,7 +71,7 @@ template <int DK, int NP, bool VEC> struct TreeLds {
 };
 
 template <typename T, int DK, int NP, int NW, bool VEC>
-__global__ __launch_bounds__(64 * NW) void tree_kernel(TreeArgs a) {
+__global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel(TreeArgs a) {
     using L = TreeLds<DK, NP, VEC>;
     constexpr int TH = 64 * NW, NT = NP / 16, F = DK / 16, Q = DK / 4;
     __shared__ __align__(16) L s;
@@ -89,86 +89,111 @@ __global__ __launch_bounds__(64 * NW) void tree_kernel(TreeArgs a) {
     const bool active = 16 * tile < a.dv;
     const long rows = (long)bh * N;
 
-    // ---- the state's rows of this wave, in the order its products take them
+    // ---- loads, first needed first: the tree, keys and queries, then the state's rows in the
+    // order their products take them
+    int p = -1;
+    double gate = 0.0;
+    if (wave == 0) {
+        p = l < NP ? tree_parent(a.parent + (long)b * N, cnt, l) : -1;
+        if (l < cnt && a.gate == DN_GATE_SCALAR) gate = tree_clamp(a.g[rows + l]);
+        if (l < cnt && a.gate == DN_GATE_HEAD) gate = tree_clamp(a.g[h]);
+    }
+    constexpr int PC = (NP * Q + TH - 1) / TH;   // pieces of four channels a thread
+    f32x4 kr[PC], qr[PC], gr[VEC ? PC : 1];
+    float br[PC];
+#pragma unroll
+    for (int i = 0; i < PC; ++i) {
+        const int id = tid + TH * i, n = id / Q, c = 4 * (id % Q);
+        kr[i] = qr[i] = zero4();
+        br[i] = 0.f;
+        if constexpr (VEC) gr[i] = zero4();
+        if (n < cnt) {
+            const long at = (rows + n) * DK + c;
+            if constexpr (VEC) gr[i] = *reinterpret_cast<const f32x4*>(a.g + at);
+            kr[i] = ld4<T>(static_cast<const T*>(a.k) + at);
+            qr[i] = ld4<T>(static_cast<const T*>(a.q) + at);
+            if (delta && c == 0) br[i] = a.beta[rows + n];
+        }
+    }
     f32x4 S[F];
     const int vrow = 16 * tile + m;
 #pragma unroll
     for (int f = 0; f < F; ++f)
         S[f] = active ? *reinterpret_cast<const f32x4*>(a.state + ((long)bh * a.dv + vrow) * DK + 16 * f + 4 * g) : zero4();
-    float vin[NT][4];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = 16 * t + 4 * g + i;
-            vin[t][i] = active && n < cnt ? to_f(static_cast<const T*>(a.v)[(rows + n) * a.dv + vrow]) : 0.f;
-        }
 
     // ---- the tree: paths and their decays
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < PC; ++i) {
+            const int id = tid + TH * i;
+            if (id < NP * Q)
+                *reinterpret_cast<f32x4*>(&s.km[id / Q][4 * (id % Q)]) =
+                    f32x4{tree_clamp(gr[i][0]), tree_clamp(gr[i][1]), tree_clamp(gr[i][2]), tree_clamp(gr[i][3])};
+        }
+    }
     if (wave == 0) {
-        const int p = l < NP ? tree_parent(a.parent + (long)b * N, cnt, l) : -1;
-        double x = 0.0;
-        if (l < cnt && a.gate == DN_GATE_SCALAR) x = tree_clamp(a.g[rows + l]);
-        if (l < cnt && a.gate == DN_GATE_HEAD) x = tree_clamp(a.g[h]);
-        const unsigned long long on = tree_path(p, l, x);
+        const unsigned long long on = tree_path<NP>(p, l, gate);
         if (l < NP) {
             s.on[l] = on;
-            s.gam[l] = x;
+            s.gam[l] = gate;
             s.parent[l] = p;
         }
     }
+    bool deep = false;
     if constexpr (VEC) {
-        for (int id = tid; id < NP * Q; id += TH) {
-            const int n = id / Q, c = 4 * (id % Q);
-            f32x4 x = zero4();
-            if (n < cnt) x = *reinterpret_cast<const f32x4*>(a.g + (rows + n) * DK + c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s.km[n][c + i] = tree_clamp(x[i]);
-        }
         __syncthreads();
-        // path sums of a channel, a thread each; parents come before their children
+        // path sums of every channel: the paths' 0/1 matrix times the gates
         float low = 0.f;
-        for (int c = tid; c < DK; c += TH)
-            for (int n = 0; n < cnt; ++n) {
-                const int p = s.parent[n];
-                const float x = s.km[n][c] + (p >= 0 ? s.qx[p][c] : 0.f);
-                s.qx[n][c] = x;
-                low = fminf(low, x);
+        for (int ct = wave; ct < F; ct += NW) {
+            f32x4 G[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) G[t] = zero4();
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+                f32x4 gv;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) gv[i] = s.km[16 * q + 4 * g + i][16 * ct + m];
+#pragma unroll
+                for (int t = q; t < NT; ++t) {   // paths hold earlier nodes only
+                    const unsigned bits = (unsigned)(s.on[16 * t + m] >> (16 * q + 4 * g));
+                    const f32x4 on = {(float)(bits & 1), (float)(bits >> 1 & 1), (float)(bits >> 2 & 1), (float)(bits >> 3 & 1)};
+                    G[t] = tree_mma(on, gv, G[t]);
+                }
             }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s.qx[16 * t + 4 * g + i][16 * ct + m] = G[t][i];
+                    low = fminf(low, G[t][i]);
+                }
+        }
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) low = fminf(low, __shfl_xor(low, d));
         if (l == 0) s.low[wave] = low;
         __syncthreads();
-    }
-    // e^{-Gam} is finite down to -87: below, the pairs' decays are formed one by one
-    bool deep = false;
-    if constexpr (VEC) {
+        // e^{-Gam} is finite down to -87: below, the pairs' decays are formed one by one
 #pragma unroll
         for (int u = 0; u < NW; ++u) deep |= s.low[u] < -80.f;
     }
 
-    // ---- keys and queries, four channels a thread; the keys' square norms for Kaczmarz steps
-    for (int id = tid; id < NP * Q; id += TH) {
-        const int n = id / Q, c = 4 * (id % Q);
-        f32x4 kk = zero4(), qq = zero4();
-        if (n < cnt) {
-            kk = ld4<T>(static_cast<const T*>(a.k) + (rows + n) * DK + c);
-            qq = ld4<T>(static_cast<const T*>(a.q) + (rows + n) * DK + c);
-        }
+    // ---- keys and queries to LDS; the keys' square norms for Kaczmarz steps
+#pragma unroll
+    for (int j = 0; j < PC; ++j) {
+        const int id = tid + TH * j, n = id / Q, c = 4 * (id % Q);
+        if (NP * Q % TH != 0 && id >= NP * Q) continue;   // whole waves
+        f32x4 kk = kr[j], qq = qr[j];
         const float norm = group_sum<Q>(kk[0] * kk[0] + kk[1] * kk[1] + kk[2] * kk[2] + kk[3] * kk[3]);
-        if (c == 0) {
-            float bt = delta && n < cnt ? a.beta[rows + n] : 0.f;
-            if (a.kz && n < cnt) bt /= norm + a.eps;
-            s.beta[n] = bt;
-        }
+        if (c == 0) s.beta[n] = a.kz && n < cnt ? br[j] / (norm + a.eps) : br[j];
         if constexpr (VEC) {
             f32x4 e = zero4(), r = zero4();
             if (n < cnt) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(&s.qx[n][c]);
+                r = *reinterpret_cast<const f32x4*>(&s.km[n][c]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float x = s.qx[n][c + i];
-                    e[i] = expf(x);
-                    r[i] = deep ? s.km[n][c + i] : kk[i] * expf(-x);
+                    e[i] = expf(x[i]);
+                    if (!deep) r[i] = kk[i] * expf(-x[i]);
                 }
             }
             *reinterpret_cast<f32x4*>(&s.km[n][c]) = r;
@@ -194,6 +219,15 @@ __global__ __launch_bounds__(64 * NW) void tree_kernel(TreeArgs a) {
             }
         }
     }
+
+    float vin[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = 16 * t + 4 * g + i;
+            vin[t][i] = active && n < cnt ? to_f(static_cast<const T*>(a.v)[(rows + n) * a.dv + vrow]) : 0.f;
+        }
 
     // ---- node by node: A = beta (k_n . e^{..} k_m) for m before n on its path, P with q_n, m = n too
     constexpr int TRI = NT * (NT + 1) / 2;
@@ -328,10 +362,13 @@ template <typename T, int DK, int NP, int NW> hipError_t tree_launch_np(const Tr
     return hipGetLastError();
 }
 
-// 64 nodes: eight waves share the node-by-node products, which then weigh as much as the state's.
+// Eight waves, 128 state rows, share the node-by-node products and the staged rows (64
+// rows a workgroup: 35.8 us against 34.1 at 64 x 16 heads, 16 nodes); at 16 nodes 64
+// registers then let all of a compute unit's workgroups of such a batch run at once
+// (34.1 -> 24.7 us: 92 MB of inputs and outputs, 3.7 TB/s).
 template <typename T, int DK> hipError_t tree_launch_dk(const TreeArgs& a, hipStream_t s) {
-    if (a.N <= 16) return tree_launch_np<T, DK, 16, 4>(a, s);
-    if (a.N <= 32) return tree_launch_np<T, DK, 32, 4>(a, s);
+    if (a.N <= 16) return tree_launch_np<T, DK, 16, 8>(a, s);
+    if (a.N <= 32) return tree_launch_np<T, DK, 32, 8>(a, s);
     return tree_launch_np<T, DK, 64, 8>(a, s);
 }
 
