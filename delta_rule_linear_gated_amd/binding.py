@@ -140,8 +140,8 @@ def make_shape(B, H, T, dk, dv, C, dtype, gate, kaczmarz_eps=None, no_scan=False
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # the handle itself: a Stream object costs 2.5 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -530,11 +530,10 @@ class DeltaRule(torch.autograd.Function):
 # ------------------------------------------------------------------ linear attention with a decay per head
 
 
-def _check_tensors(first, want):
-    """``want``: {name: (tensor or None, dtype, shape)}.  Every tensor of that type and
-    shape, contiguous, on the CUDA device of ``first``.  Raises ValueError."""
-    dev = first.device
-    for name, (t, dt, shp) in want.items():
+def _check_tensors(dev, *want):
+    """``want``: (name, tensor or None, dtype, shape).  Every tensor of that type and shape,
+    contiguous and on ``dev``, the current CUDA device.  Raises ValueError."""
+    for name, t, dt, shp in want:
         if t is None:
             continue
         if t.dtype != dt:
@@ -547,6 +546,8 @@ def _check_tensors(first, want):
             raise ValueError(f"every tensor must be on {dev}, found one on {t.device}")
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, found one on {dev}")
+    if dev.index != torch.cuda.current_device():   # the kernels run on the current device
+        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _linear_gate(g, B, H, T, dk=None):
@@ -561,21 +562,20 @@ def _linear_gate(g, B, H, T, dk=None):
     return DN_GATE_SCALAR, (B, H, T)
 
 
-def _linear_args(q, k, v, g, no_scan=False, **more):
-    """Shape descriptor of checked tensors; ``more``: {name: (tensor, "q" | "v" | "state" | "lens")}."""
+def _linear_args(q, k, v, g, no_scan, *more):
+    """Shape descriptor of checked tensors; ``more``: (name, tensor, "v" | "state" | "lens")."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError(f"q must be [B,H,T,dk] and v [B,H,T,dv], got shapes {tuple(q.shape)}, {tuple(v.shape)}")
-    B, H, T, dk = q.shape
+    B, H, T, dk = qs = q.shape
     dv = v.shape[3]
-    if q.dtype not in _IO_DTYPES:
-        raise ValueError(f"q must be float32 or bfloat16, got {q.dtype}")
+    io = q.dtype
+    if io not in _IO_DTYPES:
+        raise ValueError(f"q must be float32 or bfloat16, got {io}")
     kind, gshape = _linear_gate(g, B, H, T)
-    kinds = {"q": (q.dtype, (B, H, T, dk)), "v": (q.dtype, (B, H, T, dv)), "state": (torch.float32, (B, H, dv, dk)),
-             "lens": (torch.int32, (B,))}
-    want = {"q": (q, *kinds["q"]), "k": (k, *kinds["q"]), "v": (v, *kinds["v"]), "g": (g, torch.float32, gshape)}
-    want.update((n, (t, *kinds[what])) for n, (t, what) in more.items())
-    _check_tensors(q, want)
-    return Shape(B, H, T, dk, dv, 64, DN_BF16 if q.dtype == torch.bfloat16 else DN_F32, kind,
+    kinds = {"v": (io, (B, H, T, dv)), "state": (torch.float32, (B, H, dv, dk)), "lens": (torch.int32, (B,))}
+    _check_tensors(q.device, ("q", q, io, qs), ("k", k, io, qs), ("v", v, *kinds["v"]), ("g", g, torch.float32, gshape),
+                   *((n, t, *kinds[what]) for n, t, what in more))
+    return Shape(B, H, T, dk, dv, 64, DN_BF16 if io == torch.bfloat16 else DN_F32, kind,
                  DN_FLAG_NO_SCAN if no_scan else 0, 0.0)
 
 
@@ -591,7 +591,7 @@ def linear_fwd(q, k, v, g=None, h0=None, lens=None, want_hT=True, ws=None, strea
     o_t = S_t q_t.  ``g``: None, [H] (a constant log-decay per head) or [B,H,T] (per step); ``lens``:
     int32 [B], the steps of each batch element (o is zero past them, hT the state after them).
     Returns (o, hT or None)."""
-    sh = _linear_args(q, k, v, g, no_scan, h0=(h0, "state"), lens=(lens, "lens"))
+    sh = _linear_args(q, k, v, g, no_scan, ("h0", h0, "state"), ("lens", lens, "lens"))
     o = torch.empty_like(v)
     hT = torch.empty(sh.B, sh.H, sh.dv, sh.dk, dtype=torch.float32, device=q.device) if want_hT else None
     ws, n = _linear_ws(sh, DN_PASS_FWD, ws, q.device)
@@ -601,7 +601,8 @@ def linear_fwd(q, k, v, g=None, h0=None, lens=None, want_hT=True, ws=None, strea
 
 def linear_bwd(q, k, v, g, h0, do, dhT=None, lens=None, want_dh0=True, ws=None, stream=None, no_scan=False):
     """Backward of linear_fwd.  Returns dict dq, dk, dv, dg (None unless g is per step), dh0 (or None)."""
-    sh = _linear_args(q, k, v, g, no_scan, h0=(h0, "state"), do=(do, "v"), dhT=(dhT, "state"), lens=(lens, "lens"))
+    sh = _linear_args(q, k, v, g, no_scan, ("h0", h0, "state"), ("do", do, "v"), ("dhT", dhT, "state"),
+                      ("lens", lens, "lens"))
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     dg = torch.empty_like(g) if sh.gate == DN_GATE_SCALAR else None
     dh0 = torch.empty(sh.B, sh.H, sh.dv, sh.dk, dtype=torch.float32, device=q.device) if want_dh0 else None
@@ -613,7 +614,7 @@ def linear_bwd(q, k, v, g, h0, do, dhT=None, lens=None, want_dh0=True, ws=None, 
 def linear_recurrent_fwd(q, k, v, g, state, stream=None):
     """T recurrent steps of linear attention (decode); ``state`` (fp32 [B,H,dv,dk]) is updated in
     place.  ``g`` as for linear_fwd.  Returns o."""
-    sh = _linear_args(q, k, v, g, state=(state, "state"))
+    sh = _linear_args(q, k, v, g, False, ("state", state, "state"))
     o = torch.empty_like(v)
     _check(dn_linear_recurrent_fwd(sh, q, k, v, g, state, o, stream))
     return o
@@ -653,10 +654,9 @@ def tree_fwd(q, k, v, beta, g, parent, state, counts=None, want_u=True, stream=N
         raise ValueError(f"q must be float32 or bfloat16, got {q.dtype}")
     kind, gshape = _linear_gate(g, B, H, N, dk)
     f32, i32 = torch.float32, torch.int32
-    _check_tensors(q, {"q": (q, q.dtype, (B, H, N, dk)), "k": (k, q.dtype, (B, H, N, dk)),
-                       "v": (v, q.dtype, (B, H, N, dv)), "beta": (beta, f32, (B, H, N)), "g": (g, f32, gshape),
-                       "parent": (parent, i32, (B, N)), "counts": (counts, i32, (B,)),
-                       "state": (state, f32, (B, H, dv, dk))})
+    _check_tensors(q.device, ("q", q, q.dtype, q.shape), ("k", k, q.dtype, q.shape), ("v", v, q.dtype, (B, H, N, dv)),
+                   ("beta", beta, f32, (B, H, N)), ("g", g, f32, gshape), ("parent", parent, i32, (B, N)),
+                   ("counts", counts, i32, (B,)), ("state", state, f32, (B, H, dv, dk)))
     sh = make_shape(B, H, N, dk, dv, 64, q.dtype, kind, kaczmarz_eps)
     o = torch.empty_like(v)
     u = torch.empty(B, H, N, dv, dtype=f32, device=q.device) if want_u else None
@@ -675,9 +675,8 @@ def tree_commit(k, u, g, parent, accept, state, stream=None):
         raise ValueError(f"k must be float32 or bfloat16, got {k.dtype}")
     kind, gshape = _linear_gate(g, B, H, N, dk)
     f32, i32 = torch.float32, torch.int32
-    _check_tensors(k, {"k": (k, k.dtype, (B, H, N, dk)), "u": (u, f32, (B, H, N, dv)), "g": (g, f32, gshape),
-                       "parent": (parent, i32, (B, N)), "accept": (accept, i32, (B,)),
-                       "state": (state, f32, (B, H, dv, dk))})
+    _check_tensors(k.device, ("k", k, k.dtype, k.shape), ("u", u, f32, (B, H, N, dv)), ("g", g, f32, gshape),
+                   ("parent", parent, i32, (B, N)), ("accept", accept, i32, (B,)), ("state", state, f32, (B, H, dv, dk)))
     sh = make_shape(B, H, N, dk, dv, 64, k.dtype, kind)
     _check(dn_tree_commit(sh, k, u, g, parent, accept, state, stream))
     return state
