@@ -4,18 +4,22 @@ Argument marshalling only: every step of the operator runs in the HIP kernels
 behind the C ABI.  PyTorch supplies device memory and the stream.  When the
 library is not built this module raises -- there is no fallback path.
 
-Low level (same names as the C ABI): ``dn_states_bytes``, ``dn_states_layout``,
-``dn_workspace_bytes``, ``dn_workspace_layout``, ``dn_chunk_fwd``, ``dn_chunk_bwd``,
-``dn_status_string``, ``dn_last_error``.  Convenience: ``chunk_fwd`` / ``chunk_bwd`` allocate outputs
-and workspace with torch and call the above; ``DeltaRule`` is a
+Low level (same names as the C ABI, ``EXPORTS``): raw calls that return the status.
+Convenience: ``chunk_fwd`` / ``chunk_bwd``, ``recurrent_fwd`` and their phase-gate forms
+for the delta rule, ``linear_fwd`` / ``linear_bwd`` / ``linear_recurrent_fwd`` for linear
+attention with a decay per head, ``tree_fwd`` / ``tree_commit`` for trees of drafted
+tokens on either's state: they check the tensors, allocate outputs and workspace with
+torch and call the above.  ``DeltaRule`` and ``LinearAttention`` are
 ``torch.autograd.Function`` over them.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdn.so")
@@ -579,6 +583,14 @@ def _linear_args(q, k, v, g, no_scan, *more):
                  DN_FLAG_NO_SCAN if no_scan else 0, 0.0)
 
 
+def _allocating(stream):
+    """Where the wrappers below allocate: on the stream that the call runs on, so that memory
+    freed here is not handed out again before that stream is done with it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
 def _linear_ws(shape, pass_, ws, device):
     n = dn_linear_workspace_bytes(shape, pass_)
     if ws is None and n:
@@ -592,9 +604,10 @@ def linear_fwd(q, k, v, g=None, h0=None, lens=None, want_hT=True, ws=None, strea
     int32 [B], the steps of each batch element (o is zero past them, hT the state after them).
     Returns (o, hT or None)."""
     sh = _linear_args(q, k, v, g, no_scan, ("h0", h0, "state"), ("lens", lens, "lens"))
-    o = torch.empty_like(v)
-    hT = torch.empty(sh.B, sh.H, sh.dv, sh.dk, dtype=torch.float32, device=q.device) if want_hT else None
-    ws, n = _linear_ws(sh, DN_PASS_FWD, ws, q.device)
+    with _allocating(stream):
+        o = torch.empty_like(v)
+        hT = torch.empty(sh.B, sh.H, sh.dv, sh.dk, dtype=torch.float32, device=q.device) if want_hT else None
+        ws, n = _linear_ws(sh, DN_PASS_FWD, ws, q.device)
     _check(dn_linear_fwd(sh, q, k, v, g, lens, h0, o, hT, ws, n, stream))
     return o, hT
 
@@ -603,10 +616,11 @@ def linear_bwd(q, k, v, g, h0, do, dhT=None, lens=None, want_dh0=True, ws=None, 
     """Backward of linear_fwd.  Returns dict dq, dk, dv, dg (None unless g is per step), dh0 (or None)."""
     sh = _linear_args(q, k, v, g, no_scan, ("h0", h0, "state"), ("do", do, "v"), ("dhT", dhT, "state"),
                       ("lens", lens, "lens"))
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dg = torch.empty_like(g) if sh.gate == DN_GATE_SCALAR else None
-    dh0 = torch.empty(sh.B, sh.H, sh.dv, sh.dk, dtype=torch.float32, device=q.device) if want_dh0 else None
-    ws, n = _linear_ws(sh, DN_PASS_BWD, ws, q.device)
+    with _allocating(stream):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dg = torch.empty_like(g) if sh.gate == DN_GATE_SCALAR else None
+        dh0 = torch.empty(sh.B, sh.H, sh.dv, sh.dk, dtype=torch.float32, device=q.device) if want_dh0 else None
+        ws, n = _linear_ws(sh, DN_PASS_BWD, ws, q.device)
     _check(dn_linear_bwd(sh, q, k, v, g, lens, h0, do, dhT, dq, dk, dv, dg, dh0, ws, n, stream))
     return {"dq": dq, "dk": dk, "dv": dv, "dg": dg, "dh0": dh0}
 
@@ -615,21 +629,25 @@ def linear_recurrent_fwd(q, k, v, g, state, stream=None):
     """T recurrent steps of linear attention (decode); ``state`` (fp32 [B,H,dv,dk]) is updated in
     place.  ``g`` as for linear_fwd.  Returns o."""
     sh = _linear_args(q, k, v, g, False, ("state", state, "state"))
-    o = torch.empty_like(v)
+    with _allocating(stream):
+        o = torch.empty_like(v)
     _check(dn_linear_recurrent_fwd(sh, q, k, v, g, state, o, stream))
     return o
 
 
 class LinearAttention(torch.autograd.Function):
-    """o, hT = LinearAttention.apply(q, k, v, g, h0, lens); g [H] gets no gradient."""
+    """o, hT = LinearAttention.apply(q, k, v, g, h0, lens); g [H] is a constant of the model."""
 
     @staticmethod
     def forward(ctx, q, k, v, g=None, h0=None, lens=None):
+        if g is not None and g.dim() == 1 and ctx.needs_input_grad[3]:
+            raise ValueError("g [H] is a constant: it gets no gradient (a learned decay is given per step, [B,H,T])")
         o, hT = linear_fwd(q, k, v, g, h0, lens=lens)
         ctx.save_for_backward(q, k, v, g, h0, lens)
         return o, hT
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, dhT):
         q, k, v, g, h0, lens = ctx.saved_tensors
         gr = linear_bwd(q, k, v, g, h0, do.contiguous(), None if dhT is None else dhT.contiguous(), lens=lens,
@@ -658,8 +676,9 @@ def tree_fwd(q, k, v, beta, g, parent, state, counts=None, want_u=True, stream=N
                    ("beta", beta, f32, (B, H, N)), ("g", g, f32, gshape), ("parent", parent, i32, (B, N)),
                    ("counts", counts, i32, (B,)), ("state", state, f32, (B, H, dv, dk)))
     sh = make_shape(B, H, N, dk, dv, 64, q.dtype, kind, kaczmarz_eps)
-    o = torch.empty_like(v)
-    u = torch.empty(B, H, N, dv, dtype=f32, device=q.device) if want_u else None
+    with _allocating(stream):
+        o = torch.empty_like(v)
+        u = torch.empty(B, H, N, dv, dtype=f32, device=q.device) if want_u else None
     _check(dn_tree_fwd(sh, q, k, v, beta, g, parent, counts, state, o, u, stream))
     return o, u
 

@@ -8,8 +8,8 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <utility>
-#include <vector>
 
 #include "dn.h"
 #include "dn_internal.h"
@@ -90,17 +90,17 @@ struct Buf {
 
 // Required pointers must be non-NULL when non-empty; all must be 16-byte
 // aligned; outputs may not overlap anything else.
-dn_status check_buffers(const std::vector<Buf>& bufs) {
+dn_status check_buffers(std::initializer_list<Buf> bufs) {   // no allocation: nothing here can throw
     for (const Buf& b : bufs) {
         if (b.bytes == 0 || !b.p) continue;
         if (reinterpret_cast<uintptr_t>(b.p) % 16 != 0)
             return fail(DN_ERR_INVALID, "%s is not 16-byte aligned", b.name);
     }
-    for (size_t i = 0; i < bufs.size(); ++i) {
-        const Buf& a = bufs[i];
+    for (const Buf* i = bufs.begin(); i != bufs.end(); ++i) {
+        const Buf& a = *i;
         if (!a.p || a.bytes == 0) continue;
-        for (size_t j = i + 1; j < bufs.size(); ++j) {
-            const Buf& b = bufs[j];
+        for (const Buf* j = i + 1; j != bufs.end(); ++j) {
+            const Buf& b = *j;
             if (!b.p || b.bytes == 0 || (!a.output && !b.output)) continue;
             const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), a1 = a0 + a.bytes;
             const uintptr_t b0 = reinterpret_cast<uintptr_t>(b.p), b1 = b0 + b.bytes;

@@ -275,3 +275,55 @@ def test_other_stream_and_shared_workspace():
     side.synchronize()
     for n, t in {"o": o, "hT": hT, **gr}.items():
         assert torch.equal(t, ref[n]), n
+
+
+def test_guard_bands():
+    """Outputs and workspace inside pattern-filled margins through the raw calls: nothing is
+    written outside them, and inputs stay as they are."""
+    for dtype, (Bn, H, T, dk, dv), lens in (("bf16", (2, 1, 1300, 128, 64), [1300, 90]), ("fp32", (1, 3, 77, 16, 128), None)):
+        d = draw(dtype, "scalar", Bn, H, T, dk, dv, lens=lens, seed=40)
+        keep = {n: t.clone() for n, t in d.items() if t is not None}
+        ref = run(d)
+        sh = B.make_shape(Bn, H, T, dk, dv, 64, dtype, "scalar")
+        margin = 4096
+        bufs, views = [], {}
+
+        def banded(name, like=None, nbytes=None):
+            n = nbytes if like is None else like.numel() * like.element_size()
+            buf = torch.full((n + 2 * margin,), 0xA5, dtype=torch.uint8, device="cuda")
+            bufs.append((name, buf, n))
+            mid = buf[margin:margin + n]
+            views[name] = mid if like is None else mid.view(like.dtype).view(like.shape)
+            return views[name]
+
+        nf, nb = B.dn_linear_workspace_bytes(sh, B.DN_PASS_FWD), B.dn_linear_workspace_bytes(sh, B.DN_PASS_BWD)
+        st = B.dn_linear_fwd(sh, d["q"], d["k"], d["v"], d["g"], d["lens"], d["h0"], banded("o", ref["o"]),
+                             banded("hT", ref["hT"]), banded("wf", nbytes=nf) if nf else None, nf)
+        assert st == B.DN_OK
+        outs = [banded(n, ref[n]) for n in ("dq", "dk", "dv", "dg", "dh0")]
+        st = B.dn_linear_bwd(sh, d["q"], d["k"], d["v"], d["g"], d["lens"], d["h0"], d["do"], d["dhT"], *outs,
+                             banded("wb", nbytes=nb), nb)
+        assert st == B.DN_OK
+        torch.cuda.synchronize()
+        for name, buf, n in bufs:
+            assert bool((buf[:margin] == 0xA5).all()) and bool((buf[margin + n:] == 0xA5).all()), name
+        for n in ref:
+            assert torch.equal(views[n], ref[n]), n
+        for n, t in keep.items():
+            assert torch.equal(d[n], t), n
+
+
+def test_memory_of_a_call_on_another_stream():
+    """Workspace that the wrapper allocates for a call on a side stream is not handed out to the
+    current stream's tensors while that call runs."""
+    d = draw("bf16", "scalar", 1, 2, 4000, 64, 64, seed=41)
+    ref = run(d)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(8):
+        gr = B.linear_bwd(d["q"], d["k"], d["v"], d["g"], d["h0"], d["do"], d["dhT"], stream=side)
+        junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(16)]
+        side.synchronize()
+        for n, t in gr.items():
+            assert torch.equal(t, ref[n]), n
+        del junk, gr

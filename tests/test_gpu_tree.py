@@ -285,3 +285,32 @@ def test_graph_capture():
         ro, ru = step(fresh, at)
         torch.cuda.synchronize()
         assert torch.equal(o, ro) and torch.equal(u, ru) and torch.equal(static["state"], fresh["state"]), seed
+
+
+def test_guard_bands():
+    for dtype, gate, shape in (("bf16", "vector", (2, 3, 19, 64, 80)), ("fp32", "scalar", (1, 2, 64, 128, 16))):
+        d = draw(dtype, gate, True, *shape, seed=40)
+        Bn, H, N, dk, dv = shape
+        keep = {n: t.clone() for n, t in d.items() if t is not None}
+        o, u = B.tree_fwd(d["q"], d["k"], d["v"], d["beta"], d["g"], d["parent"], d["state"])
+        at = torch.full((Bn,), N - 1, dtype=torch.int32, device="cuda")
+        want = B.tree_commit(d["k"], u, d["g"], d["parent"], at, d["state"].clone())
+        margin, bufs = 4096, []
+
+        def banded(like):
+            n = like.numel() * like.element_size()
+            buf = torch.full((n + 2 * margin,), 0xA5, dtype=torch.uint8, device="cuda")
+            bufs.append((buf, n))
+            return buf[margin:margin + n].view(like.dtype).view(like.shape)
+
+        sh = B.make_shape(Bn, H, N, dk, dv, 64, dtype, gate)
+        o2, u2, st = banded(o), banded(u), banded(want)
+        st.copy_(d["state"])
+        assert B.dn_tree_fwd(sh, d["q"], d["k"], d["v"], d["beta"], d["g"], d["parent"], None, d["state"], o2, u2) == B.DN_OK
+        assert B.dn_tree_commit(sh, d["k"], u2, d["g"], d["parent"], at, st) == B.DN_OK
+        torch.cuda.synchronize()
+        for buf, n in bufs:
+            assert bool((buf[:margin] == 0xA5).all()) and bool((buf[margin + n:] == 0xA5).all())
+        assert torch.equal(o, o2) and torch.equal(u, u2) and torch.equal(st, want)
+        for n, t in keep.items():
+            assert torch.equal(d[n], t), n
