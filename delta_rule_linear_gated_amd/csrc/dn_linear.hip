@@ -15,37 +15,32 @@ constexpr int kLinMaxSeg = 64;   // parallel segments of a sequence
 // Boundary states of the parallel segments: entry s of snap holds segment s's own
 // contribution (from a zero state) and gets the state the segment starts from,
 //     start_{s+1} = dec_s start_s + end_s,
-// walked first to last (rev: last to first).  A thread owns four elements of one
-// (b, h) state; 16 entries are loaded at once, since the walk waits for nothing else.
-__global__ __launch_bounds__(256) void lin_join_kernel(LinArgs a) {
-    const int quads = a.kd * a.nd / 4;   // a multiple of 64
-    const int per = (quads + 255) / 256;
-    const int oi = blockIdx.y;
+// walked first to last (rev: last to first).  A thread owns one element of one (b, h)
+// state and loads all N >= nseg entries of it at once: the walk itself is short, and
+// waiting for the entries batch by batch took most of the time (4 heads, 64 segments:
+// 23 us in four batches, 13 us at once).
+template <int N> __global__ __launch_bounds__(256) void lin_join_kernel(LinArgs a) {
+    const int se = a.kd * a.nd;   // a multiple of 256
+    const int per = se / 256, oi = blockIdx.y;
     const int bh = blockIdx.x / per, at = (blockIdx.x % per) * 256 + threadIdx.x;
-    if (at >= quads) return;
     const LinOp& op = a.op[oi];
-    const long se = (long)a.kd * a.nd;
-    float* base = op.snap + bh * op.snap_bh + 4 * at;
+    float* base = op.snap + bh * op.snap_bh + at;
     // one factor a lane: loaded once, not waited for at every entry
-    static_assert(kLinMaxSeg <= 64, "a factor of each segment in a lane");
+    static_assert(N <= 64, "a factor of each segment in a lane");
     const float dec = a.segdec[((long)oi * a.BH + bh) * a.nseg + min(lane_id(), a.nseg - 1)];
-    f32x4 cur = op.init ? *reinterpret_cast<const f32x4*>(op.init + bh * se + 4 * at) : zero4();
+    float cur = op.init ? op.init[(long)bh * se + at] : 0.f;
+    const int r = a.seg_len / a.snap, last = (a.NT - 1) / a.snap;
     auto slot = [&](int i) {   // i-th segment walked -> its entry
         const int s = op.rev ? a.nseg - 1 - i : i;
-        const int c0 = s * a.seg_len, c1 = min(a.NT, c0 + a.seg_len);
-        return reinterpret_cast<f32x4*>(base + (op.rev ? (c1 - 1) / a.snap : c0 / a.snap) * se);
+        return base + (long)(op.rev ? min((s + 1) * r - 1, last) : s * r) * se;
     };
-    constexpr int AHEAD = 16;   // entries loaded at once
-    for (int i0 = 0; i0 < a.nseg; i0 += AHEAD) {
-        f32x4 own[AHEAD];
+    float own[N];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) own[i] = *slot(min(i0 + i, a.nseg - 1));
+    for (int i = 0; i < N; ++i) own[i] = *slot(min(i, a.nseg - 1));
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            if (i0 + i >= a.nseg) break;
-            *slot(i0 + i) = cur;   // the last segment's own part is nowhere formed, nor used
-            if (i0 + i + 1 < a.nseg) cur = cur * __shfl(dec, op.rev ? a.nseg - 1 - (i0 + i) : i0 + i) + own[i];
-        }
+    for (int i = 0; i < N; ++i) {
+        if (i < a.nseg) *slot(i) = cur;   // the last segment's own part is nowhere formed, nor used
+        cur = cur * __shfl(dec, op.rev ? a.nseg - 1 - i : i) + own[i];
     }
 }
 
@@ -278,8 +273,13 @@ hipError_t launch_boundaries(const LinProblem& pr, LinArgs a, hipStream_t s) {
     prof_end(s);
     if (e != hipSuccess) return e;
     prof_begin(s, "linear_join");
-    const int per = (a.kd * a.nd / 4 + 255) / 256;
-    hipLaunchKernelGGL(lin_join_kernel, dim3((unsigned)(a.BH * per), a.nops), dim3(256), 0, s, a);
+    const dim3 grid((unsigned)(a.BH * (a.kd * a.nd / 256)), a.nops), block(256);
+    if (a.nseg <= 8)
+        hipLaunchKernelGGL(lin_join_kernel<8>, grid, block, 0, s, a);
+    else if (a.nseg <= 16)
+        hipLaunchKernelGGL(lin_join_kernel<16>, grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL(lin_join_kernel<kLinMaxSeg>, grid, block, 0, s, a);
     prof_end(s);
     return hipGetLastError();
 }
