@@ -29,6 +29,7 @@
 
 #include "dn_device.h"
 #include "dn_linear.h"
+#include "dn_split.h"
 
 namespace dn {
 
@@ -77,18 +78,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t lin_range(const void* base, in
 }
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int at) {
     return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
-}
-
-// Two floats as two packed bf16; what that leaves of them stays in a, b.  N such steps
-// hold 8 N bits of each.  (Written on pairs: one conversion and four more operations a
-// step.)
-__device__ __forceinline__ unsigned take_bf16(float& a, float& b) {
-    typedef __attribute__((ext_vector_type(2))) float f32x2;
-    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
-    const unsigned u = __builtin_bit_cast(unsigned, __builtin_convertvector((f32x2{a, b}), bf16x2));
-    a -= __builtin_bit_cast(float, u << 16);
-    b -= __builtin_bit_cast(float, u & 0xffff0000u);
-    return u;
 }
 
 // LDS rows of y and z are padded for the transposed reads, which take four rows of 32

@@ -9,17 +9,22 @@
 // state is read once whatever the number of branches, and never copied.
 //
 // A workgroup takes one (b, h) and a block of state rows (16 a wave).  Everything is held
-// and multiplied in fp32 (fp32 matrix-core steps, operands straight from the state's own
-// rows): u is an fp32 output from which states are continued, and at 16 nodes the
-// products take under half of the time that reading the states takes.  A wave keeps its
+// to fp32, since u is an fp32 output from which states are continued: fp32 matrix-core
+// steps, or, where keys and queries are bf16 and no channel has a gate of its own (HALF),
+// bf16 steps that are as exact: the products of keys and queries as they are, those with
+// the state on three bf16 parts of it (24 bits), at a fifth of the fp32 steps' time.
+// The state's operands come straight from its rows.  A wave keeps its
 // columns of u in accumulators from the first product to the last: accumulator row
 // 4 g + i is K slot g of step i of the next product, so the chain X -> R -> u -> o needs
 // no LDS besides the node-by-node matrices.  The system is solved by 16-node blocks, the
 // diagonal ones inverted by substitution, one lane a column.
 #pragma once
 
+#include <type_traits>
+
 #include "dn.h"
 #include "dn_device.h"
+#include "dn_split.h"
 #include "dn_tree.h"
 
 namespace dn {
@@ -58,9 +63,12 @@ template <int NP> __device__ __forceinline__ unsigned long long tree_path(int p,
     return on;
 }
 
-template <int DK, int NP, bool VEC> struct TreeLds {
-    static constexpr int LD = DK + 4, LN = NP + 4;
-    float kx[NP][LD], qx[NP][LD];        // k, q; per channel gate: times e^{Gam}
+template <typename T, int DK, int NP, bool VEC> struct TreeLds {
+    static constexpr bool HALF = sizeof(T) == 2 && !VEC;
+    static constexpr int DP = HALF && DK < 32 ? 32 : DK;   // one bf16 step at least, zeros behind DK
+    static constexpr int LD = DP + (HALF ? 16 : 4), LN = NP + 4;
+    typedef typename std::conditional<HALF, bf16, float>::type X;
+    X kx[NP][LD], qx[NP][LD];            // k, q; per channel gate: times e^{Gam}
     float km[VEC ? NP : 1][VEC ? LD : 1];   // k e^{-Gam}, or the gates where that would overflow
     float A[NP][LN], P[NP][LN];          // the system's matrix (its diagonal blocks inverted in place), the outputs'
     unsigned long long on[NP];
@@ -72,7 +80,8 @@ template <int DK, int NP, bool VEC> struct TreeLds {
 
 template <typename T, int DK, int NP, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel(TreeArgs a) {
-    using L = TreeLds<DK, NP, VEC>;
+    using L = TreeLds<T, DK, NP, VEC>;
+    constexpr bool HALF = L::HALF;
     constexpr int TH = 64 * NW, NT = NP / 16, F = DK / 16, Q = DK / 4;
     __shared__ __align__(16) L s;
     const int nblk = (a.dv / 16 + NW - 1) / NW;
@@ -115,11 +124,14 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
             if (delta && c == 0) br[i] = a.beta[rows + n];
         }
     }
-    f32x4 S[F];
+    constexpr int SF = L::DP / 16;
+    f32x4 S[SF];   // pieces of four channels: of step f, 16 f + 4 g; HALF: of step f / 2, 32 (f / 2) + 8 g + 4 (f % 2)
     const int vrow = 16 * tile + m;
 #pragma unroll
-    for (int f = 0; f < F; ++f)
-        S[f] = active ? *reinterpret_cast<const f32x4*>(a.state + ((long)bh * a.dv + vrow) * DK + 16 * f + 4 * g) : zero4();
+    for (int f = 0; f < SF; ++f) {
+        const int c = HALF ? 32 * (f / 2) + 8 * g + 4 * (f % 2) : 16 * f + 4 * g;
+        S[f] = active && c < DK ? *reinterpret_cast<const f32x4*>(a.state + ((long)bh * a.dv + vrow) * DK + c) : zero4();
+    }
 
     // ---- the tree: paths and their decays
     if constexpr (VEC) {
@@ -200,8 +212,12 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
             kk = kk * e;
             qq = qq * e;
         }
-        *reinterpret_cast<f32x4*>(&s.kx[n][c]) = kk;
-        *reinterpret_cast<f32x4*>(&s.qx[n][c]) = qq;
+        st4<typename L::X>(&s.kx[n][c], kk);
+        st4<typename L::X>(&s.qx[n][c], qq);
+        if constexpr (L::DP > DK) {
+            st4<typename L::X>(&s.kx[n][DK + c], zero4());
+            st4<typename L::X>(&s.qx[n][DK + c], zero4());
+        }
     }
     __syncthreads();
 
@@ -210,16 +226,41 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
 #pragma unroll
     for (int t = 0; t < NT; ++t) X[t] = zero4(), o[t] = zero4();
     if (active) {
+        if constexpr (HALF) {
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
+            for (int f = 0; f < L::DP / 32; ++f) {
+                float x[8];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                o[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.qx[16 * t + m][16 * f + 4 * g]), S[f], o[t]);
-                if (delta) X[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.kx[16 * t + m][16 * f + 4 * g]), S[f], X[t]);
+                for (int e = 0; e < 8; ++e) x[e] = S[2 * f + e / 4][e & 3];
+                unsigned part[3][4];
+#pragma unroll
+                for (int e = 0; e < 8; e += 2)
+#pragma unroll
+                    for (int r = 0; r < 3; ++r) part[r][e / 2] = take_bf16(x[e], x[e + 1]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const bf16x8 qf = *reinterpret_cast<const bf16x8*>(&s.qx[16 * t + m][32 * f + 8 * g]);
+                    const bf16x8 kf = *reinterpret_cast<const bf16x8*>(&s.kx[16 * t + m][32 * f + 8 * g]);
+#pragma unroll
+                    for (int r = 0; r < 3; ++r) {
+                        const bf16x8 sp = *reinterpret_cast<const bf16x8*>(part[r]);
+                        o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf, sp, o[t], 0, 0, 0);
+                        if (delta) X[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, sp, X[t], 0, 0, 0);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    o[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.qx[16 * t + m][16 * f + 4 * g]), S[f], o[t]);
+                    if (delta)
+                        X[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.kx[16 * t + m][16 * f + 4 * g]), S[f], X[t]);
+                }
             }
         }
     }
-
     float vin[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -238,12 +279,19 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
             int tn = 0, tm = isP ? id : id - TRI;
             while (tm > tn) tm -= ++tn;
             f32x4 acc = zero4();
+            const typename L::X* nr = isP ? &s.qx[16 * tn + m][0] : &s.kx[16 * tn + m][0];
+            if constexpr (HALF) {
 #pragma unroll
-            for (int f = 0; f < F; ++f) {
-                const float* nr = isP ? &s.qx[16 * tn + m][0] : &s.kx[16 * tn + m][0];
+                for (int f = 0; f < L::DP / 32; ++f)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        *reinterpret_cast<const bf16x8*>(nr + 32 * f + 8 * g),
+                        *reinterpret_cast<const bf16x8*>(&s.kx[16 * tm + m][32 * f + 8 * g]), acc, 0, 0, 0);
+            } else {
                 const float* mr = VEC ? &s.km[16 * tm + m][0] : &s.kx[16 * tm + m][0];
-                acc = tree_mma(*reinterpret_cast<const f32x4*>(nr + 16 * f + 4 * g),
-                               *reinterpret_cast<const f32x4*>(mr + 16 * f + 4 * g), acc);
+#pragma unroll
+                for (int f = 0; f < F; ++f)
+                    acc = tree_mma(*reinterpret_cast<const f32x4*>(nr + 16 * f + 4 * g),
+                                   *reinterpret_cast<const f32x4*>(mr + 16 * f + 4 * g), acc);
             }
             const int mm = 16 * tm + m;
 #pragma unroll
@@ -365,7 +413,7 @@ template <typename T, int DK, int NP, int NW> hipError_t tree_launch_np(const Tr
 // Eight waves, 128 state rows, share the node-by-node products and the staged rows (64
 // rows a workgroup: 35.8 us against 34.1 at 64 x 16 heads, 16 nodes); at 16 nodes 64
 // registers then let all of a compute unit's workgroups of such a batch run at once
-// (34.1 -> 24.7 us: 92 MB of inputs and outputs, 3.7 TB/s).
+// (34.1 -> 24.7 us; with the bf16 steps 18.6: 92 MB of inputs and outputs, 4.9 TB/s).
 template <typename T, int DK> hipError_t tree_launch_dk(const TreeArgs& a, hipStream_t s) {
     if (a.N <= 16) return tree_launch_np<T, DK, 16, 8>(a, s);
     if (a.N <= 32) return tree_launch_np<T, DK, 32, 8>(a, s);
