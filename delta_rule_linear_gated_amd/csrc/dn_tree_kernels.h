@@ -10,9 +10,10 @@
 //
 // A workgroup takes one (b, h) and a block of state rows (16 a wave).  Everything is held
 // to fp32, since u is an fp32 output from which states are continued: fp32 matrix-core
-// steps, or, where keys and queries are bf16 and no channel has a gate of its own (HALF),
-// bf16 steps that are as exact: the products of keys and queries as they are, those with
-// the state on three bf16 parts of it (24 bits), at a fifth of the fp32 steps' time.
+// steps for fp32 keys and queries; for bf16 ones bf16 steps that are as exact, on three
+// bf16 parts (24 bits) of the state, of keys scaled by channel gates  and two of
+// queries scaled by them (o is rounded to bf16): a fifth of the fp32 steps' time,
+// a third with channel gates.
 // The state's operands come straight from its rows.  A wave keeps its
 // columns of u in accumulators from the first product to the last: accumulator row
 // 4 g + i is K slot g of step i of the next product, so the chain X -> R -> u -> o needs
@@ -33,6 +34,18 @@ __device__ __forceinline__ f32x4 tree_mma(f32x4 a, f32x4 b, f32x4 c) {   // K ov
 #pragma unroll
     for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
     return c;
+}
+
+// Eight floats as three bf16 parts (24 bits).
+__device__ __forceinline__ void tree_parts(f32x4 a, f32x4 b, bf16x8 (&p)[3]) {
+    float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    unsigned u[3][4];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+#pragma unroll
+        for (int r = 0; r < 3; ++r) u[r][e / 2] = take_bf16(x[e], x[e + 1]);
+#pragma unroll
+    for (int r = 0; r < 3; ++r) p[r] = *reinterpret_cast<const bf16x8*>(u[r]);
 }
 
 // Gates below -1000 are a factor of zero whatever follows, and their sums stay finite.
@@ -64,11 +77,15 @@ template <int NP> __device__ __forceinline__ unsigned long long tree_path(int p,
 }
 
 template <typename T, int DK, int NP, bool VEC> struct TreeLds {
-    static constexpr bool HALF = sizeof(T) == 2 && !VEC;
-    static constexpr int DP = HALF && DK < 32 ? 32 : DK;   // one bf16 step at least, zeros behind DK
-    static constexpr int LD = DP + (HALF ? 16 : 4), LN = NP + 4;
-    typedef typename std::conditional<HALF, bf16, float>::type X;
-    X kx[NP][LD], qx[NP][LD];            // k, q; per channel gate: times e^{Gam}
+    static constexpr bool BF = sizeof(T) == 2;
+    static constexpr int DP = BF && DK < 32 ? 32 : DK;     // one bf16 step at least, zeros behind DK
+    static constexpr int LD = DK + 4, LN = NP + 4;
+    // k and q; per channel gate: times e^{Gam}.  bf16 parts or fp32.
+    static constexpr int KP = !BF ? 1 : VEC ? 3 : 1, QP = !BF ? 1 : VEC ? 2 : 1;
+    static constexpr int LX = BF ? DP + (VEC ? 8 : 16) : LD;
+    typedef typename std::conditional<BF, bf16, float>::type X;
+    __align__(16) X kx[KP][NP][LX];
+    X qx[QP][NP][LX];
     float km[VEC ? NP : 1][VEC ? LD : 1];   // k e^{-Gam}, or the gates where that would overflow
     float A[NP][LN], P[NP][LN];          // the system's matrix (its diagonal blocks inverted in place), the outputs'
     unsigned long long on[NP];
@@ -81,7 +98,8 @@ template <typename T, int DK, int NP, bool VEC> struct TreeLds {
 template <typename T, int DK, int NP, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel(TreeArgs a) {
     using L = TreeLds<T, DK, NP, VEC>;
-    constexpr bool HALF = L::HALF;
+    constexpr bool BF = L::BF, PARTS = BF && VEC;
+    constexpr int KP = L::KP, QP = L::QP;
     constexpr int TH = 64 * NW, NT = NP / 16, F = DK / 16, Q = DK / 4;
     __shared__ __align__(16) L s;
     const int nblk = (a.dv / 16 + NW - 1) / NW;
@@ -125,11 +143,11 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
         }
     }
     constexpr int SF = L::DP / 16;
-    f32x4 S[SF];   // pieces of four channels: of step f, 16 f + 4 g; HALF: of step f / 2, 32 (f / 2) + 8 g + 4 (f % 2)
+    f32x4 S[SF];   // pieces of four channels: of step f, 16 f + 4 g; BF: of step f / 2, 32 (f / 2) + 8 g + 4 (f % 2)
     const int vrow = 16 * tile + m;
 #pragma unroll
     for (int f = 0; f < SF; ++f) {
-        const int c = HALF ? 32 * (f / 2) + 8 * g + 4 * (f % 2) : 16 * f + 4 * g;
+        const int c = BF ? 32 * (f / 2) + 8 * g + 4 * (f % 2) : 16 * f + 4 * g;
         S[f] = active && c < DK ? *reinterpret_cast<const f32x4*>(a.state + ((long)bh * a.dv + vrow) * DK + c) : zero4();
     }
 
@@ -152,6 +170,8 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
         }
     }
     bool deep = false;
+    float* G0 = reinterpret_cast<float*>(PARTS ? static_cast<void*>(s.kx) : static_cast<void*>(s.qx));   // Gam of every channel
+    constexpr int LD = L::LD;
     if constexpr (VEC) {
         __syncthreads();
         // path sums of every channel: the paths' 0/1 matrix times the gates
@@ -176,7 +196,7 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    s.qx[16 * t + 4 * g + i][16 * ct + m] = G[t][i];
+                    G0[(16 * t + 4 * g + i) * LD + 16 * ct + m] = G[t][i];
                     low = fminf(low, G[t][i]);
                 }
         }
@@ -184,9 +204,10 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
         for (int d = 1; d < 64; d *= 2) low = fminf(low, __shfl_xor(low, d));
         if (l == 0) s.low[wave] = low;
         __syncthreads();
-        // e^{-Gam} is finite down to -87: below, the pairs' decays are formed one by one
+        // Down to -60 e^{Gam}, e^{-Gam} and their parts keep clear of the ends of the exponents'
+        // range; below, the pairs' decays are formed one by one.
 #pragma unroll
-        for (int u = 0; u < NW; ++u) deep |= s.low[u] < -80.f;
+        for (int u = 0; u < NW; ++u) deep |= s.low[u] < -60.f;
     }
 
     // ---- keys and queries to LDS; the keys' square norms for Kaczmarz steps
@@ -194,13 +215,13 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
     for (int j = 0; j < PC; ++j) {
         const int id = tid + TH * j, n = id / Q, c = 4 * (id % Q);
         if (NP * Q % TH != 0 && id >= NP * Q) continue;   // whole waves
-        f32x4 kk = kr[j], qq = qr[j];
+        const f32x4 kk = kr[j];
         const float norm = group_sum<Q>(kk[0] * kk[0] + kk[1] * kk[1] + kk[2] * kk[2] + kk[3] * kk[3]);
         if (c == 0) s.beta[n] = a.kz && n < cnt ? br[j] / (norm + a.eps) : br[j];
         if constexpr (VEC) {
             f32x4 e = zero4(), r = zero4();
             if (n < cnt) {
-                const f32x4 x = *reinterpret_cast<const f32x4*>(&s.qx[n][c]);
+                const f32x4 x = *reinterpret_cast<const f32x4*>(&G0[n * LD + c]);
                 r = *reinterpret_cast<const f32x4*>(&s.km[n][c]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -209,15 +230,31 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
                 }
             }
             *reinterpret_cast<f32x4*>(&s.km[n][c]) = r;
-            kk = kk * e;
-            qq = qq * e;
+            kr[j] = kk * e;
+            qr[j] = qr[j] * e;
         }
-        st4<typename L::X>(&s.kx[n][c], kk);
-        st4<typename L::X>(&s.qx[n][c], qq);
-        if constexpr (L::DP > DK) {
-            st4<typename L::X>(&s.kx[n][DK + c], zero4());
-            st4<typename L::X>(&s.qx[n][DK + c], zero4());
-        }
+    }
+    if constexpr (PARTS) __syncthreads();   // the path sums lie where the parts go
+#pragma unroll
+    for (int j = 0; j < PC; ++j) {
+        const int id = tid + TH * j, n = id / Q, c = 4 * (id % Q);
+        if (NP * Q % TH != 0 && id >= NP * Q) continue;
+        f32x4 kk = kr[j], qq = qr[j];
+        auto put = [&](typename L::X (&to)[NP][L::LX], f32x4 (&v)) {   // the first part; what it leaves stays in v
+            if constexpr (BF) {
+                float v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
+                const unsigned u0 = take_bf16(v0, v1), u1 = take_bf16(v2, v3);
+                *reinterpret_cast<uint2*>(&to[n][c]) = make_uint2(u0, u1);
+                v = f32x4{v0, v1, v2, v3};
+                if constexpr (L::DP > DK) *reinterpret_cast<uint2*>(&to[n][DK + c]) = make_uint2(0u, 0u);
+            } else {
+                *reinterpret_cast<f32x4*>(&to[n][c]) = v;
+            }
+        };
+#pragma unroll
+        for (int r = 0; r < KP; ++r) put(s.kx[r], kk);
+#pragma unroll
+        for (int r = 0; r < QP; ++r) put(s.qx[r], qq);
     }
     __syncthreads();
 
@@ -225,27 +262,31 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
     f32x4 X[NT], o[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) X[t] = zero4(), o[t] = zero4();
+    // Parts r of one factor and q of the other are multiplied for r + q below the number of
+    // parts that the result needs: three for u, two for outputs of per-channel gates (the
+    // scaled queries are two parts), three where the queries are exact.
     if (active) {
-        if constexpr (HALF) {
+        if constexpr (BF) {
 #pragma unroll
             for (int f = 0; f < L::DP / 32; ++f) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = S[2 * f + e / 4][e & 3];
-                unsigned part[3][4];
-#pragma unroll
-                for (int e = 0; e < 8; e += 2)
-#pragma unroll
-                    for (int r = 0; r < 3; ++r) part[r][e / 2] = take_bf16(x[e], x[e + 1]);
+                bf16x8 sp[3];
+                tree_parts(S[2 * f], S[2 * f + 1], sp);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const bf16x8 qf = *reinterpret_cast<const bf16x8*>(&s.qx[16 * t + m][32 * f + 8 * g]);
-                    const bf16x8 kf = *reinterpret_cast<const bf16x8*>(&s.kx[16 * t + m][32 * f + 8 * g]);
 #pragma unroll
-                    for (int r = 0; r < 3; ++r) {
-                        const bf16x8 sp = *reinterpret_cast<const bf16x8*>(part[r]);
-                        o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf, sp, o[t], 0, 0, 0);
-                        if (delta) X[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, sp, X[t], 0, 0, 0);
+                    for (int r = 0; r < QP; ++r) {
+                        const bf16x8 qf = *reinterpret_cast<const bf16x8*>(&s.qx[r][16 * t + m][32 * f + 8 * g]);
+#pragma unroll
+                        for (int q = 0; q < (PARTS ? 2 : 3) - r; ++q)
+                            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf, sp[q], o[t], 0, 0, 0);
+                    }
+                    if (!delta) continue;
+#pragma unroll
+                    for (int r = 0; r < KP; ++r) {
+                        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(&s.kx[r][16 * t + m][32 * f + 8 * g]);
+#pragma unroll
+                        for (int q = 0; q < 3 - r; ++q)
+                            X[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, sp[q], X[t], 0, 0, 0);
                     }
                 }
             }
@@ -254,9 +295,9 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
             for (int f = 0; f < F; ++f) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    o[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.qx[16 * t + m][16 * f + 4 * g]), S[f], o[t]);
+                    o[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.qx[0][16 * t + m][16 * f + 4 * g]), S[f], o[t]);
                     if (delta)
-                        X[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.kx[16 * t + m][16 * f + 4 * g]), S[f], X[t]);
+                        X[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.kx[0][16 * t + m][16 * f + 4 * g]), S[f], X[t]);
                 }
             }
         }
@@ -279,15 +320,40 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
             int tn = 0, tm = isP ? id : id - TRI;
             while (tm > tn) tm -= ++tn;
             f32x4 acc = zero4();
-            const typename L::X* nr = isP ? &s.qx[16 * tn + m][0] : &s.kx[16 * tn + m][0];
-            if constexpr (HALF) {
+            if constexpr (BF) {
 #pragma unroll
-                for (int f = 0; f < L::DP / 32; ++f)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        *reinterpret_cast<const bf16x8*>(nr + 32 * f + 8 * g),
-                        *reinterpret_cast<const bf16x8*>(&s.kx[16 * tm + m][32 * f + 8 * g]), acc, 0, 0, 0);
+                for (int f = 0; f < L::DP / 32; ++f) {
+                    bf16x8 mp[3];
+                    if constexpr (VEC) {   // k e^{-Gam} of 8 channels in parts (zero behind DK)
+                        const int c = 32 * f + 8 * g;
+                        const float* mr = &s.km[16 * tm + m][c < DK ? c : 0];
+                        const f32x4 z = zero4();
+                        tree_parts(c < DK ? *reinterpret_cast<const f32x4*>(mr) : z,
+                                   c < DK ? *reinterpret_cast<const f32x4*>(mr + 4) : z, mp);
+                    } else {
+                        mp[0] = *reinterpret_cast<const bf16x8*>(&s.kx[0][16 * tm + m][32 * f + 8 * g]);
+                    }
+                    if (isP) {
+#pragma unroll
+                        for (int r = 0; r < QP; ++r) {
+                            const bf16x8 nf = *reinterpret_cast<const bf16x8*>(&s.qx[r][16 * tn + m][32 * f + 8 * g]);
+#pragma unroll
+                            for (int q = 0; q < QP - r; ++q)
+                                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf, mp[q], acc, 0, 0, 0);
+                        }
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < KP; ++r) {
+                            const bf16x8 nf = *reinterpret_cast<const bf16x8*>(&s.kx[r][16 * tn + m][32 * f + 8 * g]);
+#pragma unroll
+                            for (int q = 0; q < KP - r; ++q)
+                                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf, mp[q], acc, 0, 0, 0);
+                        }
+                    }
+                }
             } else {
-                const float* mr = VEC ? &s.km[16 * tm + m][0] : &s.kx[16 * tm + m][0];
+                const float* nr = isP ? &s.qx[0][16 * tn + m][0] : &s.kx[0][16 * tn + m][0];
+                const float* mr = VEC ? &s.km[16 * tm + m][0] : &s.kx[0][16 * tm + m][0];
 #pragma unroll
                 for (int f = 0; f < F; ++f)
                     acc = tree_mma(*reinterpret_cast<const f32x4*>(nr + 16 * f + 4 * g),

@@ -144,6 +144,16 @@ def test_steep_gates_and_resets(gate, dtype):
     verify(d, f"reset {gate} {dtype}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scale", [0.6, 1.1, 1.4, 1.8, 2.5])
+def test_long_decays_of_channels(scale, dtype):
+    """Paths whose channels decay by e^-20 to e^-90, on both sides of where the pairs' decays
+    stop being products of two factors."""
+    for N in (16, 40):
+        d = draw(dtype, "vector", True, 2, 2, N, 64, 64, "chain", seed=30, scale=scale * 40 / N)
+        verify(d, f"long decay {scale} {N} {dtype}")
+
+
 @pytest.mark.parametrize("gate", ["scalar", "vector"])
 def test_kaczmarz_steps(gate):
     d = draw("bf16", gate, True, 2, 2, 24, 64, 64, seed=5)
