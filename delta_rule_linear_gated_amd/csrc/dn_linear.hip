@@ -1,6 +1,8 @@
 // dn_linear.hip -- linear attention with a decay per head: the split of the steps,
 // the launch sequences, the kernels between the chunk kernels (dn_linear_kernels.h)
 // and the recurrent form.
+#include <algorithm>
+
 #include "dn_device.h"
 #include "dn_internal.h"
 #include "dn_linear.h"
@@ -217,17 +219,24 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 int blocks_of(int nd, int bf16) { return nd / lin_vb(nd, bf16 != 0); }
 
 // Parallel segments of the steps.  One run of all chunks reads every tensor once; s > 1
-// segments cost a pass over the two tensors of the state and the boundary states, and
-// pay while the device has idle compute units.
+// segments cost a pass over the two tensors of the state, the boundary states and two
+// launches, and pay while the device has idle compute units.  From 256 workgroups on
+// (one for each unit): one run (8 x 16 heads, 4096 steps: 137 us, 2 segments 215).
+// Below, segments of at least 4 chunks for up to four workgroups a unit, which the units
+// take in turn (32 heads, 32768 steps, backward: 1.10 ms, with 512 workgroups 1.29); while
+// even those leave units idle, of 2 chunks (4 heads, 1024 steps: 20 us, of 4 chunks 26,
+// one run 37; with 512 workgroups there already they cost more than they save: 4 x 16
+// heads, 1024 steps 45 us against 55).
 LinPlan lin_plan(const LinProblem& pr, int nops, bool dots) {
     const int NT = ceil_div(pr.T, kLinC);
     const long wgs = (long)pr.B * pr.H * blocks_of(pr.dv, pr.bf16) * nops;
-    constexpr long kWant = 1024, kFull = 256, kMinLen = 4;
-    long ns = wgs > 0 ? kWant / wgs : 1;
-    if (pr.no_scan || wgs >= kFull) ns = 1;
-    if (ns > kLinMaxSeg) ns = kLinMaxSeg;
-    if (ns > NT / kMinLen) ns = NT / kMinLen;
-    if (ns < 1) ns = 1;
+    constexpr long kUnits = 256;
+    long ns = 1;
+    if (!pr.no_scan && wgs > 0 && wgs < kUnits) {
+        ns = std::min<long>(4 * kUnits / wgs, NT / 4);
+        if (NT >= 8 && ns * wgs < kUnits) ns = std::min<long>(kUnits / wgs, NT / 2);
+        ns = std::max<long>(1, std::min<long>(ns, kLinMaxSeg));
+    }
     LinPlan p;
     p.seg_len = NT > 0 ? ceil_div(NT, (int)ns) : 1;
     if (dots && ns > 1 && p.seg_len > kLinSnap) p.seg_len = ceil_div(p.seg_len, kLinSnap) * kLinSnap;
@@ -236,6 +245,9 @@ LinPlan lin_plan(const LinProblem& pr, int nops, bool dots) {
     p.nent = NT > 0 ? ceil_div(NT, p.snap) : 1;
     return p;
 }
+
+// Evaluations that share a launch in the backward.
+int bwd_ops(bool dots) { return dots ? 2 : 3; }
 
 const LinLaunch kLaunch[2][3] = {{lin_f32_k32, lin_f32_k64, lin_f32_k128}, {lin_bf16_k32, lin_bf16_k64, lin_bf16_k128}};
 
@@ -290,7 +302,7 @@ struct LinWs {
 LinWs lin_ws(const LinProblem& pr, int pass) {
     const size_t BH = (size_t)pr.B * pr.H, se = (size_t)pr.dk * pr.dv * 4;
     const bool bwd = pass != 0, dots = bwd && pr.gate == kLinScalar;
-    const LinPlan p = lin_plan(pr, bwd ? 3 : 1, dots);
+    const LinPlan p = lin_plan(pr, bwd ? bwd_ops(dots) : 1, dots);
     const bool keep = p.nseg > 1 || dots;
     LinWs w{};
     size_t off = 0;
@@ -344,7 +356,7 @@ hipError_t launch_linear_fwd(const LinProblem& pr, const LinFwd& f, char* ws, hi
 hipError_t launch_linear_bwd(const LinProblem& pr, const LinBwd& f, char* ws, hipStream_t s) {
     if (pr.B * pr.H == 0) return hipSuccess;
     const bool dots = pr.gate == kLinScalar;
-    const LinPlan pl = lin_plan(pr, 3, dots);
+    const LinPlan pl = lin_plan(pr, bwd_ops(dots), dots);
     const LinWs w = lin_ws(pr, 1);
     const bool keep = pl.nseg > 1 || dots;
     float* s_snap = keep ? reinterpret_cast<float*>(ws + w.s_snap) : nullptr;
