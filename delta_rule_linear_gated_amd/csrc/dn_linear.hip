@@ -55,21 +55,17 @@ template <int N> __global__ __launch_bounds__(256) void lin_join_kernel(LinArgs 
 // a stretch are known from the kept states, and what the sum misses at t0 is taken off
 // evenly along it; the pairs inside a chunk sum to zero over it, and what they sum to
 // is taken off evenly along the chunk.  Sums in 64 bits.  A thread owns four steps.
-__device__ __forceinline__ double block_sum(double x, double* part) {
-    part[threadIdx.x] = x;
+__device__ __forceinline__ double block_sum(double x, double* part) {   // part: one slot a wave, used once
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
+    if (lane_id() == 0) part[wave_id()] = x;
     __syncthreads();
-    for (int d = 128; d > 0; d /= 2) {
-        if ((int)threadIdx.x < d) part[threadIdx.x] += part[threadIdx.x + d];
-        __syncthreads();
-    }
-    const double r = part[0];
-    __syncthreads();
-    return r;
+    return part[0] + part[1] + part[2] + part[3];
 }
 __global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* h0, const float* s_snap,
                                                         const float* d_snap, const float* dhT, const float* dots1,
                                                         int n1, const float* dots2, int n2, float* dg) {
-    __shared__ double part[256];
+    __shared__ double part[3][4];
     const int bh = blockIdx.x / a.nent, e = blockIdx.x % a.nent, tid = threadIdx.x;
     const int n = lin_len(a.lens, bh / a.H, a.T);
     const int len = a.snap * kLinC, t0 = e * len, t1 = min(t0 + len, n);
@@ -80,12 +76,23 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* 
         return;
     }
     // B at step t from the state before it and the cotangent from it on (NULL: zero)
-    auto straddle = [&](const float* S, const float* D, int t) {
+    auto straddle = [&](const float* S, const float* D, int t, double* part) {
         if (!S || !D) return 0.0;
         double x = 0.0;
-        for (long i = 4 * tid; i < se; i += 1024) {
-            const f32x4 u = *reinterpret_cast<const f32x4*>(S + i), v = *reinterpret_cast<const f32x4*>(D + i);
-            x += (double)u[0] * v[0] + (double)u[1] * v[1] + (double)u[2] * v[2] + (double)u[3] * v[3];
+        constexpr int AHEAD = 8;   // pieces in flight (a state: 16 at most)
+        for (int i0 = 4 * tid; i0 < (int)se; i0 += 1024 * AHEAD) {
+            f32x4 u[AHEAD], v[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int at = i0 + 1024 * i < (int)se ? i0 + 1024 * i : i0;
+                u[i] = *reinterpret_cast<const f32x4*>(S + at);
+                v[i] = *reinterpret_cast<const f32x4*>(D + at);
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (i0 + 1024 * i < (int)se)
+                    x += (double)u[i][0] * v[i][0] + (double)u[i][1] * v[i][1] + (double)u[i][2] * v[i][2] +
+                         (double)u[i][3] * v[i][3];
         }
         return block_sum(x, part) * (t < n ? (double)expf(a.g[row + t]) : 1.0);
     };
@@ -93,9 +100,10 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* 
     const float* dk = d_snap + (long)bh * (a.nent + 1) * se;
     const bool last = t1 >= n;   // then the cotangent is dhT and the state the last one
     const double B1 = straddle(sk + (last ? a.nent : e + 1) * se, last ? (dhT ? dhT + bh * se : nullptr) : dk + e * se,
-                               last ? n : t1);
+                               last ? n : t1, part[0]);
     // the first step's gate decays h0, and nothing without one
-    const double B0 = straddle(e > 0 ? sk + e * se : h0 ? h0 + bh * se : nullptr, dk + (e > 0 ? e - 1 : a.nent) * se, t0);
+    const double B0 = straddle(e > 0 ? sk + e * se : h0 ? h0 + bh * se : nullptr, dk + (e > 0 ? e - 1 : a.nent) * se, t0,
+                               part[1]);
     const long nt = (long)a.BH * a.T;
     const int ta = t0 + 4 * tid, tb = min(ta + 4, t1);
     double inter[4], pairs[4], off = 0.0;
@@ -124,16 +132,23 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* 
         if (ta + i < tb) inter[i] += pairs[i] - off / live;
         own += inter[i];
     }
-    part[tid] = own;
-    __syncthreads();
-    for (int d = 1; d < 256; d *= 2) {   // suffix sums
-        const double y = tid + d < 256 ? part[tid + d] : 0.0;
-        __syncthreads();
-        part[tid] += y;
-        __syncthreads();
+    // sums of the threads from each on: within the wave, then the waves behind it
+    double from = own;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const double y = __shfl_down(from, d);
+        if (lane_id() + d < 64) from += y;
     }
-    const double slope = (B0 - (B1 + part[0])) / (t1 - t0);
-    double acc = B1 + (tid < 255 ? part[tid + 1] : 0.0);
+    if (lane_id() == 0) part[2][wave_id()] = from;
+    __syncthreads();
+    double all = 0.0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        all += part[2][u];
+        if (u > wave_id()) from += part[2][u];
+    }
+    const double slope = (B0 - (B1 + all)) / (t1 - t0);
+    double acc = B1 + from - own;
 #pragma unroll
     for (int i = 3; i >= 0; --i) {
         const int t = ta + i;

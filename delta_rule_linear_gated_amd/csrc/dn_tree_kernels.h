@@ -19,6 +19,11 @@
 // 4 g + i is K slot g of step i of the next product, so the chain X -> R -> u -> o needs
 // no LDS besides the node-by-node matrices.  The system is solved by 16-node blocks, the
 // diagonal ones inverted by substitution, one lane a column.
+//
+// Measured (bf16, d = 128): 64 x 16 heads, 16 nodes 18.6 us for 92 MB (4.9 TB/s where a
+// copy reaches 5.2: bound by the state's bytes); 16 x 16 heads, 61 nodes with channel
+// gates 28.7 us for 49 MB: one workgroup on a compute unit, bound by its chain of phases
+// (loads, path sums, scaling, products, solution), the products a third of it.
 #pragma once
 
 #include <type_traits>
@@ -92,7 +97,7 @@ template <typename T, int DK, int NP, bool VEC> struct TreeLds {
     double gam[NP];                      // Gam of a gate per step or head
     float beta[NP];
     int parent[NP];
-    float low[8];                        // the lowest Gam of any channel, by wave
+    float low[8];                        // less the largest |Gam| of any channel, by wave
 };
 
 template <typename T, int DK, int NP, int NW, bool VEC>
@@ -197,15 +202,15 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     G0[(16 * t + 4 * g + i) * LD + 16 * ct + m] = G[t][i];
-                    low = fminf(low, G[t][i]);
+                    low = fminf(low, -fabsf(G[t][i]));
                 }
         }
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) low = fminf(low, __shfl_xor(low, d));
         if (l == 0) s.low[wave] = low;
         __syncthreads();
-        // Down to -60 e^{Gam}, e^{-Gam} and their parts keep clear of the ends of the exponents'
-        // range; below, the pairs' decays are formed one by one.
+        // Up to |Gam| = 60 e^{Gam}, e^{-Gam} and their parts keep clear of the ends of the
+        // exponents' range; beyond, the pairs' decays are formed one by one.
 #pragma unroll
         for (int u = 0; u < NW; ++u) deep |= s.low[u] < -60.f;
     }

@@ -374,7 +374,8 @@ dn_status dn_linear_recurrent_fwd(const dn_shape* shape, const void* q, const vo
  *            counts int32 [B] or NULL: the nodes of each batch element (clamped to
  *            0 .. T), o and u are zero from there on; accept int32 [B]; state fp32
  *            [B][H][dv][dk].  Gates below -1000 act as -1000 (a factor of zero).
- *   outputs: o (io) and u fp32, both [B][H][T][dv] (u NULL = not wanted); fp32 arithmetic
+ *   outputs: o (io) and u fp32, both [B][H][T][dv] (u NULL = not wanted); fp32 arithmetic.
+ *            NaN or Inf in a node may reach every node of its tree
  * Validation and errors as for dn_recurrent_fwd; no workspace.
  */
 dn_status dn_tree_fwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* beta,
