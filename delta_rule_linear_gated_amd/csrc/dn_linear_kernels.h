@@ -18,7 +18,8 @@
 // Rounding (bf16 I/O): P enters its product with z as two bf16 parts (16 bits: a
 // sequence of one step has a single P, whose rounding nothing averages), S is
 // rounded once for its product with x, which adds at most as much to an output's
-// error as the output's own rounding.  The state itself is held to fp32: its operand
+// error as the output's own rounding (two parts in the first chunk: a call of few steps
+// from a cached state has few outputs to average it over).  The state itself is held to fp32: its operand
 // z e^{..} enters as three bf16 parts (24 bits), since a state (hT, dh0) is an
 // fp32 output.  Where the gate's gradient is wanted, an fp32 sum of differences of
 // r . out, P and the state enter in three parts too, and P's diagonal, which is no part
@@ -95,9 +96,10 @@ template <typename T, int KD, int NV, int MODE> struct LinLds {
     static constexpr int VB = 16 * NV, E = 16 / sizeof(T), PAD = sizeof(T) == 2 ? 2 * E : E;
     static constexpr int LY = KD + PAD, LZ = VB + PAD, LS = KD + E;
     static constexpr int NS = MODE == kLinState ? 0 : DG && sizeof(T) == 2 ? 3 : 1;   // parts of the state operand
+    static constexpr int N1 = MODE == kLinOut && sizeof(T) == 2 ? 2 : NS;             // of the first chunk's
     T y[kLinC * LY];
     T z[kLinC * LZ];
-    T s[NS > 0 ? NS : 1][NS > 0 ? VB * LS : 1];
+    T s[N1 > 0 ? N1 : 1][N1 > 0 ? VB * LS : 1];
     // R: G from the first step of the row's 16 (two floats); e^{G_63 - G};
     // e^{G_16w - G_j} of the rows j before 16 w, w = 1, 2, 3; e^{G_16w}; the chunk's factor
     float hi[kLinC], lo[kLinC], ew[kLinC], tab[3][kLinC], eref[4], etot;
@@ -126,7 +128,7 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
     using X = LinT<T>;
     using Frag = typename X::Frag;
     using L = LinLds<T, KD, NV, MODE>;
-    constexpr int E = X::E, JS = X::JS, VB = 16 * NV, LY = L::LY, LZ = L::LZ, LS = L::LS, NS = L::NS;
+    constexpr int E = X::E, JS = X::JS, VB = 16 * NV, LY = L::LY, LZ = L::LZ, LS = L::LS, NS = L::NS, N1 = L::N1;
     constexpr int NVW = NV / HV;                             // output tiles of a wave
     constexpr int XF = KD / (4 * E);                         // fragments of an x row
     constexpr int WV = 4 / NV;                               // waves that share a state tile column
@@ -329,17 +331,18 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
                 }
             });
         };
-        auto put_state = [&]() {
+        auto put_state = [&](auto parts) {
+            constexpr int N = decltype(parts)::value;
             if (!owns) return;
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 const int at = (16 * vt + m) * LS + 16 * (ct0 + ct) + 4 * g;
-                if constexpr (NS == 1) {
+                if constexpr (N == 1) {
                     st4<T>(&s.s[0][at], S[ct]);
                 } else {
                     float v0 = S[ct][0], v1 = S[ct][1], v2 = S[ct][2], v3 = S[ct][3];
 #pragma unroll
-                    for (int p = 0; p < NS; ++p) {
+                    for (int p = 0; p < N; ++p) {
                         const u32x2 v = {take_bf16(v0, v1), take_bf16(v2, v3)};
                         *reinterpret_cast<u32x2*>(&s.s[p][at]) = v;
                     }
@@ -363,9 +366,10 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
                 put_gates();
             }
             put_tiles();
-            if constexpr (OUT && !O) put_state();
+            if constexpr (OUT && !O) put_state(std::integral_constant<int, N1>{});
         }
-        for (int ci = 0; ci < count; ++ci) {
+        auto chunk = [&](int ci, auto of_run) {
+            constexpr bool FIRST = decltype(of_run)::value;   // of the run
             const int c = first + step * ci;
             const int next = ci + 1 < count ? c + step : c;   // after the last chunk: it again, unused
             __syncthreads();
@@ -377,10 +381,11 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
 #pragma unroll
                 for (int i = 0; i < NVW; ++i) acc[i] = zero4();
                 // ---- from earlier chunks
+                constexpr int NP1 = FIRST ? N1 : NS;
 #pragma unroll
                 for (int f = 0; f < XF; ++f)
 #pragma unroll
-                    for (int p = 0; p < NS; ++p)
+                    for (int p = 0; p < NP1; ++p)
 #pragma unroll
                         for (int i = 0; i < NVW; ++i) {   // consecutive steps: different accumulators
                             const int at = out_col(tile0 + i, m >> 2, m & 3) * LS + 4 * E * f + E * g;
@@ -553,11 +558,14 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
             __syncthreads();
             if (gates) put_gates();
             put_tiles();
-            if constexpr (OUT && !O) put_state();
+            if constexpr (OUT && !O) put_state(std::integral_constant<int, NS>{});
             if constexpr (DG && O && HV > 1) {   // the halves of a step's dot
                 if (wave < 2) put_dot(wave, c, row_at(l, 1) / (int)sizeof(T) * 4, s.dot[wave][0][l] + s.dot[wave][1][l]);
             }
-        }
+        };
+        // Apart where its state has more parts: a branch in the loop would cost a tenth of its time.
+        if (count > 0) chunk(0, std::integral_constant<bool, (N1 > NS)>{});
+        for (int ci = 1; ci < count; ++ci) chunk(ci, std::false_type{});
 
         // ---- the last state, the segment's own state and factor
         if constexpr (!O) {
