@@ -563,6 +563,8 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
                 if (wave < 2) put_dot(wave, c, row_at(l, 1) / (int)sizeof(T) * 4, s.dot[wave][0][l] + s.dot[wave][1][l]);
             }
         };
+        // The waves that are done first with a chunk go first (1 % of the time of long runs).
+        if constexpr (MODE != kLinState && (MODE == kLinOut) == O) __builtin_amdgcn_s_setprio(3);
         // Apart where its state has more parts: a branch in the loop would cost a tenth of its time.
         if (count > 0) chunk(0, std::integral_constant<bool, (N1 > NS)>{});
         for (int ci = 1; ci < count; ++ci) chunk(ci, std::false_type{});
