@@ -121,6 +121,29 @@ __device__ __forceinline__ double lin_log2(float g, int n, int t, int rev) {
     return (double)(g < -1000.f ? -1000.f : g) * 1.4426950408889634;
 }
 
+// Sums in 64 bits over the lanes of a wave up to each, and the value of one lane, on the
+// vector ALU alone (a scan by LDS permutes took a quarter of a chunk's time in the wave
+// that makes it): DPP row_shr 1, 2, 4, 8, then row_bcast 15 and 31 into the rows behind.
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_add(double x) {
+    const uint2 u = __builtin_bit_cast(uint2, x);
+    const uint2 v = make_uint2((unsigned)__builtin_amdgcn_update_dpp(0, (int)u.x, CTRL, ROWS, 0xF, false),
+                               (unsigned)__builtin_amdgcn_update_dpp(0, (int)u.y, CTRL, ROWS, 0xF, false));
+    return x + __builtin_bit_cast(double, v);
+}
+__device__ __forceinline__ double wave_scan(double x) {
+    x = dpp_add<0x111, 0xF>(x);
+    x = dpp_add<0x112, 0xF>(x);
+    x = dpp_add<0x114, 0xF>(x);
+    x = dpp_add<0x118, 0xF>(x);
+    x = dpp_add<0x142, 0xA>(x);
+    return dpp_add<0x143, 0xC>(x);
+}
+__device__ __forceinline__ double of_lane(double x, int l) {
+    const uint2 u = __builtin_bit_cast(uint2, x);
+    return __builtin_bit_cast(double, make_uint2((unsigned)__builtin_amdgcn_readlane((int)u.x, l),
+                                                 (unsigned)__builtin_amdgcn_readlane((int)u.y, l)));
+}
+
 template <typename T, int KD, int NV, int MODE>
 __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MODE, sizeof(T) == 2)) void lin_kernel(LinArgs a) {
     constexpr bool OUT = MODE != kLinState, DG = MODE == kLinDots;
@@ -261,19 +284,16 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
         double dec = 0.0;                                  // of the run so far
         float ghi = 0.f, glo = 0.f, gew = 0.f, gtab[4] = {}, getot = 0.f, geref = 0.f;
         auto form_gates = [&](double x2) {
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                const double y2 = __shfl_up(x2, d);
-                if (l >= d) x2 += y2;
-            }
-            const double tot = __shfl(x2, 63), own = __shfl(x2, l & 48);
+            x2 = wave_scan(x2);
+            const double tot = of_lane(x2, 63), at[4] = {of_lane(x2, 0), of_lane(x2, 16), of_lane(x2, 32), of_lane(x2, 48)};
+            const double own = g < 2 ? (g == 0 ? at[0] : at[1]) : (g == 2 ? at[2] : at[3]);   // of the row's block
             ghi = (float)(x2 - own), glo = (float)(x2 - own - (double)ghi);
             gew = exp2_hw((float)(tot - x2));
             getot = exp2_hw((float)tot);
             geref = exp2_hw((float)own);
             if constexpr (OUT) {
 #pragma unroll
-                for (int u = 1; u < 4; ++u) gtab[u] = exp2_hw((float)(__shfl(x2, 16 * u) - x2));
+                for (int u = 1; u < 4; ++u) gtab[u] = exp2_hw((float)(at[u] - x2));
             }
             dec += tot;
         };
