@@ -700,7 +700,8 @@ dn_status linear_shape(const dn_shape* s, bool recurrent, dn::LinProblem* pr, Di
     if (!width(s->dk)) return fail(DN_ERR_UNSUPPORTED, "dk must be 16, 32, 64 or 128");
     if (recurrent) {
         if (s->dv % 16 != 0) return fail(DN_ERR_UNSUPPORTED, "dv must be a positive multiple of 16");
-        if ((long long)s->B * s->H * (s->dv / 16) > 0x7fffffffLL) return fail(DN_ERR_UNSUPPORTED, "B*H*dv/16 too large");
+        // a launch holds less than 2^32 threads, 256 for 16 state rows
+        if ((long long)s->B * s->H > 0xffffffLL / (s->dv / 16)) return fail(DN_ERR_UNSUPPORTED, "B*H*dv/16 too large");
     } else {
         if (!width(s->dv)) return fail(DN_ERR_UNSUPPORTED, "dv must be 16, 32, 64 or 128");
         if ((long long)s->B * s->H > 65535) return fail(DN_ERR_UNSUPPORTED, "B*H must be <= 65535");
@@ -859,7 +860,8 @@ dn_status tree_shape(const dn_shape* s, dn::TreeArgs* a, Dims* d) {
     if (s->dk != 16 && s->dk != 32 && s->dk != 64 && s->dk != 128)
         return fail(DN_ERR_UNSUPPORTED, "dk must be 16, 32, 64 or 128");
     if (s->dv <= 0 || s->dv % 16 != 0) return fail(DN_ERR_UNSUPPORTED, "dv must be a positive multiple of 16");
-    if ((long long)s->B * s->H * ((s->dv + 63) / 64) > 0x7fffffffLL)
+    // a launch holds less than 2^32 threads: 512 for 128 state rows here, 256 for 64 in the commit
+    if ((long long)s->B * s->H > 0x7fffffLL / ((s->dv + 63) / 64))
         return fail(DN_ERR_UNSUPPORTED, "B*H*ceil(dv/64) too large");
     *a = dn::TreeArgs{};
     a->B = s->B;

@@ -347,7 +347,7 @@ dn_status dn_linear_bwd(const dn_shape* shape, const void* q, const void* k, con
  * Its recurrent form (decode): T steps per batch element and head, the state (fp32
  * [B][H][dv][dk]) updated in place, as dn_recurrent_fwd.
  *   shape  : dk in {16, 32, 64, 128}, dv a positive multiple of 16; gate as for
- *            dn_linear_fwd; C unused; flags as for dn_linear_fwd
+ *            dn_linear_fwd; C unused; flags as for dn_linear_fwd; B*H*dv/16 <= 2^24 - 1
  */
 dn_status dn_linear_recurrent_fwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* g,
                                   float* state, void* o, void* stream);
@@ -368,7 +368,7 @@ dn_status dn_linear_recurrent_fwd(const dn_shape* shape, const void* q, const vo
  *            multiple of 16; dtype (q, k, v, o); gate: any dn_gate (g [B][H][T],
  *            [B][H][T][dk] or [H]); flags: DN_FLAG_KACZMARZ (dn_tree_fwd with beta, which
  *            then carries eta; dn_tree_commit ignores it), DN_FLAG_NO_SCAN is ignored; C
- *            unused.  B*H*ceil(dv/64) <= 2^31 - 1
+ *            unused.  B*H*ceil(dv/64) <= 2^23 - 1
  *   inputs : q, k, v, beta (NULL: linear attention), g (NULL iff no gate) as for
  *            dn_recurrent_fwd, the nodes in the place of the steps; parent int32 [B][T];
  *            counts int32 [B] or NULL: the nodes of each batch element (clamped to

@@ -137,6 +137,20 @@ def test_tree_pointers():
     assert commit(sh(), state=FAKE * 2) == INVALID                     # over u
 
 
+def test_more_heads_than_a_launch_holds():
+    """A launch has less than 2^32 threads: calls past that are refused for it, the one before is not."""
+    for B_, H in ((2 ** 23, 1), (4096, 2048), (2 ** 31 - 1, 2 ** 31 - 1)):
+        s = sh(B=B_, H=H, T=1, dk=16, dv=16)
+        for call in (tree, commit):
+            assert call(s, state=None) == UNSUPPORTED and "B*H" in B.dn_last_error()
+    for call in (tree, commit):
+        assert call(sh(B=2 ** 23 - 1, H=1, T=1, dk=16, dv=16), state=None) == INVALID
+        assert call(sh(B=2 ** 22, H=1, T=1, dk=16, dv=80), state=None) == UNSUPPORTED
+    assert lin_rec(sh(B=2 ** 24, H=1, T=1, dk=16, dv=16), state=None) == UNSUPPORTED and "B*H" in B.dn_last_error()
+    assert lin_rec(sh(B=2 ** 12, H=2 ** 8, T=1, dk=16, dv=256), state=None) == UNSUPPORTED
+    assert lin_rec(sh(B=2 ** 24 - 1, H=1, T=1, dk=16, dv=16), state=None) == INVALID
+
+
 def _tensors(dtype=torch.bfloat16, Bn=2, H=3, T=10, dk=32, dv=64):
     z = torch.zeros
     return dict(q=z(Bn, H, T, dk, dtype=dtype), k=z(Bn, H, T, dk, dtype=dtype), v=z(Bn, H, T, dv, dtype=dtype),
