@@ -588,7 +588,9 @@ def _allocating(stream):
     freed here is not handed out again before that stream is done with it."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    if not isinstance(stream, torch.cuda.Stream):   # a handle; 0 is the default stream's
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _linear_ws(shape, pass_, ws, device):
@@ -636,7 +638,10 @@ def linear_recurrent_fwd(q, k, v, g, state, stream=None):
 
 
 class LinearAttention(torch.autograd.Function):
-    """o, hT = LinearAttention.apply(q, k, v, g, h0, lens); g [H] is a constant of the model."""
+    """o, hT = LinearAttention.apply(q, k, v, g, h0, lens); g [H] is a constant of the model.
+    A backward pass is captured into a HIP graph only while no eager autograd graph of the same
+    leaves lives: such a graph ties their gradients to its own stream, which the capture may not
+    touch (linear_fwd and linear_bwd themselves can always be captured)."""
 
     @staticmethod
     def forward(ctx, q, k, v, g=None, h0=None, lens=None):

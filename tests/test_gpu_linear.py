@@ -327,3 +327,17 @@ def test_memory_of_a_call_on_another_stream():
         for n, t in gr.items():
             assert torch.equal(t, ref[n]), n
         del junk, gr
+
+
+def test_memory_of_a_call_on_the_default_stream_by_its_handle():
+    """stream=0 names the default stream: what the wrapper allocates for it is that stream's memory,
+    not another's, which would hand it out again while the default stream still works on it."""
+    d = draw("fp32", "head", 1, 2, 2048, 64, 64, seed=42)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        o, _ = B.linear_fwd(d["q"], d["k"], d["v"], d["g"], None, want_hT=False, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(o, B.linear_fwd(d["q"], d["k"], d["v"], d["g"], None, want_hT=False)[0])
+    own = [s for s in torch.cuda.memory_snapshot() if 0 <= o.data_ptr() - s["address"] < s["total_size"]]
+    assert [s["stream"] for s in own] == [0]
