@@ -99,7 +99,12 @@ template <typename T, int KD, int NV, int MODE> struct LinLds {
     static constexpr int N1 = MODE == kLinOut && sizeof(T) == 2 ? 2 : NS;             // of the first chunk's
     T y[kLinC * LY];
     T z[kLinC * LZ];
-    T s[N1 > 0 ? N1 : 1][N1 > 0 ? VB * LS : 1];
+    // The state operand.  bf16: double, so that the waves of the state, which are done before those
+    // of the outputs, write the next chunk's at once (the first chunk's parts take both buffers);
+    // with fp32 rows it is the state that the others wait for.
+    static constexpr bool TWO = sizeof(T) == 2 && MODE != kLinState;
+    T s[TWO ? 2 * NS : NS > 0 ? NS : 1][NS > 0 ? VB * LS : 1];
+    static_assert(N1 <= (TWO ? 2 : 1) * NS, "the first chunk's parts fit the buffers");
     // R: G from the first step of the row's 16 (two floats); e^{G_63 - G};
     // e^{G_16w - G_j} of the rows j before 16 w, w = 1, 2, 3; e^{G_16w}; the chunk's factor
     float hi[kLinC], lo[kLinC], ew[kLinC], tab[3][kLinC], eref[4], etot;
@@ -351,12 +356,12 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
                 }
             });
         };
-        auto put_state = [&](auto parts) {
+        auto put_state = [&](auto parts, int buf) {
             constexpr int N = decltype(parts)::value;
             if (!owns) return;
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                const int at = (16 * vt + m) * LS + 16 * (ct0 + ct) + 4 * g;
+                const int at = buf * NS * VB * LS + (16 * vt + m) * LS + 16 * (ct0 + ct) + 4 * g;
                 if constexpr (N == 1) {
                     st4<T>(&s.s[0][at], S[ct]);
                 } else {
@@ -386,12 +391,14 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
                 put_gates();
             }
             put_tiles();
-            if constexpr (OUT && !O) put_state(std::integral_constant<int, N1>{});
+            if constexpr (OUT && !O) put_state(std::integral_constant<int, N1>{}, 0);
         }
         auto chunk = [&](int ci, auto of_run) {
             constexpr bool FIRST = decltype(of_run)::value;   // of the run
             const int c = first + step * ci;
             const int next = ci + 1 < count ? c + step : c;   // after the last chunk: it again, unused
+            constexpr bool EARLY = L::TWO && !FIRST;   // the next state operand is written beside this one's reads
+            const int buf = L::TWO ? ci & 1 : 0, buf1 = L::TWO ? buf ^ 1 : 0;
             __syncthreads();
             const float gn = lin_gate(a, gp, n, time_of(next, l), rev);
             load(next);
@@ -408,7 +415,7 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
                     for (int p = 0; p < NP1; ++p)
 #pragma unroll
                         for (int i = 0; i < NVW; ++i) {   // consecutive steps: different accumulators
-                            const int at = out_col(tile0 + i, m >> 2, m & 3) * LS + 4 * E * f + E * g;
+                            const int at = buf * NS * VB * LS + out_col(tile0 + i, m >> 2, m & 3) * LS + 4 * E * f + E * g;
                             acc[i] = X::mma(*reinterpret_cast<const Frag*>(&s.s[p][at]), x[f], acc[i]);
                         }
                 // The factors of a step's row: e^{G_16w} and e^{R}; pairs with the 16-step blocks before
@@ -573,18 +580,19 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct) S[ct] = X::mma(yf[ct], zw[p], S[ct]);
                 }
+                if constexpr (OUT && EARLY) put_state(std::integral_constant<int, NS>{}, buf1);
             }
             if (gates && ci + 1 < count) form_gates(lin_log2(gn, n, time_of(next, l), rev));
             __syncthreads();
             if (gates) put_gates();
             put_tiles();
-            if constexpr (OUT && !O) put_state(std::integral_constant<int, NS>{});
+            if constexpr (OUT && !O && !EARLY) put_state(std::integral_constant<int, NS>{}, buf1);
             if constexpr (DG && O && HV > 1) {   // the halves of a step's dot
                 if (wave < 2) put_dot(wave, c, row_at(l, 1) / (int)sizeof(T) * 4, s.dot[wave][0][l] + s.dot[wave][1][l]);
             }
         };
-        // The waves that are done first with a chunk go first (1 % of the time of long runs).
-        if constexpr (MODE != kLinState && (MODE == kLinOut) == O) __builtin_amdgcn_s_setprio(3);
+        // The outputs' waves, which the others wait for, go first (3 % of the time of train steps).
+        if constexpr (OUT && O) __builtin_amdgcn_s_setprio(3);
         // Apart where its state has more parts: a branch in the loop would cost a tenth of its time.
         if (count > 0) chunk(0, std::integral_constant<bool, (N1 > NS)>{});
         for (int ci = 1; ci < count; ++ci) chunk(ci, std::false_type{});
