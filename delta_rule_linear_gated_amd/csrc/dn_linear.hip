@@ -233,23 +233,28 @@ size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 int blocks_of(int nd, int bf16) { return nd / lin_vb(nd, bf16 != 0); }
 
-// Parallel segments of the steps.  One run of all chunks reads every tensor once; s > 1
-// segments cost a pass over the two tensors of the state, the boundary states and two
-// launches, and pay while the device has idle compute units.  From 256 workgroups on
-// (one for each unit): one run (8 x 16 heads, 4096 steps: 137 us, 2 segments 215).
-// Below, segments of at least 4 chunks for up to four workgroups a unit, which the units
-// take in turn (32 heads, 32768 steps, backward: 1.10 ms, with 512 workgroups 1.29); while
-// even those leave units idle, of 2 chunks (4 heads, 1024 steps: 20 us, of 4 chunks 26,
-// one run 37; with 512 workgroups there already they cost more than they save: 4 x 16
-// heads, 1024 steps 45 us against 55).
+// Parallel segments of the steps.  One run of all chunks reads every tensor once and takes
+// a time that grows with the chunks alone while a compute unit has at most one workgroup;
+// segments fill the units, at the cost of a pass over the two tensors of the state, the
+// boundary states and two launches.  With w workgroups in one run, segments take
+// w / full of its time per chunk and `cost` chunks more (measured against one run at w from
+// 6 to 252, 8 to 256 chunks, d = 64 and 128; one run -> segments):
+//     bf16 outputs      w  8, 16 chunks 32 -> 22 us, 64: 35 -> 36, 192: 36 -> 65;
+//                       w 64, 256 chunks 409 -> 214 us, 128: 423 -> 414, 192: 467 -> 611
+//     bf16, gate's gradient  w 96, 16 chunks 97 -> 92 us; w 192, 256 chunks 1351 -> 1205, 224: 1370 -> 1425
+//     fp32 (matrix steps, not bytes, bound it)  w 192, 128 chunks 389 -> 387 us; with the
+//                       gate's gradient w 224, 64 chunks 468 -> 430
+// Segments are of at least 4 chunks, for up to four workgroups a unit, which the units take
+// in turn; while even those leave units idle, of 2 chunks (w 8, 16 chunks: 20 us against 26).
 LinPlan lin_plan(const LinProblem& pr, int nops, bool dots) {
     const int NT = ceil_div(pr.T, kLinC);
     const long wgs = (long)pr.B * pr.H * blocks_of(pr.dv, pr.bf16) * nops;
     constexpr long kUnits = 256;
+    const long full = pr.bf16 ? (dots ? 216 : 144) : (dots ? 256 : 208), cost = pr.bf16 ? (dots ? 6 : 9) : 4;
     long ns = 1;
-    if (!pr.no_scan && wgs > 0 && wgs < kUnits) {
+    if (!pr.no_scan && wgs > 0 && NT * (full - wgs) >= cost * full) {
         ns = std::min<long>(4 * kUnits / wgs, NT / 4);
-        if (NT >= 8 && ns * wgs < kUnits) ns = std::min<long>(kUnits / wgs, NT / 2);
+        if (ns * wgs < kUnits) ns = std::min<long>(kUnits / wgs, NT / 2);
         ns = std::max<long>(1, std::min<long>(ns, kLinMaxSeg));
     }
     LinPlan p;
