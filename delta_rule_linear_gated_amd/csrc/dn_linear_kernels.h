@@ -19,19 +19,19 @@
 // sequence of one step has a single P, whose rounding nothing averages), S is
 // rounded once for its product with x, which adds at most as much to an output's
 // error as the output's own rounding (two parts in the first chunk: a call of few steps
-// from a cached state has few outputs to average it over).  The state itself is held to fp32: its operand
-// z e^{..} enters as three bf16 parts (24 bits), since a state (hT, dh0) is an
-// fp32 output.  Where the gate's gradient is wanted, an fp32 sum of differences of
+// from a cached state has few outputs to average it over).  The state itself is held to
+// fp32: its operand z e^{..} enters as three bf16 parts (24 bits), since a state (hT, dh0)
+// is an fp32 output.  Where the gate's gradient is wanted, an fp32 sum of differences of
 // r . out, P and the state enter in three parts too, and P's diagonal, which is no part
 // of that gradient, is applied apart from the others.
 // fp32 I/O: every product on fp32 matrix-core steps.
 //
 // Measured (bf16, d = 128).  Forward, 8 x 16 heads, 4096 steps, one workgroup on a
-// compute unit: 150 us for 0.55 GB, 3.6 TB/s where a copy reaches 5.2; its matrix (30 %
-// busy), vector (36 %) and LDS (41 %) work overlap in part only.  Two workgroups on a
-// unit (32 heads, 32768 steps in 16 segments): 245 us for 1.1 GB, 4.4 TB/s, bound by the
-// memory.  Without any loads in the loop it takes a sixth less.  Blocks of 64 channels
-// of z: of 32, 219 us (x y^T is formed once for each block).
+// compute unit: 136 us for 0.55 GB, 4.0 TB/s where a copy reaches 5.2; its matrix (35 %
+// busy) and LDS (46 %) work overlap in part only.  Two workgroups on a unit (32 heads,
+// 32768 steps in 16 segments): 245 us for 1.1 GB, 4.6 TB/s, bound by the memory.  Blocks of
+// 64 channels of z: of 32, 219 us where these took 150 (x y^T is formed once for each block).
+// With the gate's gradient, two evaluations: 541 us for 1.4 GB; LDS 46 %, matrix 27 % busy.
 #pragma once
 
 #include <type_traits>

@@ -11,7 +11,7 @@
 // A workgroup takes one (b, h) and a block of state rows (16 a wave).  Everything is held
 // to fp32, since u is an fp32 output from which states are continued: fp32 matrix-core
 // steps for fp32 keys and queries; for bf16 ones bf16 steps that are as exact, on three
-// bf16 parts (24 bits) of the state, of keys scaled by channel gates  and two of
+// bf16 parts (24 bits) of the state, of keys scaled by channel gates and two of
 // queries scaled by them (o is rounded to bf16): a fifth of the fp32 steps' time,
 // a third with channel gates.
 // The state's operands come straight from its rows.  A wave keeps its
@@ -20,7 +20,7 @@
 // no LDS besides the node-by-node matrices.  The system is solved by 16-node blocks, the
 // diagonal ones inverted by substitution, one lane a column.
 //
-// Measured (bf16, d = 128): 64 x 16 heads, 16 nodes 18.6 us for 92 MB (4.9 TB/s where a
+// Measured (bf16, d = 128): 64 x 16 heads, 16 nodes 20 us for 92 MB (4.6 TB/s where a
 // copy reaches 5.2: bound by the state's bytes); 16 x 16 heads, 61 nodes with channel
 // gates 28.7 us for 49 MB: one workgroup on a compute unit, bound by its chain of phases
 // (loads, path sums, scaling, products, solution), the products a third of it.
@@ -484,7 +484,7 @@ template <typename T, int DK, int NP, int NW> hipError_t tree_launch_np(const Tr
 // Eight waves, 128 state rows, share the node-by-node products and the staged rows (64
 // rows a workgroup: 35.8 us against 34.1 at 64 x 16 heads, 16 nodes); at 16 nodes 64
 // registers then let all of a compute unit's workgroups of such a batch run at once
-// (34.1 -> 24.7 us; with the bf16 steps 18.6: 92 MB of inputs and outputs, 4.9 TB/s).
+// (34.1 -> 24.7 us; with the bf16 steps 20).
 template <typename T, int DK> hipError_t tree_launch_dk(const TreeArgs& a, hipStream_t s) {
     if (a.N <= 16) return tree_launch_np<T, DK, 16, 8>(a, s);
     if (a.N <= 32) return tree_launch_np<T, DK, 32, 8>(a, s);
