@@ -86,8 +86,10 @@ __host__ __device__ constexpr int lin_threads(int mode, bool bf16, int nv) {
     return mode == kLinState ? 256 : 256 + 256 * lin_halves(mode, bf16, nv);
 }
 // Waves a SIMD holds at once: the registers of fp32 rows and of the gate's gradient leave
-// room for few.
-__host__ __device__ constexpr int lin_waves(int mode, bool bf16) { return mode == kLinOut && bf16 ? 4 : 2; }
+// room for few, LDS at 128 x 64 channels for one workgroup.
+__host__ __device__ constexpr int lin_waves(int mode, bool bf16, int kd, int nv) {
+    return mode == kLinOut && bf16 && kd * nv < 128 * 4 ? 4 : 2;
+}
 typedef hipError_t (*LinLaunch)(const LinArgs& a, int nv, int mode, hipStream_t s);
 hipError_t lin_bf16_k32(const LinArgs&, int, int, hipStream_t);
 hipError_t lin_bf16_k64(const LinArgs&, int, int, hipStream_t);

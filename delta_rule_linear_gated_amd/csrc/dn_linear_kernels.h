@@ -15,23 +15,23 @@
 // of y.  Four waves form the outputs, 16 steps each; four more the state, so
 // that the two halves of a chunk's work, which only share the tiles, run side by side.
 //
-// Rounding (bf16 I/O): P enters its product with z as two bf16 parts (16 bits: a
-// sequence of one step has a single P, whose rounding nothing averages), S is
-// rounded once for its product with x, which adds at most as much to an output's
-// error as the output's own rounding (two parts in the first chunk: a call of few steps
-// from a cached state has few outputs to average it over).  The state itself is held to
-// fp32: its operand z e^{..} enters as three bf16 parts (24 bits), since a state (hT, dh0)
-// is an fp32 output.  Where the gate's gradient is wanted, an fp32 sum of differences of
-// r . out, P and the state enter in three parts too, and P's diagonal, which is no part
-// of that gradient, is applied apart from the others.
+// Rounding (bf16 I/O): P and S enter the products that form an output as two bf16 parts
+// each (what they leave is at most 2^-16 of a term, wherever in the run the chunk is), so
+// that an output's error is its own rounding.  With S as one part, rounded like the
+// outputs, their error was 1.1 to 1.4 roundings and differed with the split of the steps
+// (8 x 16 heads, 4096 ragged steps: 143 us against 163; 32 heads, 32768 steps, train step:
+// 1315 against 1525).  The state itself is held to fp32: its operand z e^{..} enters as
+// three bf16 parts (24 bits), since a state (hT, dh0) is an fp32 output.  Where the gate's
+// gradient is wanted, an fp32 sum of differences of r . out, P and S enter in three
+// parts too, and P's diagonal, which is no part of that gradient, is applied apart from
+// the others.
 // fp32 I/O: every product on fp32 matrix-core steps.
 //
-// Measured (bf16, d = 128).  Forward, 8 x 16 heads, 4096 steps, one workgroup on a
-// compute unit: 136 us for 0.55 GB, 4.0 TB/s where a copy reaches 5.2; its matrix (35 %
-// busy) and LDS (46 %) work overlap in part only.  Two workgroups on a unit (32 heads,
-// 32768 steps in 16 segments): 245 us for 1.1 GB, 4.6 TB/s, bound by the memory.  Blocks of
-// 64 channels of z: of 32, 219 us where these took 150 (x y^T is formed once for each block).
-// With the gate's gradient, two evaluations: 541 us for 1.4 GB; LDS 46 %, matrix 27 % busy.
+// Measured (bf16, d = 128, one workgroup on a compute unit), whole calls: prompts of 8 x 16
+// heads, up to 4096 steps, 163 us; 4 heads, 32768 steps in 64 segments, 85 us; train steps with
+// a gate per step at 8 x 16 heads, 4096 steps, 863 us; with a decay per head at 32 heads,
+// 32768 steps, 1520 us.  Blocks of 64 channels of z: of 32, x y^T is formed twice as often
+// (219 us where these took 150).
 #pragma once
 
 #include <type_traits>
@@ -95,16 +95,15 @@ template <typename T, int KD, int NV, int MODE> struct LinLds {
     static constexpr bool DG = MODE == kLinDots;
     static constexpr int VB = 16 * NV, E = 16 / sizeof(T), PAD = sizeof(T) == 2 ? 2 * E : E;
     static constexpr int LY = KD + PAD, LZ = VB + PAD, LS = KD + E;
-    static constexpr int NS = MODE == kLinState ? 0 : DG && sizeof(T) == 2 ? 3 : 1;   // parts of the state operand
-    static constexpr int N1 = MODE == kLinOut && sizeof(T) == 2 ? 2 : NS;             // of the first chunk's
+    static constexpr int NS = MODE == kLinState ? 0 : sizeof(T) == 2 ? DG ? 3 : 2 : 1;   // parts of the state operand
     T y[kLinC * LY];
     T z[kLinC * LZ];
     // The state operand.  bf16: double, so that the waves of the state, which are done before those
-    // of the outputs, write the next chunk's at once (the first chunk's parts take both buffers);
-    // with fp32 rows it is the state that the others wait for.
+    // of the outputs, write the next chunk's at once (one buffer would leave room for a second
+    // workgroup on a unit at d = 128, but took 180 us where two take 163, 8 x 16 heads, 4096 ragged
+    // steps); with fp32 rows it is the state that the others wait for.
     static constexpr bool TWO = sizeof(T) == 2 && MODE != kLinState;
     T s[TWO ? 2 * NS : NS > 0 ? NS : 1][NS > 0 ? VB * LS : 1];
-    static_assert(N1 <= (TWO ? 2 : 1) * NS, "the first chunk's parts fit the buffers");
     // R: G from the first step of the row's 16 (two floats); e^{G_63 - G};
     // e^{G_16w - G_j} of the rows j before 16 w, w = 1, 2, 3; e^{G_16w}; the chunk's factor
     float hi[kLinC], lo[kLinC], ew[kLinC], tab[3][kLinC], eref[4], etot;
@@ -150,13 +149,13 @@ __device__ __forceinline__ double of_lane(double x, int l) {
 }
 
 template <typename T, int KD, int NV, int MODE>
-__global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MODE, sizeof(T) == 2)) void lin_kernel(LinArgs a) {
+__global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MODE, sizeof(T) == 2, KD, NV)) void lin_kernel(LinArgs a) {
     constexpr bool OUT = MODE != kLinState, DG = MODE == kLinDots;
     constexpr int TH = lin_threads(MODE, sizeof(T) == 2, NV), HV = lin_halves(MODE, sizeof(T) == 2, NV);
     using X = LinT<T>;
     using Frag = typename X::Frag;
     using L = LinLds<T, KD, NV, MODE>;
-    constexpr int E = X::E, JS = X::JS, VB = 16 * NV, LY = L::LY, LZ = L::LZ, LS = L::LS, NS = L::NS, N1 = L::N1;
+    constexpr int E = X::E, JS = X::JS, VB = 16 * NV, LY = L::LY, LZ = L::LZ, LS = L::LS, NS = L::NS;
     constexpr int NVW = NV / HV;                             // output tiles of a wave
     constexpr int XF = KD / (4 * E);                         // fragments of an x row
     constexpr int WV = 4 / NV;                               // waves that share a state tile column
@@ -391,14 +390,12 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
                 put_gates();
             }
             put_tiles();
-            if constexpr (OUT && !O) put_state(std::integral_constant<int, N1>{}, 0);
+            if constexpr (OUT && !O) put_state(std::integral_constant<int, NS>{}, 0);
         }
-        auto chunk = [&](int ci, auto of_run) {
-            constexpr bool FIRST = decltype(of_run)::value;   // of the run
+        auto chunk = [&](int ci) {
             const int c = first + step * ci;
             const int next = ci + 1 < count ? c + step : c;   // after the last chunk: it again, unused
-            constexpr bool EARLY = L::TWO && !FIRST;   // the next state operand is written beside this one's reads
-            const int buf = L::TWO ? ci & 1 : 0, buf1 = L::TWO ? buf ^ 1 : 0;
+            const int buf = L::TWO ? ci & 1 : 0, buf1 = L::TWO ? buf ^ 1 : 0;   // TWO: the next operand is written beside this one's reads
             __syncthreads();
             const float gn = lin_gate(a, gp, n, time_of(next, l), rev);
             load(next);
@@ -408,11 +405,10 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
 #pragma unroll
                 for (int i = 0; i < NVW; ++i) acc[i] = zero4();
                 // ---- from earlier chunks
-                constexpr int NP1 = FIRST ? N1 : NS;
 #pragma unroll
                 for (int f = 0; f < XF; ++f)
 #pragma unroll
-                    for (int p = 0; p < NP1; ++p)
+                    for (int p = 0; p < NS; ++p)
 #pragma unroll
                         for (int i = 0; i < NVW; ++i) {   // consecutive steps: different accumulators
                             const int at = buf * NS * VB * LS + out_col(tile0 + i, m >> 2, m & 3) * LS + 4 * E * f + E * g;
@@ -580,22 +576,20 @@ __global__ __launch_bounds__(lin_threads(MODE, sizeof(T) == 2, NV), lin_waves(MO
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct) S[ct] = X::mma(yf[ct], zw[p], S[ct]);
                 }
-                if constexpr (OUT && EARLY) put_state(std::integral_constant<int, NS>{}, buf1);
+                if constexpr (OUT && L::TWO) put_state(std::integral_constant<int, NS>{}, buf1);
             }
             if (gates && ci + 1 < count) form_gates(lin_log2(gn, n, time_of(next, l), rev));
             __syncthreads();
             if (gates) put_gates();
             put_tiles();
-            if constexpr (OUT && !O && !EARLY) put_state(std::integral_constant<int, NS>{}, buf1);
+            if constexpr (OUT && !O && !L::TWO) put_state(std::integral_constant<int, NS>{}, buf1);
             if constexpr (DG && O && HV > 1) {   // the halves of a step's dot
                 if (wave < 2) put_dot(wave, c, row_at(l, 1) / (int)sizeof(T) * 4, s.dot[wave][0][l] + s.dot[wave][1][l]);
             }
         };
         // The outputs' waves, which the others wait for, go first (3 % of the time of train steps).
         if constexpr (OUT && O) __builtin_amdgcn_s_setprio(3);
-        // Apart where its state has more parts: a branch in the loop would cost a tenth of its time.
-        if (count > 0) chunk(0, std::integral_constant<bool, (N1 > NS)>{});
-        for (int ci = 1; ci < count; ++ci) chunk(ci, std::false_type{});
+        for (int ci = 0; ci < count; ++ci) chunk(ci);
 
         // ---- the last state, the segment's own state and factor
         if constexpr (!O) {

@@ -332,7 +332,8 @@ dn_status dn_chunk_phase_bwd(const dn_shape* shape, const void* q, const void* k
  *            zero): dq, dk, dv, dg (DN_GATE_SCALAR only, else NULL), dh0 (NULL = not
  *            wanted); nothing of the forward is kept
  *   ws     : >= dn_linear_workspace_bytes(shape, DN_PASS_FWD or DN_PASS_BWD)
- * States, running sums and gate gradients are held to fp32 for bf16 I/O too.  NaN or Inf in
+ * States, running sums and gate gradients are held to fp32 for bf16 I/O too; the factors of an
+ * output's terms to 16 bits, so that its error is its own rounding to bf16.  NaN or Inf in
  * a step may reach every step of its chunk of 64, as NaN.  Layouts,
  * validation and errors as for dn_chunk_fwd.
  */
