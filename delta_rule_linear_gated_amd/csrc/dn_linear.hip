@@ -46,6 +46,66 @@ template <int N> __global__ __launch_bounds__(256) void lin_join_kernel(LinArgs 
     }
 }
 
+// Sums over runs of steps: a thread owns steps ta .. ta + 3 of [lo, hi), bit i of cuts says
+// that a run starts at ta + i.  pre, suf: the run's values before each of its steps, and
+// from the step on; start, end: where the run begins and ends.  Values of one run reach no
+// other.  ACROSS: runs cross the waves (part: LDS, two entries a wave, used once), else a
+// run ends with its wave.
+struct Run {
+    double sum;
+    int cut;   // the cut that ends it (it starts from); -1: none so far
+};
+__device__ __forceinline__ Run joined(Run a, Run b) {   // a, then b beyond it
+    return a.cut < 0 ? Run{a.sum + b.sum, b.cut} : a;
+}
+template <bool ACROSS>
+__device__ __forceinline__ void run_sums(const double (&x)[4], unsigned cuts, int ta, int lo, int hi, Run* part,
+                                         double (&pre)[4], double (&suf)[4], int (&start)[4], int (&end)[4]) {
+    const int l = lane_id(), w = wave_id();
+    const Run none{0.0, -1};
+    auto back = [&](Run at) {   // from the steps behind the thread's to its first
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            suf[i] = x[i] + at.sum;
+            end[i] = at.cut < 0 ? hi : at.cut;
+            at = cuts >> i & 1 ? Run{0.0, ta + i} : Run{suf[i], at.cut};
+        }
+        return at;
+    };
+    auto ahead = [&](Run at) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (cuts >> i & 1) at = Run{0.0, ta + i};
+            pre[i] = at.sum;
+            start[i] = at.cut < 0 ? lo : at.cut;
+            at.sum += x[i];
+        }
+        return at;
+    };
+    Run b = back(none), f = ahead(none);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const Run y{__shfl_down(b.sum, d), __shfl_down(b.cut, d)}, z{__shfl_up(f.sum, d), __shfl_up(f.cut, d)};
+        if (l + d < 64) b = joined(b, y);
+        if (l >= d) f = joined(f, z);
+    }
+    Run rb = none, rf = none;   // of the waves behind and before this one
+    if constexpr (ACROSS) {
+        if (l == 0) part[2 * w] = b;
+        if (l == 63) part[2 * w + 1] = f;
+        __syncthreads();
+#pragma unroll
+        for (int u = 3; u >= 0; --u)
+            if (u > w) rb = joined(part[2 * u], rb);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (u < w) rf = joined(part[2 * u + 1], rf);
+    }
+    const Run nb{__shfl_down(b.sum, 1), __shfl_down(b.cut, 1)}, nf{__shfl_up(f.sum, 1), __shfl_up(f.cut, 1)};
+    back(l == 63 ? rb : joined(nb, rb));
+    ahead(l == 0 ? rf : joined(nf, rf));
+}
+
 // Gate gradient of the steps t0 .. t1 - 1 that one kept state covers:
 //     dg_t = B1 + sum_{t <= s < t1} (a_s - b_s),   B(t) = dg_t = e^{g_t} <S_{t - 1}, D_t>
 // (the pairs that straddle t), a_s = q_s . dq_s and b_s = v_s . dv_s (= k_s . dk_s),
@@ -55,6 +115,11 @@ template <int N> __global__ __launch_bounds__(256) void lin_join_kernel(LinArgs 
 // a stretch are known from the kept states, and what the sum misses at t0 is taken off
 // evenly along it; the pairs inside a chunk sum to zero over it, and what they sum to
 // is taken off evenly along the chunk.  Sums in 64 bits.  A thread owns four steps.
+// A step whose factor is below fp32's normal numbers (a reset) lets no pair through: its
+// dg is zero, and the sums, their ends and what is taken off stop on either side of it, so
+// that what is rounded in one document reaches no other's gradient.
+constexpr float kLinReset = -87.33655f;   // ln 2^-126
+
 __device__ __forceinline__ double block_sum(double x, double* part) {   // part: one slot a wave, used once
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
@@ -65,7 +130,8 @@ __device__ __forceinline__ double block_sum(double x, double* part) {   // part:
 __global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* h0, const float* s_snap,
                                                         const float* d_snap, const float* dhT, const float* dots1,
                                                         int n1, const float* dots2, int n2, float* dg) {
-    __shared__ double part[3][4];
+    __shared__ double part[2][4];
+    __shared__ Run runs[8];
     const int bh = blockIdx.x / a.nent, e = blockIdx.x % a.nent, tid = threadIdx.x;
     const int n = lin_len(a.lens, bh / a.H, a.T);
     const int len = a.snap * kLinC, t0 = e * len, t1 = min(t0 + len, n);
@@ -77,7 +143,8 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* 
     }
     // B at step t from the state before it and the cotangent from it on (NULL: zero)
     auto straddle = [&](const float* S, const float* D, int t, double* part) {
-        if (!S || !D) return 0.0;
+        const float gate = t < n ? a.g[row + t] : 0.f;
+        if (!S || !D || gate < kLinReset) return 0.0;
         double x = 0.0;
         constexpr int AHEAD = 8;   // pieces in flight (a state: 16 at most)
         for (int i0 = 4 * tid; i0 < (int)se; i0 += 1024 * AHEAD) {
@@ -94,7 +161,7 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* 
                     x += (double)u[i][0] * v[i][0] + (double)u[i][1] * v[i][1] + (double)u[i][2] * v[i][2] +
                          (double)u[i][3] * v[i][3];
         }
-        return block_sum(x, part) * (t < n ? (double)expf(a.g[row + t]) : 1.0);
+        return block_sum(x, part) * (double)expf(gate);
     };
     const float* sk = s_snap + (long)bh * (a.nent + 1) * se;
     const float* dk = d_snap + (long)bh * (a.nent + 1) * se;
@@ -105,56 +172,40 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* 
     const double B0 = straddle(e > 0 ? sk + e * se : h0 ? h0 + bh * se : nullptr, dk + (e > 0 ? e - 1 : a.nent) * se, t0,
                                part[1]);
     const long nt = (long)a.BH * a.T;
-    const int ta = t0 + 4 * tid, tb = min(ta + 4, t1);
-    double inter[4], pairs[4], off = 0.0;
+    const int ta = t0 + 4 * tid;
+    double x[4], pairs[4];
+    unsigned cuts = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        inter[i] = pairs[i] = 0.0;
-        if (ta + i >= tb) continue;
+        x[i] = pairs[i] = 0.0;
+        if (ta + i >= t1) continue;
+        if (ta + i > t0 && a.g[row + ta + i] < kLinReset) cuts |= 1u << i;
         for (int b = 0; b < n1; ++b) {
             const float* d = dots1 + b * nt + row + ta + i;
-            inter[i] += d[0];
+            x[i] += d[0];
             pairs[i] += (double)d[n1 * nt] - d[0];
         }
         for (int b = 0; b < n2; ++b) {
             const float* d = dots2 + b * nt + row + ta + i;
-            inter[i] -= d[0];
+            x[i] -= d[0];
             pairs[i] -= (double)d[n2 * nt] - d[0];
         }
-        off += pairs[i];
     }
+    double pre[4], suf[4];
+    int start[4], end[4];
+    const int wt = t0 + 256 * wave_id();   // steps of this wave: whole chunks
+    run_sums<false>(pairs, cuts | (ta < t1 && ta % kLinC == 0 ? 1u : 0u), ta, wt, min(wt + 256, t1), nullptr, pre, suf, start, end);
 #pragma unroll
-    for (int d = 1; d < kLinC / 4; d *= 2) off += __shfl_xor(off, d);   // the 16 threads of a chunk
-    const int c0 = t0 + (tid / (kLinC / 4)) * kLinC, live = min(c0 + kLinC, t1) - c0;
-    double own = 0.0;
+    for (int i = 0; i < 4; ++i)
+        if (ta + i < t1) x[i] += pairs[i] - (pre[i] + suf[i]) / (end[i] - start[i]);
+    run_sums<true>(x, cuts, ta, t0, t1, runs, pre, suf, start, end);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (ta + i < tb) inter[i] += pairs[i] - off / live;
-        own += inter[i];
-    }
-    // sums of the threads from each on: within the wave, then the waves behind it
-    double from = own;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const double y = __shfl_down(from, d);
-        if (lane_id() + d < 64) from += y;
-    }
-    if (lane_id() == 0) part[2][wave_id()] = from;
-    __syncthreads();
-    double all = 0.0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        all += part[2][u];
-        if (u > wave_id()) from += part[2][u];
-    }
-    const double slope = (B0 - (B1 + all)) / (t1 - t0);
-    double acc = B1 + from - own;
-#pragma unroll
-    for (int i = 3; i >= 0; --i) {
         const int t = ta + i;
-        if (t >= tb) continue;
-        acc += inter[i];
-        dg[row + t] = t == t0 ? (float)B0 : (float)(acc + slope * (t1 - t));
+        if (t >= t1) continue;
+        const double L = start[i] > t0 ? 0.0 : B0, R = end[i] < t1 ? 0.0 : B1;   // its run's ends
+        const double slope = (L - (R + pre[i] + suf[i])) / (end[i] - start[i]);
+        dg[row + t] = t == start[i] ? (float)L : (float)(R + suf[i] + slope * (end[i] - t));
     }
     for (int t = t1 + tid; t < tend; t += 256) dg[row + t] = 0.f;
 }

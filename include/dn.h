@@ -327,6 +327,8 @@ dn_status dn_chunk_phase_bwd(const dn_shape* shape, const void* q, const void* k
  *            dk, dv and dg are zero there
  *   g      : any value below -1000 acts as -1000 (a factor of zero: -inf resets the
  *            state); positive values grow the state and overflow as the recurrence does
+ *            (dg of a step whose factor is below 2^-126, g < -87.34, is zero, and no step's dg
+ *            depends on what lies beyond such a step)
  *   forward : q, k, v, g (NULL iff no gate), h0 (NULL = zero) -> o, hT (NULL = not wanted)
  *   backward: the vector-Jacobian products of L = <o, dout> + <hT, dhT> (dhT NULL =
  *            zero): dq, dk, dv, dg (DN_GATE_SCALAR only, else NULL), dh0 (NULL = not
