@@ -117,7 +117,9 @@ __device__ __forceinline__ void run_sums(const double (&x)[4], unsigned cuts, in
 // is taken off evenly along the chunk.  Sums in 64 bits.  A thread owns four steps.
 // A step whose factor is below fp32's normal numbers (a reset) lets no pair through: its
 // dg is zero, and the sums, their ends and what is taken off stop on either side of it, so
-// that what is rounded in one document reaches no other's gradient.
+// that what is rounded in one document reaches no other's gradient.  NaN or Inf in a step
+// of q, do or k, v reaches what lies before or behind it only: where a run's whole sum is not
+// finite, each step takes the sum to whichever end is.
 constexpr float kLinReset = -87.33655f;   // ln 2^-126
 
 __device__ __forceinline__ double block_sum(double x, double* part) {   // part: one slot a wave, used once
@@ -205,7 +207,12 @@ __global__ __launch_bounds__(256) void lin_dgate_kernel(LinArgs a, const float* 
         if (t >= t1) continue;
         const double L = start[i] > t0 ? 0.0 : B0, R = end[i] < t1 ? 0.0 : B1;   // its run's ends
         const double slope = (L - (R + pre[i] + suf[i])) / (end[i] - start[i]);
-        dg[row + t] = t == start[i] ? (float)L : (float)(R + suf[i] + slope * (end[i] - t));
+        double x = R + suf[i];
+        if (isfinite(slope))
+            x += slope * (end[i] - t);
+        else if (!isfinite(x))   // NaN or Inf in some step of the run: in one of its ends' sums only, on this side of it
+            x = L - pre[i];
+        dg[row + t] = t == start[i] ? (float)L : (float)x;
     }
     for (int t = t1 + tid; t < tend; t += 256) dg[row + t] = 0.f;
 }

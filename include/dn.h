@@ -336,8 +336,9 @@ dn_status dn_chunk_phase_bwd(const dn_shape* shape, const void* q, const void* k
  *   ws     : >= dn_linear_workspace_bytes(shape, DN_PASS_FWD or DN_PASS_BWD)
  * States, running sums and gate gradients are held to fp32 for bf16 I/O too; the factors of an
  * output's terms to 16 bits, so that its error is its own rounding to bf16.  NaN or Inf in
- * a step may reach every step of its chunk of 64, as NaN.  Layouts,
- * validation and errors as for dn_chunk_fwd.
+ * a step may reach every step of its chunk of 64, as NaN, and else only what the formulas
+ * let it reach: from k or v the o, dq and dg of later steps, hT too, from q or dout the dk, dv
+ * and dg of earlier ones, dh0 too.  Layouts, validation and errors as for dn_chunk_fwd.
  */
 size_t dn_linear_workspace_bytes(const dn_shape* shape, int pass);
 dn_status dn_linear_fwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* g,
