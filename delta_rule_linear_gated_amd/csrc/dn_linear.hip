@@ -13,6 +13,7 @@ namespace dn {
 namespace {
 
 constexpr int kLinMaxSeg = 64;   // parallel segments of a sequence
+constexpr int kLinUnits = 256;   // compute units
 
 // Boundary states of the parallel segments: entry s of snap holds segment s's own
 // contribution (from a zero state) and gets the state the segment starts from,
@@ -291,35 +292,60 @@ size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 int blocks_of(int nd, int bf16) { return nd / lin_vb(nd, bf16 != 0); }
 
+// Time of a launch of segments of len chunks, in chunks of one workgroup alone on its unit:
+// `per` workgroups for each (b, h) and segment, whose units (bh, segment) go to the 8 XCDs in
+// turn, so that the fullest XCD counts; two workgroups on a unit take 1.7 of one's time, and each
+// begins with a chunk's worth of loads.  The pass that makes the segments' own states (`state`
+// workgroups in all) takes half as much for a chunk and fits a unit more often.
+float segments_time(long units, int per, int len, long state) {
+    const long k = ((units + kXcds - 1) / kXcds * per + kLinUnits / kXcds - 1) / (kLinUnits / kXcds);
+    const float outs = 1.7f * (float)(k / 2) + (float)(k % 2), states = std::max(1.f, (float)state / (2 * kLinUnits));
+    return (len + 1) * (outs + 0.5f * states);
+}
+
 // Parallel segments of the steps.  One run of all chunks reads every tensor once and takes
 // a time that grows with the chunks alone while a compute unit has at most one workgroup;
 // segments fill the units, at the cost of a pass over the two tensors of the state, the
 // boundary states and two launches.  With w workgroups in one run, segments take
-// w / full of its time per chunk and `cost` chunks more (measured against one run at w from
-// 6 to 252, 8 to 256 chunks, d = 64 and 128; one run -> segments):
-//     bf16 outputs      w  8, 16 chunks 32 -> 22 us, 64: 35 -> 36, 192: 36 -> 65;
-//                       w 64, 256 chunks 409 -> 214 us, 128: 423 -> 414, 192: 467 -> 611
-//     bf16, gate's gradient  w 96, 16 chunks 97 -> 92 us; w 192, 256 chunks 1351 -> 1205, 224: 1370 -> 1425
-//     fp32 (matrix steps, not bytes, bound it)  w 192, 128 chunks 389 -> 387 us; with the
-//                       gate's gradient w 224, 64 chunks 468 -> 430
-// Segments are of at least 4 chunks, for up to four workgroups a unit, which the units take
-// in turn; while even those leave units idle, of 2 chunks (w 8, 16 chunks: 20 us against 26).
+// w / full of its time per chunk and `cost` chunks more.  Measured (one run -> the best of 2 to 64
+// segments, d = 128):
+//     bf16 outputs, NT 256      w  96 503 -> 339 us, 128: 500 -> 453; 192 (NT 512): 1012 -> 1154
+//     bf16, gate's gradient, NT 256  w  96 1360 -> 630 us, 200: 1442 -> 1303
+//     fp32 outputs, NT 256      w  96 1223 -> 615 us, 128: 1230 -> 804; gate's gradient, w 240: 3045 -> 2785
+// Where the fullest XCD has workgroups for two turns of its units although all together would
+// fit in one (fp32, 20 heads x 12 workgroups: 2430 us in one run, 1454 in 5 segments), w counts
+// half.  The number of segments is then the fastest by segments_time, of the lengths that there
+// are after rounding (with the gate's gradient to whole numbers of kept states): over 2 to 64
+// segments of 6 to 240 workgroups, 16 to 256 chunks, d = 32, 64 and 128, within 2 % of the best
+// on average (filling four workgroups a unit: 3.5 %).  Segments are of at least 4 chunks, or,
+// while those leave units idle, of 2.
 LinPlan lin_plan(const LinProblem& pr, int nops, bool dots) {
-    const int NT = ceil_div(pr.T, kLinC);
-    const long wgs = (long)pr.B * pr.H * blocks_of(pr.dv, pr.bf16) * nops;
-    constexpr long kUnits = 256;
+    const int NT = ceil_div(pr.T, kLinC), nblk = blocks_of(pr.dv, pr.bf16);
+    const long BH = (long)pr.B * pr.H, wgs = BH * nblk * nops;
     const long full = pr.bf16 ? (dots ? 216 : 144) : (dots ? 256 : 208), cost = pr.bf16 ? (dots ? 6 : 9) : 4;
-    long ns = 1;
-    if (!pr.no_scan && wgs > 0 && NT * (full - wgs) >= cost * full) {
-        ns = std::min<long>(4 * kUnits / wgs, NT / 4);
-        if (ns * wgs < kUnits) ns = std::min<long>(kUnits / wgs, NT / 2);
-        ns = std::max<long>(1, std::min<long>(ns, kLinMaxSeg));
-    }
+    const long fullest = (BH + kXcds - 1) / kXcds * kXcds * nblk * nops;
+    const long w = wgs <= kLinUnits && fullest > kLinUnits ? wgs / 2 : wgs;
+    // kept states of a segment of len chunks: at equal distances, at most kLinSnap
+    auto distance = [&](int len) { return ceil_div(len, ceil_div(len, kLinSnap)); };
     LinPlan p;
-    p.seg_len = NT > 0 ? ceil_div(NT, (int)ns) : 1;
-    if (dots && ns > 1 && p.seg_len > kLinSnap) p.seg_len = ceil_div(p.seg_len, kLinSnap) * kLinSnap;
-    p.nseg = NT > 0 ? ceil_div(NT, p.seg_len) : 1;
-    p.snap = dots ? (p.nseg > 1 && p.seg_len < kLinSnap ? p.seg_len : kLinSnap) : p.seg_len;
+    p.nseg = 1;
+    p.seg_len = std::max(NT, 1);
+    p.snap = dots ? kLinSnap : p.seg_len;
+    if (!pr.no_scan && wgs > 0 && NT * (full - w) >= cost * full) {
+        const int most = (int)std::min<long>({kLinMaxSeg, NT / 2, 8 * kLinUnits / wgs});
+        float best = 0.f;
+        for (int ns = 2; ns <= most; ++ns) {
+            int len = ceil_div(NT, ns);
+            const int snap = dots ? distance(len) : len;
+            len = ceil_div(len, snap) * snap;
+            const int nseg = ceil_div(NT, len);
+            if (nseg < 2 || (len < 4 && nseg * wgs > kLinUnits)) continue;
+            const float time = segments_time(BH * nseg, nblk * nops, len, BH * (nseg - 1) * nblk * (nops > 1 ? 2 : 1));
+            if (p.nseg > 1 && time >= best) continue;
+            best = time;
+            p.nseg = nseg, p.seg_len = len, p.snap = snap;
+        }
+    }
     p.nent = NT > 0 ? ceil_div(NT, p.snap) : 1;
     return p;
 }
