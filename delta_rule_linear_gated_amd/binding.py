@@ -36,7 +36,7 @@ EXPORTS = ("dn_states_bytes", "dn_states_layout", "dn_workspace_bytes", "dn_work
            "dn_chunk_fwd_noalloc", "dn_chunk_bwd", "dn_recurrent_fwd", "dn_recurrent_phase_fwd", "dn_phase_states_bytes",
            "dn_phase_workspace_bytes", "dn_chunk_phase_fwd", "dn_chunk_phase_bwd", "dn_linear_workspace_bytes",
            "dn_linear_fwd", "dn_linear_bwd", "dn_linear_recurrent_fwd", "dn_tree_fwd", "dn_tree_commit",
-           "dn_status_string", "dn_last_error",
+           "dn_tree_commit_counts", "dn_status_string", "dn_last_error",
            "dn_profile_enable", "dn_profile_collect")
 
 
@@ -104,6 +104,8 @@ def lib():
     L.dn_tree_fwd.restype = i32
     L.dn_tree_commit.argtypes = [sp] + [vp] * 7
     L.dn_tree_commit.restype = i32
+    L.dn_tree_commit_counts.argtypes = [sp] + [vp] * 8
+    L.dn_tree_commit_counts.restype = i32
     L.dn_status_string.argtypes = [i32]
     L.dn_status_string.restype = ctypes.c_char_p
     L.dn_last_error.argtypes = []
@@ -294,6 +296,12 @@ def dn_tree_commit(shape, k, u, g, parent, accept, state, stream=None) -> int:
     """Raw call; returns the dn_status (no exception)."""
     return lib().dn_tree_commit(ctypes.byref(shape), _ptr(k), _ptr(u), _ptr(g), _ptr(parent), _ptr(accept), _ptr(state),
                                 _stream(stream))
+
+
+def dn_tree_commit_counts(shape, k, u, g, parent, counts, accept, state, stream=None) -> int:
+    """Raw call; returns the dn_status (no exception)."""
+    return lib().dn_tree_commit_counts(ctypes.byref(shape), _ptr(k), _ptr(u), _ptr(g), _ptr(parent), _ptr(counts),
+                                       _ptr(accept), _ptr(state), _stream(stream))
 
 
 # ------------------------------------------------------------------ convenience
@@ -688,9 +696,10 @@ def tree_fwd(q, k, v, beta, g, parent, state, counts=None, want_u=True, stream=N
     return o, u
 
 
-def tree_commit(k, u, g, parent, accept, state, stream=None):
+def tree_commit(k, u, g, parent, accept, state, stream=None, counts=None):
     """Move ``state`` (fp32 [B,H,dv,dk], in place) along the path that ends at node ``accept`` (int32 [B];
-    -1 accepts nothing) of the tree that tree_fwd read; ``u`` is what it returned.  Returns state."""
+    -1, or a node from ``counts`` on, accepts nothing) of the tree that tree_fwd read; ``u`` is what it
+    returned, ``counts`` (int32 [B]) what it was given.  Returns state."""
     if k.dim() != 4 or u.dim() != 4:
         raise ValueError(f"k must be [B,H,N,dk] and u [B,H,N,dv], got shapes {tuple(k.shape)}, {tuple(u.shape)}")
     B, H, N, dk = k.shape
@@ -700,7 +709,8 @@ def tree_commit(k, u, g, parent, accept, state, stream=None):
     kind, gshape = _linear_gate(g, B, H, N, dk)
     f32, i32 = torch.float32, torch.int32
     _check_tensors(k.device, ("k", k, k.dtype, k.shape), ("u", u, f32, (B, H, N, dv)), ("g", g, f32, gshape),
-                   ("parent", parent, i32, (B, N)), ("accept", accept, i32, (B,)), ("state", state, f32, (B, H, dv, dk)))
+                   ("parent", parent, i32, (B, N)), ("counts", counts, i32, (B,)), ("accept", accept, i32, (B,)),
+                   ("state", state, f32, (B, H, dv, dk)))
     sh = make_shape(B, H, N, dk, dv, 64, k.dtype, kind)
-    _check(dn_tree_commit(sh, k, u, g, parent, accept, state, stream))
+    _check(dn_tree_commit_counts(sh, k, u, g, parent, counts, accept, state, stream))
     return state

@@ -931,6 +931,12 @@ dn_status dn_tree_fwd(const dn_shape* shape, const void* q, const void* k, const
 
 dn_status dn_tree_commit(const dn_shape* shape, const void* k, const float* u, const float* g, const int32_t* parent,
                          const int32_t* accept, float* state, void* stream) {
+    return dn_tree_commit_counts(shape, k, u, g, parent, nullptr, accept, state, stream);
+}
+
+dn_status dn_tree_commit_counts(const dn_shape* shape, const void* k, const float* u, const float* g,
+                                const int32_t* parent, const int32_t* counts, const int32_t* accept, float* state,
+                                void* stream) {
     g_err[0] = '\0';
     dn::TreeArgs a;
     Dims d;
@@ -948,12 +954,14 @@ dn_status dn_tree_commit(const dn_shape* shape, const void* k, const float* u, c
                           {"u", u, nu, false},
                           {"g", g, ng, false},
                           {"parent", parent, np, false},
+                          {"counts", counts, na, false},
                           {"accept", accept, na, false},
                           {"state", state, ns, true}}));
     a.k = k;
     a.u = const_cast<float*>(u);
     a.g = g;
     a.parent = parent;
+    a.counts = counts;
     a.accept = accept;
     a.state = state;
     const hipError_t e = dn::launch_tree_commit(a, static_cast<hipStream_t>(stream));

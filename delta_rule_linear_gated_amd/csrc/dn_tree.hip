@@ -28,7 +28,8 @@ __global__ __launch_bounds__(kCommitThreads) void tree_commit_kernel(TreeArgs a)
     head_and_block(nblk, a.B * a.H, bh, blk);
     const int b = bh / a.H, h = bh % a.H, N = a.N, tid = threadIdx.x, l = lane_id(), j = l & 15;
     const int at = __builtin_amdgcn_readfirstlane(a.accept[b]);
-    if (at < 0 || at >= N) return;
+    const int cnt = a.counts ? __builtin_amdgcn_readfirstlane(a.counts[b]) : N;
+    if (at < 0 || at >= min(cnt, N)) return;
     const long rows = (long)bh * N;
 
     // ---- the tree's loads, then state rows r = 16 i + tid / 16 of the block

@@ -369,6 +369,10 @@ dn_status dn_linear_recurrent_fwd(const dn_shape* shape, const void* q, const vo
  *   dn_tree_commit moves `state` along the path that ends at node accept[b] (in place),
  *                  from the u of dn_tree_fwd; any accept[b] outside 0 .. T - 1 (e.g. -1)
  *                  leaves that batch element's states as they are, unread.
+ *   dn_tree_commit_counts does the same for trees of fewer nodes, by the counts of dn_tree_fwd
+ *                  (NULL: T): an accept[b] from counts[b] on accepts nothing either.
+ *                  dn_tree_commit takes all T nodes for the tree's; one from counts[b] on is
+ *                  then applied as it stands, its padding's key and gate too.
  *   shape  : T = nodes per batch element, 0 .. 64; dk in {16, 32, 64, 128}; dv a positive
  *            multiple of 16; dtype (q, k, v, o); gate: any dn_gate (g [B][H][T],
  *            [B][H][T][dk] or [H]); flags: DN_FLAG_KACZMARZ (dn_tree_fwd with beta, which
@@ -388,6 +392,9 @@ dn_status dn_tree_fwd(const dn_shape* shape, const void* q, const void* k, const
                       float* u, void* stream);
 dn_status dn_tree_commit(const dn_shape* shape, const void* k, const float* u, const float* g, const int32_t* parent,
                          const int32_t* accept, float* state, void* stream);
+dn_status dn_tree_commit_counts(const dn_shape* shape, const void* k, const float* u, const float* g,
+                                const int32_t* parent, const int32_t* counts, const int32_t* accept, float* state,
+                                void* stream);
 
 /* Static description of a status code. */
 const char* dn_status_string(dn_status status);
