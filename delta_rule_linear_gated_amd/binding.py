@@ -574,7 +574,7 @@ def _linear_gate(g, B, H, T, dk=None):
     return DN_GATE_SCALAR, (B, H, T)
 
 
-def _linear_args(q, k, v, g, no_scan, *more):
+def _linear_args(q, k, v, g, no_scan, ws, *more):
     """Shape descriptor of checked tensors; ``more``: (name, tensor, "v" | "state" | "lens")."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError(f"q must be [B,H,T,dk] and v [B,H,T,dv], got shapes {tuple(q.shape)}, {tuple(v.shape)}")
@@ -583,6 +583,8 @@ def _linear_args(q, k, v, g, no_scan, *more):
     io = q.dtype
     if io not in _IO_DTYPES:
         raise ValueError(f"q must be float32 or bfloat16, got {io}")
+    if ws is not None and not (ws.is_contiguous() and ws.device == q.device):   # its size: the C ABI
+        raise ValueError(f"ws must be contiguous and on {q.device}")
     kind, gshape = _linear_gate(g, B, H, T)
     kinds = {"v": (io, (B, H, T, dv)), "state": (torch.float32, (B, H, dv, dk)), "lens": (torch.int32, (B,))}
     _check_tensors(q.device, ("q", q, io, qs), ("k", k, io, qs), ("v", v, *kinds["v"]), ("g", g, torch.float32, gshape),
@@ -605,7 +607,7 @@ def _linear_ws(shape, pass_, ws, device):
     n = dn_linear_workspace_bytes(shape, pass_)
     if ws is None and n:
         ws = torch.empty(n, dtype=torch.uint8, device=device)
-    return ws, (0 if ws is None else ws.numel())
+    return ws, (0 if ws is None else ws.numel() * ws.element_size())
 
 
 def linear_fwd(q, k, v, g=None, h0=None, lens=None, want_hT=True, ws=None, stream=None, no_scan=False):
@@ -613,7 +615,7 @@ def linear_fwd(q, k, v, g=None, h0=None, lens=None, want_hT=True, ws=None, strea
     o_t = S_t q_t.  ``g``: None, [H] (a constant log-decay per head) or [B,H,T] (per step); ``lens``:
     int32 [B], the steps of each batch element (o is zero past them, hT the state after them).
     Returns (o, hT or None)."""
-    sh = _linear_args(q, k, v, g, no_scan, ("h0", h0, "state"), ("lens", lens, "lens"))
+    sh = _linear_args(q, k, v, g, no_scan, ws, ("h0", h0, "state"), ("lens", lens, "lens"))
     with _allocating(stream):
         o = torch.empty_like(v)
         hT = torch.empty(sh.B, sh.H, sh.dv, sh.dk, dtype=torch.float32, device=q.device) if want_hT else None
@@ -624,7 +626,7 @@ def linear_fwd(q, k, v, g=None, h0=None, lens=None, want_hT=True, ws=None, strea
 
 def linear_bwd(q, k, v, g, h0, do, dhT=None, lens=None, want_dh0=True, ws=None, stream=None, no_scan=False):
     """Backward of linear_fwd.  Returns dict dq, dk, dv, dg (None unless g is per step), dh0 (or None)."""
-    sh = _linear_args(q, k, v, g, no_scan, ("h0", h0, "state"), ("do", do, "v"), ("dhT", dhT, "state"),
+    sh = _linear_args(q, k, v, g, no_scan, ws, ("h0", h0, "state"), ("do", do, "v"), ("dhT", dhT, "state"),
                       ("lens", lens, "lens"))
     with _allocating(stream):
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
@@ -638,7 +640,7 @@ def linear_bwd(q, k, v, g, h0, do, dhT=None, lens=None, want_dh0=True, ws=None, 
 def linear_recurrent_fwd(q, k, v, g, state, stream=None):
     """T recurrent steps of linear attention (decode); ``state`` (fp32 [B,H,dv,dk]) is updated in
     place.  ``g`` as for linear_fwd.  Returns o."""
-    sh = _linear_args(q, k, v, g, False, ("state", state, "state"))
+    sh = _linear_args(q, k, v, g, False, None, ("state", state, "state"))
     with _allocating(stream):
         o = torch.empty_like(v)
     _check(dn_linear_recurrent_fwd(sh, q, k, v, g, state, o, stream))
