@@ -326,7 +326,8 @@ dn_status dn_chunk_phase_bwd(const dn_shape* shape, const void* q, const void* k
  *            inputs hold there is not used, hT is the state after the last step, o, dq,
  *            dk, dv and dg are zero there
  *   g      : any value below -1000 acts as -1000 (a factor of zero: -inf resets the
- *            state); positive values grow the state and overflow as the recurrence does
+ *            state); positive values grow the state; where they sum to more than 88 within a
+ *            chunk of 64 steps, results overflow (Inf or NaN) whatever the state holds
  *            (dg of a step whose factor is below 2^-126, g < -87.34, is zero, and no step's dg
  *            depends on what lies beyond such a step)
  *   forward : q, k, v, g (NULL iff no gate), h0 (NULL = zero) -> o, hT (NULL = not wanted)
@@ -383,8 +384,10 @@ dn_status dn_linear_recurrent_fwd(const dn_shape* shape, const void* q, const vo
  *            counts int32 [B] or NULL: the nodes of each batch element (clamped to
  *            0 .. T), o and u are zero from there on; accept int32 [B]; state fp32
  *            [B][H][dv][dk].  Gates below -1000 act as -1000 (a factor of zero).
- *   outputs: o (io) and u fp32, both [B][H][T][dv] (u NULL = not wanted); fp32 arithmetic.
- *            NaN or Inf in a node may reach every node of its tree
+ *   outputs: o (io) and u fp32, both [B][H][T][dv] (u NULL = not wanted).  Held to fp32; with bf16
+ *            I/O and a gate per channel the scaled queries, which only o takes, to 16 bits.
+ *            NaN or Inf in a node may reach every node of its tree; so may positive gates that
+ *            sum to more than 88 on a path
  * Validation and errors as for dn_recurrent_fwd; no workspace.
  */
 dn_status dn_tree_fwd(const dn_shape* shape, const void* q, const void* k, const void* v, const float* beta,
