@@ -11,19 +11,20 @@
 // A workgroup takes one (b, h) and a block of state rows (16 a wave).  Everything is held
 // to fp32, since u is an fp32 output from which states are continued: fp32 matrix-core
 // steps for fp32 keys and queries; for bf16 ones bf16 steps that are as exact, on three
-// bf16 parts (24 bits) of the state, of keys scaled by channel gates and two of
-// queries scaled by them (o is rounded to bf16): a fifth of the fp32 steps' time,
-// a third with channel gates.
+// bf16 parts (24 bits) of the state and of keys and queries scaled by channel gates: a
+// fifth of the fp32 steps' time, 0.4 of it with channel gates.
 // The state's operands come straight from its rows.  A wave keeps its
 // columns of u in accumulators from the first product to the last: accumulator row
 // 4 g + i is K slot g of step i of the next product, so the chain X -> R -> u -> o needs
 // no LDS besides the node-by-node matrices.  The system is solved by 16-node blocks, the
 // diagonal ones inverted by substitution, one lane a column.
 //
-// Measured (bf16, d = 128): 64 x 16 heads, 16 nodes 20 us for 92 MB (4.6 TB/s where a
-// copy reaches 5.2: bound by the state's bytes); 16 x 16 heads, 61 nodes with channel
-// gates 28.7 us for 49 MB: one workgroup on a compute unit, bound by its chain of phases
-// (loads, path sums, scaling, products, solution), the products a third of it.
+// Measured (bf16, d = 128, whole calls): 64 x 16 heads, 16 nodes 23 us for 92 MB (the kernel
+// 20: 4.6 TB/s where a copy reaches 5.2, bound by the state's bytes; fp32 29); 16 x 16 heads, 61
+// nodes with channel gates 31.5 us for 49 MB (fp32 35): one workgroup on a compute unit, bound
+// by its chain of phases (loads, path sums, scaling, products, solution), the products a third
+// of it.  With a path's |Gam| beyond 60, where each node's path is walked by a wave: the same trees
+// 50 us, chains of 61 nodes 142.
 #pragma once
 
 #include <type_traits>
@@ -82,17 +83,20 @@ template <int NP> __device__ __forceinline__ unsigned long long tree_path(int p,
 }
 
 template <typename T, int DK, int NP, bool VEC> struct TreeLds {
-    static constexpr bool BF = sizeof(T) == 2;
+    static constexpr bool BF = sizeof(T) == 2, PARTS = BF && VEC;
     static constexpr int DP = BF && DK < 32 ? 32 : DK;     // one bf16 step at least, zeros behind DK
     static constexpr int LD = DK + 4, LN = NP + 4;
-    // k and q; per channel gate: times e^{Gam}.  bf16 parts or fp32.
-    static constexpr int KP = !BF ? 1 : VEC ? 3 : 1, QP = !BF ? 1 : VEC ? 2 : 1;
+    static constexpr int KP = PARTS ? 3 : 1;               // of k and q; per channel gate: times e^{Gam}.  bf16 parts or fp32
     static constexpr int LX = BF ? DP + (VEC ? 8 : 16) : LD;
     typedef typename std::conditional<BF, bf16, float>::type X;
     __align__(16) X kx[KP][NP][LX];
-    X qx[QP][NP][LX];
+    static constexpr int ROOM = (int)(2 * sizeof(float) * LN - sizeof(X) * KP * LX) * NP;
+    char room[PARTS && ROOM > 0 ? ROOM : 16];   // of A and P behind kx (see sys)
+    X qx[KP][NP][LX];
     float km[VEC ? NP : 1][VEC ? LD : 1];   // k e^{-Gam}, or the gates where that would overflow
-    float A[NP][LN], P[NP][LN];          // the system's matrix (its diagonal blocks inverted in place), the outputs'
+    // The system's matrix A (its diagonal blocks inverted in place) and the outputs' P.  PARTS: where kx
+    // lies, which is read no more when they are written (the third part of q has its room from that).
+    float sys[PARTS ? 1 : 2][PARTS ? 1 : NP][PARTS ? 1 : LN];
     unsigned long long on[NP];
     double gam[NP];                      // Gam of a gate per step or head
     float beta[NP];
@@ -103,10 +107,13 @@ template <typename T, int DK, int NP, bool VEC> struct TreeLds {
 template <typename T, int DK, int NP, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel(TreeArgs a) {
     using L = TreeLds<T, DK, NP, VEC>;
-    constexpr bool BF = L::BF, PARTS = BF && VEC;
-    constexpr int KP = L::KP, QP = L::QP;
+    constexpr bool BF = L::BF, PARTS = L::PARTS;
+    constexpr int KP = L::KP;
     constexpr int TH = 64 * NW, NT = NP / 16, F = DK / 16, Q = DK / 4;
     __shared__ __align__(16) L s;
+    typedef float Sys[NP][L::LN];
+    Sys* sys = reinterpret_cast<Sys*>(PARTS ? static_cast<void*>(s.kx) : static_cast<void*>(s.sys));
+    Sys &A = sys[0], &P = sys[1];
     const int nblk = (a.dv / 16 + NW - 1) / NW;
     const int BH = a.B * a.H;
     int bh, blk;   // blocks of a head: ids equal mod 8 (one XCD, whose L2 holds its rows)
@@ -259,7 +266,7 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
 #pragma unroll
         for (int r = 0; r < KP; ++r) put(s.kx[r], kk);
 #pragma unroll
-        for (int r = 0; r < QP; ++r) put(s.qx[r], qq);
+        for (int r = 0; r < KP; ++r) put(s.qx[r], qq);
     }
     __syncthreads();
 
@@ -267,9 +274,7 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
     f32x4 X[NT], o[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) X[t] = zero4(), o[t] = zero4();
-    // Parts r of one factor and q of the other are multiplied for r + q below the number of
-    // parts that the result needs: three for u, two for outputs of per-channel gates (the
-    // scaled queries are two parts), three where the queries are exact.
+    // Parts r of one factor and q of the other are multiplied for r + q < 3.
     if (active) {
         if constexpr (BF) {
 #pragma unroll
@@ -279,10 +284,10 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
 #pragma unroll
-                    for (int r = 0; r < QP; ++r) {
+                    for (int r = 0; r < KP; ++r) {
                         const bf16x8 qf = *reinterpret_cast<const bf16x8*>(&s.qx[r][16 * t + m][32 * f + 8 * g]);
 #pragma unroll
-                        for (int q = 0; q < (PARTS ? 2 : 3) - r; ++q)
+                        for (int q = 0; q < 3 - r; ++q)
                             o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf, sp[q], o[t], 0, 0, 0);
                     }
                     if (!delta) continue;
@@ -317,13 +322,19 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
         }
 
     // ---- node by node: A = beta (k_n . e^{..} k_m) for m before n on its path, P with q_n, m = n too
-    constexpr int TRI = NT * (NT + 1) / 2;
+    constexpr int TRI = NT * (NT + 1) / 2, TILES = (2 * TRI + NW - 1) / NW;   // of both; of a wave
     if (!deep) {
-        for (int id = wave; id < 2 * TRI; id += NW) {
+        f32x4 pair[TILES];
+        int row[TILES], col[TILES];   // tiles of nodes
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+            const int id = wave + NW * j;
             const bool isP = id < TRI;
-            if (!isP && !delta) break;
             int tn = 0, tm = isP ? id : id - TRI;
             while (tm > tn) tm -= ++tn;
+            row[j] = tn, col[j] = tm;
+            pair[j] = zero4();
+            if (id >= (delta ? 2 : 1) * TRI) continue;
             f32x4 acc = zero4();
             if constexpr (BF) {
 #pragma unroll
@@ -338,22 +349,13 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
                     } else {
                         mp[0] = *reinterpret_cast<const bf16x8*>(&s.kx[0][16 * tm + m][32 * f + 8 * g]);
                     }
-                    if (isP) {
 #pragma unroll
-                        for (int r = 0; r < QP; ++r) {
-                            const bf16x8 nf = *reinterpret_cast<const bf16x8*>(&s.qx[r][16 * tn + m][32 * f + 8 * g]);
+                    for (int r = 0; r < KP; ++r) {
+                        const bf16x8 nf = *reinterpret_cast<const bf16x8*>(
+                            isP ? &s.qx[r][16 * tn + m][32 * f + 8 * g] : &s.kx[r][16 * tn + m][32 * f + 8 * g]);
 #pragma unroll
-                            for (int q = 0; q < QP - r; ++q)
-                                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf, mp[q], acc, 0, 0, 0);
-                        }
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < KP; ++r) {
-                            const bf16x8 nf = *reinterpret_cast<const bf16x8*>(&s.kx[r][16 * tn + m][32 * f + 8 * g]);
-#pragma unroll
-                            for (int q = 0; q < KP - r; ++q)
-                                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf, mp[q], acc, 0, 0, 0);
-                        }
+                        for (int q = 0; q < KP - r; ++q)
+                            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(nf, mp[q], acc, 0, 0, 0);
                     }
                 }
             } else {
@@ -364,21 +366,30 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
                     acc = tree_mma(*reinterpret_cast<const f32x4*>(nr + 16 * f + 4 * g),
                                    *reinterpret_cast<const f32x4*>(mr + 16 * f + 4 * g), acc);
             }
-            const int mm = 16 * tm + m;
+            pair[j] = acc;
+        }
+        if constexpr (PARTS) __syncthreads();   // kx is read no more
+#pragma unroll
+        for (int j = 0; j < TILES; ++j) {
+            const int id = wave + NW * j;
+            const bool isP = id < TRI;
+            if (id >= (delta ? 2 : 1) * TRI) continue;
+            const int mm = 16 * col[j] + m;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int n = 16 * tn + 4 * g + i;
+                const int n = 16 * row[j] + 4 * g + i;
                 const bool on = (s.on[n] >> mm & 1) && (isP || mm != n);
                 float w = 1.f;
                 if (!VEC) w = __builtin_amdgcn_exp2f((float)((s.gam[n] - s.gam[mm]) * 1.4426950408889634));
-                const float x = on ? acc[i] * w : 0.f;
-                if (isP) s.P[n][mm] = x;
-                else s.A[n][mm] = x * s.beta[n];
+                const float x = on ? pair[j][i] * w : 0.f;
+                if (isP) P[n][mm] = x;
+                else A[n][mm] = x * s.beta[n];
             }
         }
     } else if constexpr (VEC) {
         // Up each node's path with the decay of the nodes passed, a wave a node.
-        for (int id = tid; id < NP * NP; id += TH) s.A[id / NP][id % NP] = 0.f, s.P[id / NP][id % NP] = 0.f;
+        if constexpr (PARTS) __syncthreads();   // kx is read no more
+        for (int id = tid; id < NP * NP; id += TH) A[id / NP][id % NP] = 0.f, P[id / NP][id % NP] = 0.f;
         __syncthreads();
         constexpr int C = (DK + 63) / 64;
         for (int n = wave; n < cnt; n += NW) {
@@ -405,8 +416,8 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
 #pragma unroll
                 for (int d = 1; d < 64; d *= 2) pk += __shfl_xor(pk, d), pq += __shfl_xor(pq, d);
                 if (l == 0) {
-                    s.P[n][mm] = pq;
-                    if (mm != n && delta) s.A[n][mm] = bn * pk;
+                    P[n][mm] = pq;
+                    if (mm != n && delta) A[n][mm] = bn * pk;
                 }
             }
         }
@@ -422,12 +433,12 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
             for (int i = 0; i < 16; ++i) {
                 float x = i == j ? 1.f : 0.f;
 #pragma unroll
-                for (int q = 0; q < i; ++q) x -= s.A[r0 + i][r0 + q] * t[q];
+                for (int q = 0; q < i; ++q) x -= A[r0 + i][r0 + q] * t[q];
                 t[i] = x;
             }
             __builtin_amdgcn_wave_barrier();   // every lane of the block has read it
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s.A[r0 + i][r0 + j] = t[i];
+            for (int i = 0; i < 16; ++i) A[r0 + i][r0 + j] = t[i];
         }
         __syncthreads();
     }
@@ -448,9 +459,9 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
         if (delta) {
             f32x4 sub = zero4();
 #pragma unroll
-            for (int q = 0; q < t; ++q) sub = tree_mma(*reinterpret_cast<const f32x4*>(&s.A[16 * t + m][16 * q + 4 * g]), u[q], sub);
+            for (int q = 0; q < t; ++q) sub = tree_mma(*reinterpret_cast<const f32x4*>(&A[16 * t + m][16 * q + 4 * g]), u[q], sub);
             r = r - sub;
-            u[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.A[16 * t + m][16 * t + 4 * g]), r, zero4());
+            u[t] = tree_mma(*reinterpret_cast<const f32x4*>(&A[16 * t + m][16 * t + 4 * g]), r, zero4());
         } else {
             u[t] = r;
         }
@@ -458,7 +469,7 @@ __global__ __launch_bounds__(64 * NW, NP == 16 && !VEC ? 8 : 2) void tree_kernel
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int q = 0; q <= t; ++q) o[t] = tree_mma(*reinterpret_cast<const f32x4*>(&s.P[16 * t + m][16 * q + 4 * g]), u[q], o[t]);
+        for (int q = 0; q <= t; ++q) o[t] = tree_mma(*reinterpret_cast<const f32x4*>(&P[16 * t + m][16 * q + 4 * g]), u[q], o[t]);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll

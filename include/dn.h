@@ -384,8 +384,7 @@ dn_status dn_linear_recurrent_fwd(const dn_shape* shape, const void* q, const vo
  *            counts int32 [B] or NULL: the nodes of each batch element (clamped to
  *            0 .. T), o and u are zero from there on; accept int32 [B]; state fp32
  *            [B][H][dv][dk].  Gates below -1000 act as -1000 (a factor of zero).
- *   outputs: o (io) and u fp32, both [B][H][T][dv] (u NULL = not wanted).  Held to fp32; with bf16
- *            I/O and a gate per channel the scaled queries, which only o takes, to 16 bits.
+ *   outputs: o (io) and u fp32, both [B][H][T][dv] (u NULL = not wanted); held to fp32.
  *            NaN or Inf in a node may reach every node of its tree; so may positive gates that
  *            sum to more than 88 on a path
  * Validation and errors as for dn_recurrent_fwd; no workspace.
