@@ -77,7 +77,8 @@ __host__ __device__ constexpr int lin_pair(bool bf16, int nv) { return bf16 && n
 // state in LDS): eight waves form its outputs, each half of the channels, so that matrix,
 // vector and LDS work of more waves overlap (8 x 16 heads, 4096 steps, when it was chosen:
 // 580 us, four waves 607, and 1010 in 128 registers with two workgroups on a unit, which
-// spill; 541 now).
+// spill; 512 now).  The outputs alone, at 128 x 64 channels, are faster on four (163 us against
+// 190, ragged prompts of 8 x 16 heads).
 __host__ __device__ constexpr int lin_halves(int mode, bool bf16, int nv) {
     return mode == kLinDots && nv / lin_pair(bf16, nv) > 1 ? 2 : 1;
 }
