@@ -329,7 +329,7 @@ dn_status dn_chunk_phase_bwd(const dn_shape* shape, const void* q, const void* k
  *            state); positive values grow the state; where they sum to more than 88 within a
  *            chunk of 64 steps, results overflow (Inf or NaN) whatever the state holds
  *            (dg of a step whose factor is below 2^-126, g < -87.34, is zero, and no step's dg
- *            depends on what lies beyond such a step)
+ *            depends on what lies beyond such a step; NaN and Inf times zero stay NaN)
  *   forward : q, k, v, g (NULL iff no gate), h0 (NULL = zero) -> o, hT (NULL = not wanted)
  *   backward: the vector-Jacobian products of L = <o, dout> + <hT, dhT> (dhT NULL =
  *            zero): dq, dk, dv, dg (DN_GATE_SCALAR only, else NULL), dh0 (NULL = not
