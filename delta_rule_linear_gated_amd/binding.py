@@ -8,14 +8,18 @@ Low level (same names as the C ABI, ``EXPORTS``): raw calls that return the stat
 Convenience: ``chunk_fwd`` / ``chunk_bwd``, ``recurrent_fwd`` and their phase-gate forms
 for the delta rule, ``linear_fwd`` / ``linear_bwd`` / ``linear_recurrent_fwd`` for linear
 attention with a decay per head, ``tree_fwd`` / ``tree_commit`` for trees of drafted
-tokens on either's state: they check the tensors, allocate outputs and workspace with
-torch and call the above.  ``DeltaRule`` and ``LinearAttention`` are
-``torch.autograd.Function`` over them.
+tokens on either's state, ``gated_scan_fwd`` / ``gated_scan_bwd`` /
+``gated_scan_recurrent_fwd`` for the gated linear recurrence, ``qk_norm_fwd`` /
+``qk_norm_bwd`` and ``rotary_fwd`` / ``rotary_bwd`` (with ``rotary_freqs``) for what brings
+queries and keys there: they check the tensors, allocate outputs and workspace with
+torch and call the above.  ``DeltaRule``, ``LinearAttention``, ``GatedScan``, ``QKNorm``
+and ``Rotary`` are ``torch.autograd.Function`` over them.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -29,14 +33,19 @@ DN_OK, DN_ERR_INVALID, DN_ERR_SHAPE, DN_ERR_DTYPE, DN_ERR_WORKSPACE, DN_ERR_UNSU
 DN_F32, DN_BF16 = 0, 1
 DN_GATE_NONE, DN_GATE_SCALAR, DN_GATE_VECTOR, DN_GATE_HEAD = 0, 1, 2, 3
 DN_PASS_FWD, DN_PASS_BWD, DN_PASS_BWD_RECOMPUTE = 0, 1, 2
-DN_FLAG_KACZMARZ, DN_FLAG_NO_SCAN = 1, 2
+DN_FLAG_KACZMARZ, DN_FLAG_NO_SCAN, DN_FLAG_COUPLED = 1, 2, 4
+DN_NORM_NONE, DN_NORM_L2, DN_NORM_RMS = 0, 1, 2
+DN_ROT_HALVES, DN_ROT_NEIGHBOURS = 0, 1
+DN_POS_STEP, DN_POS_START, DN_POS_EACH = 0, 1, 2
 DN_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 EXPORTS = ("dn_states_bytes", "dn_states_layout", "dn_workspace_bytes", "dn_workspace_layout", "dn_chunk_fwd",
            "dn_chunk_fwd_noalloc", "dn_chunk_bwd", "dn_recurrent_fwd", "dn_recurrent_phase_fwd", "dn_phase_states_bytes",
            "dn_phase_workspace_bytes", "dn_chunk_phase_fwd", "dn_chunk_phase_bwd", "dn_linear_workspace_bytes",
            "dn_linear_fwd", "dn_linear_bwd", "dn_linear_recurrent_fwd", "dn_tree_fwd", "dn_tree_commit",
-           "dn_tree_commit_counts", "dn_status_string", "dn_last_error",
+           "dn_tree_commit_counts", "dn_gated_scan_states_bytes", "dn_gated_scan_workspace_bytes", "dn_gated_scan_fwd",
+           "dn_gated_scan_bwd", "dn_gated_scan_recurrent_fwd", "dn_qk_workspace_bytes", "dn_qk_fwd", "dn_qk_bwd",
+           "dn_status_string", "dn_last_error",
            "dn_profile_enable", "dn_profile_collect")
 
 
@@ -51,6 +60,14 @@ class Shape(ctypes.Structure):
                 ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("C", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("gate", ctypes.c_int32), ("flags", ctypes.c_uint32),
                 ("eps", ctypes.c_float)]
+
+
+class QKShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("dtype", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("pos_kind", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("amplitude", ctypes.c_float), ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
+                ("dq_stride", ctypes.c_int64 * 3), ("dk_stride", ctypes.c_int64 * 3)]
 
 
 _lib = None
@@ -106,6 +123,23 @@ def lib():
     L.dn_tree_commit.restype = i32
     L.dn_tree_commit_counts.argtypes = [sp] + [vp] * 8
     L.dn_tree_commit_counts.restype = i32
+    L.dn_gated_scan_states_bytes.argtypes = [sp]
+    L.dn_gated_scan_states_bytes.restype = sz
+    L.dn_gated_scan_workspace_bytes.argtypes = [sp, i32]
+    L.dn_gated_scan_workspace_bytes.restype = sz
+    L.dn_gated_scan_fwd.argtypes = [sp] + [vp] * 8 + [sz, vp]
+    L.dn_gated_scan_fwd.restype = i32
+    L.dn_gated_scan_bwd.argtypes = [sp] + [vp] * 11 + [sz, vp]
+    L.dn_gated_scan_bwd.restype = i32
+    L.dn_gated_scan_recurrent_fwd.argtypes = [sp] + [vp] * 5
+    L.dn_gated_scan_recurrent_fwd.restype = i32
+    qp = ctypes.POINTER(QKShape)
+    L.dn_qk_workspace_bytes.argtypes = [qp]
+    L.dn_qk_workspace_bytes.restype = sz
+    L.dn_qk_fwd.argtypes = [qp] + [vp] * 10
+    L.dn_qk_fwd.restype = i32
+    L.dn_qk_bwd.argtypes = [qp] + [vp] * 14 + [sz, vp]
+    L.dn_qk_bwd.restype = i32
     L.dn_status_string.argtypes = [i32]
     L.dn_status_string.restype = ctypes.c_char_p
     L.dn_last_error.argtypes = []
@@ -302,6 +336,51 @@ def dn_tree_commit_counts(shape, k, u, g, parent, counts, accept, state, stream=
     """Raw call; returns the dn_status (no exception)."""
     return lib().dn_tree_commit_counts(ctypes.byref(shape), _ptr(k), _ptr(u), _ptr(g), _ptr(parent), _ptr(counts),
                                        _ptr(accept), _ptr(state), _stream(stream))
+
+
+def dn_gated_scan_states_bytes(shape: Shape) -> int:
+    return lib().dn_gated_scan_states_bytes(ctypes.byref(shape))
+
+
+def dn_gated_scan_workspace_bytes(shape: Shape, pass_: int) -> int:
+    return lib().dn_gated_scan_workspace_bytes(ctypes.byref(shape), int(pass_))
+
+
+def dn_gated_scan_fwd(shape, x, g, lens, h0, o, hT, states, ws=None, ws_bytes=0, stream=None) -> int:
+    """Raw call; returns the dn_status (no exception)."""
+    return lib().dn_gated_scan_fwd(ctypes.byref(shape), _ptr(x), _ptr(g), _ptr(lens), _ptr(h0), _ptr(o), _ptr(hT),
+                                   _ptr(states), _ptr(ws), int(ws_bytes), _stream(stream))
+
+
+def dn_gated_scan_bwd(shape, x, g, lens, h0, dout, dhT, states, dx, dg, dh0, ws=None, ws_bytes=0, stream=None) -> int:
+    """Raw call; returns the dn_status (no exception)."""
+    return lib().dn_gated_scan_bwd(ctypes.byref(shape), _ptr(x), _ptr(g), _ptr(lens), _ptr(h0), _ptr(dout), _ptr(dhT),
+                                   _ptr(states), _ptr(dx), _ptr(dg), _ptr(dh0), _ptr(ws), int(ws_bytes),
+                                   _stream(stream))
+
+
+def dn_gated_scan_recurrent_fwd(shape, x, g, state, o, stream=None) -> int:
+    """Raw call; returns the dn_status (no exception)."""
+    return lib().dn_gated_scan_recurrent_fwd(ctypes.byref(shape), _ptr(x), _ptr(g), _ptr(state), _ptr(o),
+                                             _stream(stream))
+
+
+def dn_qk_workspace_bytes(shape: QKShape) -> int:
+    return lib().dn_qk_workspace_bytes(ctypes.byref(shape))
+
+
+def dn_qk_fwd(shape, q, k, wq, wk, freqs, pos, lens, yq, yk, stream=None) -> int:
+    """Raw call; returns the dn_status (no exception)."""
+    return lib().dn_qk_fwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(freqs), _ptr(pos),
+                           _ptr(lens), _ptr(yq), _ptr(yk), _stream(stream))
+
+
+def dn_qk_bwd(shape, q, k, dyq, dyk, wq, wk, freqs, pos, lens, dq, dk, dwq, dwk, ws=None, ws_bytes=0,
+              stream=None) -> int:
+    """Raw call; returns the dn_status (no exception)."""
+    return lib().dn_qk_bwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(dyq), _ptr(dyk), _ptr(wq), _ptr(wk),
+                           _ptr(freqs), _ptr(pos), _ptr(lens), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(ws),
+                           int(ws_bytes), _stream(stream))
 
 
 # ------------------------------------------------------------------ convenience
@@ -716,3 +795,280 @@ def tree_commit(k, u, g, parent, accept, state, stream=None, counts=None):
     sh = make_shape(B, H, N, dk, dv, 64, k.dtype, kind)
     _check(dn_tree_commit_counts(sh, k, u, g, parent, counts, accept, state, stream))
     return state
+
+
+# ------------------------------------------------------------------ gated linear recurrence
+
+
+def _scan_args(x, g, coupled, ws, *more):
+    """Shape descriptor of checked tensors; ``more``: (name, tensor, "x" | "g" | "state" | "lens")."""
+    if x.dim() != 4:
+        raise ValueError(f"x must be [B,H,T,d], got shape {tuple(x.shape)}")
+    B, H, T, d = x.shape
+    io, f32 = x.dtype, torch.float32
+    if io not in _IO_DTYPES:
+        raise ValueError(f"x must be float32 or bfloat16, got {io}")
+    if ws is not None and not (ws.is_contiguous() and ws.device == x.device):   # its size: the C ABI
+        raise ValueError(f"ws must be contiguous and on {x.device}")
+    kinds = {"x": (io, x.shape), "g": (f32, x.shape), "state": (f32, (B, H, d)), "lens": (torch.int32, (B,)),
+             "states": (f32, (B, H, -(-T // 128), d))}
+    _check_tensors(x.device, ("x", x, io, x.shape), ("g", g, f32, x.shape),
+                   *((n, t, *kinds[what]) for n, t, what in more))
+    return Shape(B, H, T, d, d, 64, DN_BF16 if io == torch.bfloat16 else DN_F32, DN_GATE_VECTOR,
+                 DN_FLAG_COUPLED if coupled else 0, 0.0)
+
+
+def _scan_ws(shape, pass_, ws, device):
+    n = dn_gated_scan_workspace_bytes(shape, pass_)
+    if ws is None and n:
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+    return ws, (0 if ws is None else ws.numel() * ws.element_size())
+
+
+def gated_scan_fwd(x, g, h0=None, lens=None, coupled=False, save_states=True, want_hT=True, ws=None, stream=None):
+    """Gated linear recurrence over whole sequences, a state for each channel: h_t = exp(g_t) h_{t-1} + w_t x_t,
+    o_t = h_t, with w_t = 1 or, ``coupled``, 1 - exp(g_t).  x [B,H,T,d] (any d), ``g`` fp32 like x (log-decays),
+    ``h0`` fp32 [B,H,d]; ``lens``: int32 [B], the steps of each batch element (o is zero past them, hT the state
+    after them).  Returns (o, hT or None, states or None): states is what gated_scan_bwd takes."""
+    sh = _scan_args(x, g, coupled, ws, ("h0", h0, "state"), ("lens", lens, "lens"))
+    with _allocating(stream):
+        o = torch.empty_like(x)
+        hT = torch.empty(sh.B, sh.H, sh.dv, dtype=torch.float32, device=x.device) if want_hT else None
+        states = (torch.empty(sh.B, sh.H, -(-sh.T // 128), sh.dv, dtype=torch.float32, device=x.device)
+                  if save_states else None)
+        ws, n = _scan_ws(sh, DN_PASS_FWD, ws, x.device)
+    _check(dn_gated_scan_fwd(sh, x, g, lens, h0, o, hT, states, ws, n, stream))
+    return o, hT, states
+
+
+def gated_scan_bwd(x, g, h0, do, dhT=None, states=None, lens=None, coupled=False, want_dh0=True, ws=None, stream=None):
+    """Backward of gated_scan_fwd from the states it saved, or (states None) with the states recomputed from h0.
+    Returns dict dx, dg, dh0 (or None)."""
+    sh = _scan_args(x, g, coupled, ws, ("h0", h0, "state"), ("do", do, "x"), ("dhT", dhT, "state"),
+                    ("states", states, "states"), ("lens", lens, "lens"))
+    with _allocating(stream):
+        dx, dg = torch.empty_like(x), torch.empty_like(g)
+        dh0 = torch.empty(sh.B, sh.H, sh.dv, dtype=torch.float32, device=x.device) if want_dh0 else None
+        ws, n = _scan_ws(sh, DN_PASS_BWD if states is not None else DN_PASS_BWD_RECOMPUTE, ws, x.device)
+    if states is not None and states.numel() == 0:   # no steps: nothing was saved
+        states = None
+    _check(dn_gated_scan_bwd(sh, x, g, lens, h0, do, dhT, states, dx, dg, dh0, ws, n, stream))
+    return {"dx": dx, "dg": dg, "dh0": dh0}
+
+
+def gated_scan_recurrent_fwd(x, g, state, coupled=False, stream=None):
+    """T recurrent steps of the gated linear recurrence (decode); ``state`` (fp32 [B,H,d]) is updated in place.
+    Returns o."""
+    sh = _scan_args(x, g, coupled, None, ("state", state, "state"))
+    with _allocating(stream):
+        o = torch.empty_like(x)
+    _check(dn_gated_scan_recurrent_fwd(sh, x, g, state, o, stream))
+    return o
+
+
+class GatedScan(torch.autograd.Function):
+    """o, hT = GatedScan.apply(x, g, h0, lens, coupled, recompute): with ``recompute`` no states are kept for the
+    backward.  For capture into a HIP graph see LinearAttention."""
+
+    @staticmethod
+    def forward(ctx, x, g, h0=None, lens=None, coupled=False, recompute=False):
+        o, hT, states = gated_scan_fwd(x, g, h0, lens=lens, coupled=coupled, save_states=not recompute)
+        ctx.coupled = coupled
+        ctx.save_for_backward(x, g, h0, lens, states)
+        return o, hT
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do, dhT):
+        x, g, h0, lens, states = ctx.saved_tensors
+        gr = gated_scan_bwd(x, g, h0, do.contiguous(), None if dhT is None else dhT.contiguous(), states, lens=lens,
+                            coupled=ctx.coupled, want_dh0=h0 is not None)
+        return gr["dx"], gr["dg"], gr["dh0"], None, None, None
+
+
+# ------------------------------------------------------------------ norms and rotations of queries and keys
+
+
+def rotary_freqs(rot, base=10000.0, scaling=None, factor=1.0, trained=None, fast=32.0, slow=1.0, device=None):
+    """Angle of one position of each of the rot / 2 pairs (fp64, on ``device``) and the amplitude to go with them:
+    base^(-2m / rot), for contexts ``factor`` times the trained ones scaled by
+      None      not at all
+      "linear"  all angles divided by the factor (interpolated positions)
+      "ntk"     the base raised so that the slowest pair is divided by the factor and the fastest stays
+      "yarn"    pairs that turn ``fast`` times and more within ``trained`` positions stay, those that turn ``slow``
+                times and fewer are divided by the factor, in between by a ramp; amplitude 0.1 ln(factor) + 1
+    Returns (freqs, amplitude)."""
+    if rot <= 0 or rot % 2:
+        raise ValueError(f"rot must be positive and even, got {rot}")
+    if not factor >= 1.0 or not base > 0.0:
+        raise ValueError("factor must be at least 1 and base positive")
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if not trained or not fast > slow:
+            raise ValueError("yarn needs the trained length, and fast > slow")
+        keep = ((trained * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+        amplitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    return f.to(device), amplitude
+
+
+_NORMS = {"l2": DN_NORM_L2, "rms": DN_NORM_RMS}
+
+
+def _qk_args(sides, weights, norm, eps, freqs, pos, interleaved, amplitude, lens, grads=()):
+    """Shape descriptor of checked tensors.  ``sides``: (name, q or k or None), rows [B,heads,T,d] in any order of the
+    dimensions but the last; ``grads``: (name, tensor, dense like that side)."""
+    (qn, q), (kn, k) = sides
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError(f"{qn} or {kn} must be given")
+    if one.dim() != 4:
+        raise ValueError(f"{qn} and {kn} must be [B,heads,T,d], got shape {tuple(one.shape)}")
+    B, _, T, d = one.shape
+    io, dev = one.dtype, one.device
+    if io not in _IO_DTYPES:
+        raise ValueError(f"{qn} and {kn} must be float32 or bfloat16, got {io}")
+    for n, t in sides:
+        if t is None:
+            continue
+        if t.dim() != 4 or (t.shape[0], t.shape[2], t.shape[3]) != (B, T, d):
+            raise ValueError(f"{n} must be [{B},heads,{T},{d}], got shape {tuple(t.shape)}")
+        if t.dtype != io:
+            raise ValueError(f"{n} must be {io}, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"every tensor must be on {dev}, found one on {t.device}")
+        if t.stride(3) != 1 and d > 1:
+            raise ValueError(f"the rows of {n} must be dense")
+    rot, kind = 0, DN_POS_STEP
+    if freqs is not None:
+        if freqs.dim() != 1:
+            raise ValueError(f"freqs must be [rot / 2], got shape {tuple(freqs.shape)}")
+        if freqs.requires_grad:
+            raise ValueError("freqs is a constant: it gets no gradient")
+        rot = 2 * freqs.shape[0]
+        if pos is not None:
+            kind = DN_POS_EACH if pos.dim() == 2 else DN_POS_START
+    elif pos is not None:
+        raise ValueError("pos without freqs")
+    f32, i32 = torch.float32, torch.int32
+    _check_tensors(dev, *((n, t, f32, (d,)) for n, t in weights), ("freqs", freqs, torch.float64, (rot // 2,)),
+                   ("pos", pos, i32, (B, T) if kind == DN_POS_EACH else (B,)), ("lens", lens, i32, (B,)),
+                   *((n, t, io, like.shape) for n, t, like in grads))
+    strides = [(ctypes.c_int64 * 3)(*(0, 0, 0) if t is None else t.stride()[:3]) for t in (q, k)]
+    return QKShape(B, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], T, d, rot,
+                   DN_BF16 if io == torch.bfloat16 else DN_F32, norm, DN_ROT_NEIGHBOURS if interleaved else DN_ROT_HALVES,
+                   kind, float(eps), float(amplitude), *strides)
+
+
+def _qk_norm(norm):
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be 'l2' or 'rms', got {norm!r}")
+    return _NORMS[norm]
+
+
+def _rows_like(t):
+    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def qk_norm_fwd(q, k, wq=None, wk=None, norm="l2", eps=1e-6, freqs=None, pos=None, interleaved=False, amplitude=1.0,
+                lens=None, stream=None):
+    """Rows of queries and keys normalised for each head and, with ``freqs``, rotated by position in the same pass:
+    x (|x|^2 + eps)^(-1/2) (``norm`` "l2") or x (|x|^2 / d + eps)^(-1/2) ("rms"), times ``wq`` / ``wk`` (fp32 [d]).
+    q [B,Hq,T,d], k [B,Hk,T,d] (either None): any order of the dimensions but the last, as the transposed views of a
+    projection's [B,T,heads,d], slices of a fused one among them.  Rotation, positions and ``lens`` as for
+    rotary_fwd.  Returns (yq, yk), contiguous, as the operators above take them."""
+    sh = _qk_args((("q", q), ("k", k)), (("wq", wq), ("wk", wk)), _qk_norm(norm), eps, freqs, pos, interleaved,
+                  amplitude, lens)
+    with _allocating(stream):
+        yq, yk = _rows_like(q), _rows_like(k)
+    _check(dn_qk_fwd(sh, q, k, wq, wk, freqs, pos, lens, yq, yk, stream))
+    return yq, yk
+
+
+def qk_norm_bwd(q, k, dyq, dyk, wq=None, wk=None, norm="l2", eps=1e-6, freqs=None, pos=None, interleaved=False,
+                amplitude=1.0, lens=None, want_dw=True, stream=None):
+    """Backward of qk_norm_fwd from contiguous dyq, dyk.  Returns dict dq, dk (in the order of q's and k's dimensions),
+    dwq, dwk (fp32 [d]; None without that weight)."""
+    sh = _qk_args((("q", q), ("k", k)), (("wq", wq), ("wk", wk)), _qk_norm(norm), eps, freqs, pos, interleaved,
+                  amplitude, lens, [(n, t, x) for n, t, x in (("dyq", dyq, q), ("dyk", dyk, k)) if x is not None])
+    with _allocating(stream):
+        dq, dk = (None if t is None else torch.empty_like(t) for t in (q, k))
+        dwq, dwk = (torch.empty_like(w) if want_dw and w is not None else None for w in (wq, wk))
+        n = dn_qk_workspace_bytes(sh) if dwq is not None or dwk is not None else 0
+        ws = torch.empty(n, dtype=torch.uint8, device=(q if q is not None else k).device) if n else None
+    for to, t in ((sh.dq_stride, dq), (sh.dk_stride, dk)):
+        if t is not None:
+            to[:] = t.stride()[:3]
+    _check(dn_qk_bwd(sh, q, k, dyq, dyk, wq, wk, freqs, pos, lens, dq, dk, dwq, dwk, ws, n, stream))
+    return {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
+
+
+def rotary_fwd(q, k, freqs, pos=None, interleaved=False, amplitude=1.0, lens=None, stream=None):
+    """Rows of queries and keys rotated by position: of the first 2 * len(freqs) elements of a head the pairs
+    (m, m + len(freqs)) or, ``interleaved``, (2m, 2m + 1) by position * freqs[m], times ``amplitude`` (see
+    rotary_freqs); the others stay.  q [B,Hq,T,d], k [B,Hk,T,d] (either None), any order of the dimensions but the last;
+    ``pos``: None (the step), int32 [B] (the position of the first step) or int32 [B,T]; ``lens``: int32 [B], rows from
+    there on are zero.  Returns (yq, yk), contiguous."""
+    sh = _qk_args((("q", q), ("k", k)), (), DN_NORM_NONE, 0.0, freqs, pos, interleaved, amplitude, lens)
+    with _allocating(stream):
+        yq, yk = _rows_like(q), _rows_like(k)
+    _check(dn_qk_fwd(sh, q, k, None, None, freqs, pos, lens, yq, yk, stream))
+    return yq, yk
+
+
+def rotary_bwd(dyq, dyk, freqs, pos=None, interleaved=False, amplitude=1.0, lens=None, stream=None):
+    """Backward of rotary_fwd (the rotation back) from contiguous dyq [B,Hq,T,d], dyk [B,Hk,T,d].  Returns (dq, dk),
+    contiguous."""
+    sh = _qk_args((("dyq", dyq), ("dyk", dyk)), (), DN_NORM_NONE, 0.0, freqs, pos, interleaved, amplitude, lens)
+    _contig(dyq, dyk)
+    with _allocating(stream):
+        dq, dk = _rows_like(dyq), _rows_like(dyk)
+    for to, t in ((sh.dq_stride, dq), (sh.dk_stride, dk)):
+        if t is not None:
+            to[:] = t.stride()[:3]
+    _check(dn_qk_bwd(sh, None, None, dyq, dyk, None, None, freqs, pos, lens, dq, dk, None, None, None, 0, stream))
+    return dq, dk
+
+
+class QKNorm(torch.autograd.Function):
+    """yq, yk = QKNorm.apply(q, k, wq, wk, norm, eps, freqs, pos, interleaved, amplitude, lens), as qk_norm_fwd."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq=None, wk=None, norm="l2", eps=1e-6, freqs=None, pos=None, interleaved=False,
+                amplitude=1.0, lens=None):
+        ctx.how = dict(norm=norm, eps=eps, interleaved=interleaved, amplitude=amplitude)
+        ctx.save_for_backward(q, k, wq, wk, freqs, pos, lens)
+        return qk_norm_fwd(q, k, wq, wk, freqs=freqs, pos=pos, lens=lens, **ctx.how)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dyq, dyk):
+        q, k, wq, wk, freqs, pos, lens = ctx.saved_tensors
+        gr = qk_norm_bwd(q, k, None if q is None else dyq.contiguous(), None if k is None else dyk.contiguous(), wq, wk,
+                         freqs=freqs, pos=pos, lens=lens, want_dw=any(ctx.needs_input_grad[2:4]), **ctx.how)
+        return gr["dq"], gr["dk"], gr["dwq"], gr["dwk"], None, None, None, None, None, None, None
+
+
+class Rotary(torch.autograd.Function):
+    """yq, yk = Rotary.apply(q, k, freqs, pos, interleaved, amplitude, lens), as rotary_fwd."""
+
+    @staticmethod
+    def forward(ctx, q, k, freqs, pos=None, interleaved=False, amplitude=1.0, lens=None):
+        ctx.how = dict(interleaved=interleaved, amplitude=amplitude)
+        ctx.save_for_backward(freqs, pos, lens)
+        return rotary_fwd(q, k, freqs, pos=pos, lens=lens, **ctx.how)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dyq, dyk):
+        freqs, pos, lens = ctx.saved_tensors
+        dq, dk = rotary_bwd(None if dyq is None else dyq.contiguous(), None if dyk is None else dyk.contiguous(), freqs,
+                            pos=pos, lens=lens, **ctx.how)
+        return dq, dk, None, None, None, None, None

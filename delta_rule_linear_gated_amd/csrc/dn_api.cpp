@@ -12,8 +12,10 @@
 #include <utility>
 
 #include "dn.h"
+#include "dn_gated_scan.h"
 #include "dn_internal.h"
 #include "dn_linear_api.h"
+#include "dn_qk.h"
 #include "dn_tree.h"
 
 namespace {
@@ -965,6 +967,307 @@ dn_status dn_tree_commit_counts(const dn_shape* shape, const void* k, const floa
     a.accept = accept;
     a.state = state;
     const hipError_t e = dn::launch_tree_commit(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return DN_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+struct ScanBytes {
+    size_t x, g, state, lens, saved;
+};
+dn_status scan_shape(const dn_shape* s, dn::GsProblem* pr, ScanBytes* n) {
+    if (!s) return fail(DN_ERR_INVALID, "shape is NULL");
+    if (s->B < 0 || s->H < 0 || s->T < 0) return fail(DN_ERR_SHAPE, "B, H, T must be >= 0");
+    if (s->dv <= 0) return fail(DN_ERR_SHAPE, "dv must be > 0");
+    if (s->dtype != DN_F32 && s->dtype != DN_BF16) return fail(DN_ERR_DTYPE, "unknown dtype %d", s->dtype);
+    if (s->gate < DN_GATE_NONE || s->gate > DN_GATE_HEAD) return fail(DN_ERR_INVALID, "unknown gate %d", s->gate);
+    if (s->flags & ~DN_FLAG_COUPLED) return fail(DN_ERR_INVALID, "unknown flags 0x%x", s->flags);
+    if (s->gate != DN_GATE_VECTOR) return fail(DN_ERR_UNSUPPORTED, "the gated scan has a gate per channel");
+    if (s->T > (1 << 30)) return fail(DN_ERR_UNSUPPORTED, "T must be <= 2^30");
+    if (s->dv > (1 << 22)) return fail(DN_ERR_UNSUPPORTED, "dv must be <= 2^22");
+    *pr = dn::GsProblem{s->B, s->H, s->T, s->dv, s->dtype == DN_BF16, (s->flags & DN_FLAG_COUPLED) ? 1 : 0};
+    if (!dn::gs_fits(*pr)) return fail(DN_ERR_UNSUPPORTED, "B*H*dv too large");
+    const size_t rows = (size_t)s->B * s->H * s->dv;
+    *n = ScanBytes{rows * s->T * (pr->bf16 ? 2 : 4), rows * s->T * 4, rows * 4, (size_t)s->B * 4,
+                   dn::gs_states_bytes(*pr)};
+    return DN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dn_gated_scan_states_bytes(const dn_shape* shape) {
+    dn::GsProblem pr;
+    ScanBytes n;
+    return scan_shape(shape, &pr, &n) == DN_OK ? n.saved : 0;
+}
+
+size_t dn_gated_scan_workspace_bytes(const dn_shape* shape, int pass) {
+    dn::GsProblem pr;
+    ScanBytes n;
+    if (pass < DN_PASS_FWD || pass > DN_PASS_BWD_RECOMPUTE) return 0;
+    return scan_shape(shape, &pr, &n) == DN_OK ? dn::gs_workspace_bytes(pr, pass) : 0;
+}
+
+dn_status dn_gated_scan_fwd(const dn_shape* shape, const void* x, const float* g, const int32_t* lens, const float* h0,
+                            void* o, float* hT, float* states, void* ws, size_t ws_bytes, void* stream) {
+    g_err[0] = '\0';
+    dn::GsProblem pr;
+    ScanBytes n;
+    DN_TRY(scan_shape(shape, &pr, &n));
+    const size_t nws = dn::gs_workspace_bytes(pr, DN_PASS_FWD);
+    DN_TRY(need(x, n.x, "x"));
+    DN_TRY(need(g, n.g, "g"));
+    DN_TRY(need(o, n.x, "o"));
+    if (ws_bytes < nws) return fail(DN_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, nws);
+    DN_TRY(need(ws, nws, "workspace"));
+    DN_TRY(check_buffers({{"x", x, n.x, false},
+                          {"g", g, n.g, false},
+                          {"lens", lens, n.lens, false},
+                          {"h0", h0, n.state, false},
+                          {"o", o, n.x, true},
+                          {"hT", hT, n.state, true},
+                          {"states", states, n.saved, true},
+                          {"workspace", ws, nws, true}}));
+    const dn::GsFwd f{x, g, lens, h0, o, hT, states};
+    const hipError_t e = dn::launch_gated_scan_fwd(pr, f, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return DN_OK;
+}
+
+dn_status dn_gated_scan_bwd(const dn_shape* shape, const void* x, const float* g, const int32_t* lens, const float* h0,
+                            const void* dout, const float* dhT, const float* states, void* dx, float* dg, float* dh0,
+                            void* ws, size_t ws_bytes, void* stream) {
+    g_err[0] = '\0';
+    dn::GsProblem pr;
+    ScanBytes n;
+    DN_TRY(scan_shape(shape, &pr, &n));
+    const size_t nws = dn::gs_workspace_bytes(pr, states ? DN_PASS_BWD : DN_PASS_BWD_RECOMPUTE);
+    DN_TRY(need(x, n.x, "x"));
+    DN_TRY(need(g, n.g, "g"));
+    DN_TRY(need(dout, n.x, "dout"));
+    DN_TRY(need(dx, n.x, "dx"));
+    DN_TRY(need(dg, n.g, "dg"));
+    if (ws_bytes < nws) return fail(DN_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, nws);
+    DN_TRY(need(ws, nws, "workspace"));
+    DN_TRY(check_buffers({{"x", x, n.x, false},
+                          {"g", g, n.g, false},
+                          {"lens", lens, n.lens, false},
+                          {"h0", h0, n.state, false},
+                          {"dout", dout, n.x, false},
+                          {"dhT", dhT, n.state, false},
+                          {"states", states, n.saved, false},
+                          {"dx", dx, n.x, true},
+                          {"dg", dg, n.g, true},
+                          {"dh0", dh0, n.state, true},
+                          {"workspace", ws, nws, true}}));
+    const dn::GsBwd f{x, g, lens, h0, dout, dhT, states, dx, dg, dh0};
+    const hipError_t e = dn::launch_gated_scan_bwd(pr, f, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return DN_OK;
+}
+
+dn_status dn_gated_scan_recurrent_fwd(const dn_shape* shape, const void* x, const float* g, float* state, void* o,
+                                      void* stream) {
+    g_err[0] = '\0';
+    dn::GsProblem pr;
+    ScanBytes n;
+    DN_TRY(scan_shape(shape, &pr, &n));
+    DN_TRY(need(x, n.x, "x"));
+    DN_TRY(need(g, n.g, "g"));
+    DN_TRY(need(state, n.state, "state"));
+    DN_TRY(need(o, n.x, "o"));
+    DN_TRY(check_buffers({{"x", x, n.x, false}, {"g", g, n.g, false}, {"state", state, n.state, true}, {"o", o, n.x, true}}));
+    const hipError_t e = dn::launch_gated_scan_recurrent(pr, x, g, state, o, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return DN_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks of a norm's or rotation's shape; `a` gets all but the pointers and strides.
+dn_status qk_shape(const dn_qk_shape* s, dn::QkArgs* a) {
+    if (!s) return fail(DN_ERR_INVALID, "shape is NULL");
+    if (s->B < 0 || s->Hq < 0 || s->Hk < 0 || s->T < 0) return fail(DN_ERR_SHAPE, "B, Hq, Hk, T must be >= 0");
+    if (s->d <= 0 || s->rot < 0 || s->rot > s->d) return fail(DN_ERR_SHAPE, "d must be > 0 and rot 0 .. d");
+    if (s->dtype != DN_F32 && s->dtype != DN_BF16) return fail(DN_ERR_DTYPE, "unknown dtype %d", s->dtype);
+    if (s->norm < DN_NORM_NONE || s->norm > DN_NORM_RMS) return fail(DN_ERR_INVALID, "unknown norm %d", s->norm);
+    if (s->layout < DN_ROT_HALVES || s->layout > DN_ROT_NEIGHBOURS) return fail(DN_ERR_INVALID, "unknown layout %d", s->layout);
+    if (s->pos_kind < DN_POS_STEP || s->pos_kind > DN_POS_EACH) return fail(DN_ERR_INVALID, "unknown pos_kind %d", s->pos_kind);
+    if (s->norm != DN_NORM_NONE && !(std::isfinite(s->eps) && s->eps >= 0.f))
+        return fail(DN_ERR_INVALID, "eps must be finite and >= 0");
+    if (s->rot > 0 && !std::isfinite(s->amplitude)) return fail(DN_ERR_INVALID, "amplitude must be finite");
+    if (s->norm == DN_NORM_NONE && s->rot == 0) return fail(DN_ERR_UNSUPPORTED, "neither a norm nor a rotation");
+    if (s->d != 16 && s->d != 32 && s->d != 64 && s->d != 128)
+        return fail(DN_ERR_UNSUPPORTED, "d must be 16, 32, 64 or 128");
+    if (s->rot % 8 != 0) return fail(DN_ERR_UNSUPPORTED, "rot must be a multiple of 8");
+    *a = dn::QkArgs{};
+    a->B = s->B;
+    a->T = s->T;
+    a->d = s->d;
+    a->rot = s->rot;
+    a->bf16 = s->dtype == DN_BF16;
+    a->turn = s->rot == 0 ? dn::kTurnNone : s->layout == DN_ROT_HALVES ? dn::kTurnHalves : dn::kTurnNeighbours;
+    a->norm = s->norm;
+    a->eps = s->eps;
+    a->share = s->norm == DN_NORM_RMS ? 1.f / (float)s->d : 1.f;
+    a->amplitude = s->amplitude;
+    a->pos_kind = s->pos_kind;
+    a->side[0].heads = s->Hq;
+    a->side[1].heads = s->Hk;
+    if ((long long)s->B * s->T > (1LL << 30)) return fail(DN_ERR_UNSUPPORTED, "B*T must be <= 2^30");
+    if (!dn::qk_fits(*a)) return fail(DN_ERR_UNSUPPORTED, "B*T*(Hq+Hk) too large");
+    return DN_OK;
+}
+
+// Rows [B][heads][T][d] by strides (batch, head, step; elements), and the bytes from the first
+// to the last.  An output's rows may not share memory: sorted by stride, each dimension has to
+// step over all of those before it.
+dn_status qk_strides(const dn::QkArgs& a, int heads, const int64_t stride[3], bool output, const char* name, long to[3],
+                     size_t* bytes) {
+    const int64_t size[3] = {a.B, heads, a.T};
+    const size_t E = a.bf16 ? 2 : 4;
+    *bytes = 0;
+    to[0] = to[1] = to[2] = 0;
+    if (size[0] * size[1] == 0 || size[2] == 0) return DN_OK;
+    __int128 last = a.d;
+    for (int i = 0; i < 3; ++i) {
+        if (size[i] == 1) continue;
+        if (stride[i] < 0) return fail(DN_ERR_UNSUPPORTED, "%s has a negative stride", name);
+        if (stride[i] * E % 16 != 0 || stride[i] > (1LL << 56)) return fail(DN_ERR_UNSUPPORTED, "the strides of %s must be multiples of 16 bytes", name);
+        to[i] = (long)stride[i];
+        last += (__int128)(size[i] - 1) * stride[i];
+    }
+    if (last > ((__int128)1 << 56)) return fail(DN_ERR_UNSUPPORTED, "%s reaches too far", name);
+    *bytes = (size_t)last * E;
+    if (!output) return DN_OK;
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int i, int j) { return to[i] < to[j]; });
+    __int128 over = a.d;
+    for (int i : order) {
+        if (size[i] == 1) continue;
+        if (to[i] < over) return fail(DN_ERR_INVALID, "the rows of %s overlap", name);
+        over = (__int128)to[i] * size[i];
+    }
+    return DN_OK;
+}
+
+void qk_dense(const dn::QkArgs& a, int heads, long to[3]) {
+    to[0] = (long)heads * a.T * a.d;
+    to[1] = (long)a.T * a.d;
+    to[2] = a.d;
+}
+
+size_t qk_pos_bytes(const dn_qk_shape* s) {
+    if (s->rot == 0) return 0;
+    return s->pos_kind == DN_POS_STEP ? 0 : s->pos_kind == DN_POS_START ? (size_t)s->B * 4 : (size_t)s->B * s->T * 4;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dn_qk_workspace_bytes(const dn_qk_shape* shape) {
+    dn::QkArgs a;
+    if (qk_shape(shape, &a) != DN_OK || a.norm == DN_NORM_NONE) return 0;
+    return dn::qk_workspace_bytes(a);
+}
+
+dn_status dn_qk_fwd(const dn_qk_shape* shape, const void* q, const void* k, const float* wq, const float* wk,
+                    const double* freqs, const int32_t* pos, const int32_t* lens, void* yq, void* yk, void* stream) {
+    g_err[0] = '\0';
+    dn::QkArgs a;
+    DN_TRY(qk_shape(shape, &a));
+    size_t nq, nk;
+    DN_TRY(qk_strides(a, shape->Hq, shape->q_stride, false, "q", a.side[0].xs, &nq));
+    DN_TRY(qk_strides(a, shape->Hk, shape->k_stride, false, "k", a.side[1].xs, &nk));
+    const size_t E = a.bf16 ? 2 : 4, row = (size_t)a.B * a.T * a.d * E, nw = (size_t)a.d * 4;
+    const size_t nf = (size_t)a.rot * 4, np = qk_pos_bytes(shape), any = nq + nk;
+    if (a.norm == DN_NORM_NONE && (wq || wk)) return fail(DN_ERR_INVALID, "weights without a norm");
+    DN_TRY(need(q, nq, "q"));
+    DN_TRY(need(k, nk, "k"));
+    DN_TRY(need(freqs, any ? nf : 0, "freqs"));
+    DN_TRY(need(pos, any ? np : 0, "pos"));
+    DN_TRY(need(yq, shape->Hq * row, "yq"));
+    DN_TRY(need(yk, shape->Hk * row, "yk"));
+    DN_TRY(check_buffers({{"q", q, nq, false},
+                          {"k", k, nk, false},
+                          {"wq", wq, nw, false},
+                          {"wk", wk, nw, false},
+                          {"freqs", freqs, nf, false},
+                          {"pos", pos, np, false},
+                          {"lens", lens, (size_t)a.B * 4, false},
+                          {"yq", yq, shape->Hq * row, true},
+                          {"yk", yk, shape->Hk * row, true}}));
+    a.freqs = freqs;
+    a.pos = pos;
+    a.lens = lens;
+    a.side[0].x = q, a.side[0].w = wq, a.side[0].out = yq;
+    a.side[1].x = k, a.side[1].w = wk, a.side[1].out = yk;
+    for (dn::QkSide& s : a.side) qk_dense(a, s.heads, s.os);
+    const hipError_t e = dn::launch_qk_fwd(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return DN_OK;
+}
+
+dn_status dn_qk_bwd(const dn_qk_shape* shape, const void* q, const void* k, const void* dyq, const void* dyk,
+                    const float* wq, const float* wk, const double* freqs, const int32_t* pos, const int32_t* lens,
+                    void* dq, void* dk, float* dwq, float* dwk, void* ws, size_t ws_bytes, void* stream) {
+    g_err[0] = '\0';
+    dn::QkArgs a;
+    DN_TRY(qk_shape(shape, &a));
+    const bool norm = a.norm != DN_NORM_NONE;
+    size_t nq, nk, ndq, ndk;
+    DN_TRY(qk_strides(a, shape->Hq, shape->q_stride, false, "q", a.side[0].xs, &nq));
+    DN_TRY(qk_strides(a, shape->Hk, shape->k_stride, false, "k", a.side[1].xs, &nk));
+    DN_TRY(qk_strides(a, shape->Hq, shape->dq_stride, true, "dq", a.side[0].os, &ndq));
+    DN_TRY(qk_strides(a, shape->Hk, shape->dk_stride, true, "dk", a.side[1].os, &ndk));
+    const size_t E = a.bf16 ? 2 : 4, row = (size_t)a.B * a.T * a.d * E, nw = (size_t)a.d * 4;
+    const size_t nf = (size_t)a.rot * 4, np = qk_pos_bytes(shape), any = ndq + ndk;
+    const size_t nws = norm && (dwq || dwk) ? dn::qk_workspace_bytes(a) : 0;
+    if (!norm && (q || k || wq || wk)) return fail(DN_ERR_INVALID, "q, k, wq and wk must be NULL without a norm");
+    if ((dwq && !wq) || (dwk && !wk)) return fail(DN_ERR_INVALID, "a weight's gradient without the weight");
+    DN_TRY(need(q, norm ? nq : 0, "q"));
+    DN_TRY(need(k, norm ? nk : 0, "k"));
+    DN_TRY(need(freqs, any ? nf : 0, "freqs"));
+    DN_TRY(need(pos, any ? np : 0, "pos"));
+    DN_TRY(need(dyq, shape->Hq * row, "dyq"));
+    DN_TRY(need(dyk, shape->Hk * row, "dyk"));
+    DN_TRY(need(dq, ndq, "dq"));
+    DN_TRY(need(dk, ndk, "dk"));
+    if (ws_bytes < nws) return fail(DN_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, nws);
+    DN_TRY(need(ws, nws, "workspace"));
+    DN_TRY(check_buffers({{"q", q, nq, false},
+                          {"k", k, nk, false},
+                          {"dyq", dyq, shape->Hq * row, false},
+                          {"dyk", dyk, shape->Hk * row, false},
+                          {"wq", wq, nw, false},
+                          {"wk", wk, nw, false},
+                          {"freqs", freqs, nf, false},
+                          {"pos", pos, np, false},
+                          {"lens", lens, (size_t)a.B * 4, false},
+                          {"dq", dq, ndq, true},
+                          {"dk", dk, ndk, true},
+                          {"dwq", dwq, nw, true},
+                          {"dwk", dwk, nw, true},
+                          {"workspace", ws, nws, true}}));
+    a.freqs = freqs;
+    a.pos = pos;
+    a.lens = lens;
+    a.side[0].x = norm ? q : dyq, a.side[0].dy = dyq, a.side[0].w = wq, a.side[0].out = dq, a.side[0].dw = dwq;
+    a.side[1].x = norm ? k : dyk, a.side[1].dy = dyk, a.side[1].w = wk, a.side[1].out = dk, a.side[1].dw = dwk;
+    if (!norm) {   // a rotation's gradient is the rotation back
+        for (dn::QkSide& s : a.side) qk_dense(a, s.heads, s.xs);
+        a.back = 1;
+    }
+    const hipError_t e = norm ? dn::launch_qk_bwd(a, static_cast<char*>(ws), static_cast<hipStream_t>(stream))
+                              : dn::launch_qk_fwd(a, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(DN_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
     return DN_OK;
 }

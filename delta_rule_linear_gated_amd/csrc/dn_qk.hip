@@ -1,0 +1,92 @@
+// dn_qk.hip -- launches of the queries' and keys' norms and rotations
+// (dn_qk_kernels.h): the split of tokens and heads, and the sums of the weights' gradients.
+#include <algorithm>
+
+#include "dn_device.h"
+#include "dn_internal.h"
+#include "dn_qk.h"
+
+namespace dn {
+
+namespace {
+
+constexpr int kQkUnits = 256;   // compute units
+
+// Sum of the workgroups' partial dw: 16 channels a workgroup, 16 lanes (x 16 rows) over the entries.
+__global__ __launch_bounds__(256) void qk_dw_kernel(QkArgs a) {
+    __shared__ float part[16][17];
+    const int blocks = a.d / 16, sd = blockIdx.x / blocks, j = blockIdx.x % blocks * 16 + threadIdx.x % 16;
+    if (!a.side[sd].dw) return;
+    const int r = threadIdx.x / 16;
+    const long first = sd ? (long)a.groups[0] * a.tiles : 0, n = (long)a.groups[sd] * a.tiles;
+    float sum = 0.f;
+    for (long i = r; i < n; i += 16) sum += a.parts[(first + i) * a.d + j];
+    part[r][threadIdx.x % 16] = sum;
+    __syncthreads();
+    if (r) return;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += part[i][threadIdx.x];
+    a.side[sd].dw[j] = sum;
+}
+
+// Tokens a workgroup takes, heads a lane takes.  More heads a lane share its angles; fewer fill
+// the chip.
+void qk_split(QkArgs* a, bool bwd) {
+    const long tokens = (long)a->B * a->T, per_wg = 256 / (a->d / 8);
+    const long tiles = (tokens + per_wg - 1) / per_wg;
+    const int most = std::max(a->side[0].heads, a->side[1].heads);
+    int per = 8;
+    auto groups = [&](int side) { return (a->side[side].heads + per - 1) / per; };
+    while (per > 1 && (per >= 2 * most || tiles * (groups(0) + groups(1)) < 4 * kQkUnits)) per /= 2;
+    a->per = per;
+    a->groups[0] = groups(0);
+    a->groups[1] = groups(1);
+    const long all = std::max((long)a->groups[0] + a->groups[1], 1L);
+    a->tiles = (int)(bwd ? std::min<long>(tiles, std::max(8 * kQkUnits / all, 1L)) : tiles);
+}
+
+}  // namespace
+
+bool qk_fits(const QkArgs& in) {
+    QkArgs a = in;
+    qk_split(&a, false);   // the backward takes no more workgroups
+    return (long)a.tiles * ((long)a.groups[0] + a.groups[1]) < (1L << 32) / 256;
+}
+
+size_t qk_workspace_bytes(const QkArgs& in) {
+    QkArgs a = in;
+    if ((long)a.B * a.T == 0) return 0;
+    qk_split(&a, true);
+    return (size_t)a.tiles * (a.groups[0] + a.groups[1]) * a.d * 4;
+}
+
+hipError_t launch_qk_fwd(QkArgs a, hipStream_t s) {
+    if ((long)a.B * a.T * (a.side[0].heads + a.side[1].heads) == 0) return hipSuccess;
+    qk_split(&a, false);
+    prof_begin(s, "qk_fwd");
+    const hipError_t e = (a.bf16 ? qk_fwd_bf16 : qk_fwd_f32)(a, (unsigned)(a.tiles * (a.groups[0] + a.groups[1])), s);
+    prof_end(s);
+    return e;
+}
+
+hipError_t launch_qk_bwd(QkArgs a, char* ws, hipStream_t s) {
+    const bool none = (long)a.B * a.T * (a.side[0].heads + a.side[1].heads) == 0;
+    hipError_t e = hipSuccess;
+    qk_split(&a, true);
+    a.parts = reinterpret_cast<float*>(ws);
+    if (none) {
+        a.tiles = 0;   // sums of nothing
+    } else {
+        prof_begin(s, "qk_bwd");
+        e = (a.bf16 ? qk_bwd_bf16 : qk_bwd_f32)(a, (unsigned)(a.tiles * (a.groups[0] + a.groups[1])), s);
+        prof_end(s);
+    }
+    if (e != hipSuccess || !(a.side[0].dw || a.side[1].dw)) return e;
+    prof_begin(s, "qk_dw");
+    hipLaunchKernelGGL(qk_dw_kernel, dim3(2 * a.d / 16), dim3(256), 0, s, a);
+    prof_end(s);
+    return hipGetLastError();
+}
+
+}  // namespace dn

@@ -1,0 +1,6 @@
+// dn_qk_bwd_f32.hip -- kernels of dn_qk_kernels.h for fp32 rows, backward.
+#include "dn_qk_kernels.h"
+
+namespace dn {
+hipError_t qk_bwd_f32(const QkArgs& a, unsigned blocks, hipStream_t s) { return qk_bwd_type<float>(a, blocks, s); }
+}  // namespace dn

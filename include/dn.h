@@ -126,6 +126,11 @@ typedef enum {
  */
 #define DN_FLAG_NO_SCAN 2u
 
+/* The gated recurrence (dn_gated_scan_fwd and its relatives) weighs its input with
+ * 1 - exp(g_t), an input gate that closes as the forget gate opens.  Other entry points
+ * return DN_ERR_INVALID for it. */
+#define DN_FLAG_COUPLED 4u
+
 /*
  * Per-channel gate (DN_GATE_VECTOR): the C x C products split each pair's decay
  * at the gate of a 16-step block boundary (the centred contraction, ReWY
@@ -397,6 +402,103 @@ dn_status dn_tree_commit(const dn_shape* shape, const void* k, const float* u, c
 dn_status dn_tree_commit_counts(const dn_shape* shape, const void* k, const float* u, const float* g,
                                 const int32_t* parent, const int32_t* counts, const int32_t* accept, float* state,
                                 void* stream);
+
+/*
+ * Gated linear recurrence (the recurrence of this family with a state of one number a
+ * channel: no keys, no queries):
+ *     h_t = exp(g_t) h_{t-1} + w_t x_t,   o_t = h_t,   h_0 = h0, hT = h_T,
+ *     w_t = 1, or 1 - exp(g_t) with DN_FLAG_COUPLED,
+ * over whole sequences, its gradients and its recurrent form.
+ *   shape  : B, H >= 0, 0 <= T <= 2^30; dv in 1 .. 2^22, the channels of a head (any
+ *            number; H = 1 for channels without heads); dk, C, eps unused; dtype; gate
+ *            must be DN_GATE_VECTOR; flags 0 or DN_FLAG_COUPLED (others: DN_ERR_INVALID);
+ *            fewer than 2^28 channels in all (B*H*dv, each head's rounded up to 64)
+ *   inputs : x io [B][H][T][dv]; g fp32 [B][H][T][dv]; h0 fp32 [B][H][dv] (NULL = zero);
+ *            lens int32 [B] or NULL: the steps of each batch element (clamped to 0 .. T;
+ *            what the inputs hold from there on is not used, hT is the state after the
+ *            last step, o, dx and dg are zero there)
+ *   forward : o io like x; hT fp32 [B][H][dv] (NULL = not wanted); states (fp32,
+ *            dn_gated_scan_states_bytes: [B][H][ceil(T / 128)][dv], the state entering
+ *            each run of 128 steps; those behind a sequence's end are left as they were;
+ *            NULL = not saved)
+ *   backward: the vector-Jacobian products of L = <o, dout> + <hT, dhT> (dhT NULL = zero):
+ *            dx io, dg fp32 like g, dh0 fp32 (NULL = not wanted), from the states that the
+ *            forward saved for the same inputs (h0 is then not read) or, NULL, from h0
+ *   ws     : >= dn_gated_scan_workspace_bytes(shape, DN_PASS_FWD, DN_PASS_BWD with saved
+ *            states, or DN_PASS_BWD_RECOMPUTE without)
+ * Everything is held in fp32 between its inputs and outputs.  A decay below 2^-126 is zero
+ * (g < -87.34, -inf among them): it resets the state.  Positive gates grow the state;
+ * where they sum to more than 88 over some run of steps, results overflow (Inf or NaN)
+ * whatever the state holds.  NaN or Inf stays in its channel.  Layouts, validation and
+ * errors as for dn_chunk_fwd.
+ *
+ * dn_gated_scan_recurrent_fwd: T steps, the state (fp32 [B][H][dv]) updated in place; no
+ * workspace.
+ */
+size_t dn_gated_scan_states_bytes(const dn_shape* shape);
+size_t dn_gated_scan_workspace_bytes(const dn_shape* shape, int pass);
+dn_status dn_gated_scan_fwd(const dn_shape* shape, const void* x, const float* g, const int32_t* lens, const float* h0,
+                            void* o, float* hT, float* states, void* ws, size_t ws_bytes, void* stream);
+dn_status dn_gated_scan_bwd(const dn_shape* shape, const void* x, const float* g, const int32_t* lens, const float* h0,
+                            const void* dout, const float* dhT, const float* states, void* dx, float* dg, float* dh0,
+                            void* ws, size_t ws_bytes, void* stream);
+dn_status dn_gated_scan_recurrent_fwd(const dn_shape* shape, const void* x, const float* g, float* state, void* o,
+                                      void* stream);
+
+/*
+ * Queries and keys on their way to the operators above: each row (one head of one token)
+ * normalised, then rotated by its position, and written head by head, whatever order the
+ * projection left them in.  For a row x of d elements
+ *     n = x (s |x|^2 + eps)^{-1/2} * w      DN_NORM_L2: s = 1; DN_NORM_RMS: s = 1 / d;
+ *                                           DN_NORM_NONE: n = x
+ *     (y_i, y_j) = amplitude (n_i cos a - n_j sin a,  n_j cos a + n_i sin a)
+ * for the pairs of the first rot elements, m = 0 .. rot / 2 - 1, a = position * freqs[m]:
+ * DN_ROT_HALVES pairs (m, m + rot / 2), DN_ROT_NEIGHBOURS (2m, 2m + 1); the other elements
+ * keep n.  Scaled positions are a matter of freqs and amplitude.
+ *   shape  : B, Hq, Hk, T >= 0 (queries and keys may have different heads, either may
+ *            have none); B*T <= 2^30; d in {16, 32, 64, 128}; rot a multiple of 8, 0 .. d
+ *            (0: no rotation, then freqs and pos are not read); not both without a norm and
+ *            without a rotation (DN_ERR_UNSUPPORTED); eps >= 0 and amplitude finite;
+ *            strides in elements from one batch element, head and step to the next, >= 0
+ *            and multiples of 16 bytes (those of a dimension of size 1 are not read);
+ *            the rows themselves are dense
+ *   inputs : q, k io by q_stride and k_stride; wq, wk fp32 [d] or NULL (ones); freqs fp64
+ *            [rot / 2], the angle of one position in radians; pos: NULL for DN_POS_STEP (the
+ *            position is t), int32 [B] for DN_POS_START (pos[b] + t), int32 [B][T] for
+ *            DN_POS_EACH; any sign; lens int32 [B] or NULL: rows from there on are zero in
+ *            y, dq and dk, their inputs are not used
+ *   forward : yq io [B][Hq][T][d], yk io [B][Hk][T][d]
+ *   backward: from dyq, dyk (like yq, yk): dq, dk by dq_stride and dk_stride, whose rows may
+ *            not share memory; dwq, dwk fp32 [d] (NULL = not wanted), summed over all rows.
+ *            Without a norm q, k and the weights are NULL.  ws >= dn_qk_workspace_bytes
+ *            (only where dwq or dwk is wanted)
+ * Norms, angles (in fp64 up to the reduced angle) and rotations are held to fp32.  A row of
+ * zeros with eps == 0 gives NaN; the sum of squares overflows beyond 1.8e19.  NaN or Inf
+ * stays in its row (in its pair without a norm), and in dwq, dwk.  Errors as for
+ * dn_chunk_fwd.
+ */
+typedef enum { DN_NORM_NONE = 0, DN_NORM_L2 = 1, DN_NORM_RMS = 2 } dn_norm;
+typedef enum { DN_ROT_HALVES = 0, DN_ROT_NEIGHBOURS = 1 } dn_rot_layout;
+typedef enum { DN_POS_STEP = 0, DN_POS_START = 1, DN_POS_EACH = 2 } dn_pos_kind;
+
+typedef struct {
+    int32_t B, Hq, Hk, T, d, rot;
+    int32_t dtype;      /* dn_dtype */
+    int32_t norm;       /* dn_norm */
+    int32_t layout;     /* dn_rot_layout */
+    int32_t pos_kind;   /* dn_pos_kind */
+    float eps;          /* read with a norm */
+    float amplitude;    /* read with a rotation */
+    int64_t q_stride[3], k_stride[3];     /* batch, head, step */
+    int64_t dq_stride[3], dk_stride[3];   /* read by dn_qk_bwd */
+} dn_qk_shape;
+
+size_t dn_qk_workspace_bytes(const dn_qk_shape* shape);
+dn_status dn_qk_fwd(const dn_qk_shape* shape, const void* q, const void* k, const float* wq, const float* wk,
+                    const double* freqs, const int32_t* pos, const int32_t* lens, void* yq, void* yk, void* stream);
+dn_status dn_qk_bwd(const dn_qk_shape* shape, const void* q, const void* k, const void* dyq, const void* dyk,
+                    const float* wq, const float* wk, const double* freqs, const int32_t* pos, const int32_t* lens,
+                    void* dq, void* dk, float* dwq, float* dwk, void* ws, size_t ws_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* dn_status_string(dn_status status);
