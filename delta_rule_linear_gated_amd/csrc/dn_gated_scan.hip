@@ -3,15 +3,18 @@
 // its backward pass and its recurrent form.  Layouts as in include/dn.h.
 //
 // A step is the affine map h -> a h + b; a run of steps is the map {p, e}, p the product of
-// its decays and e its end from a zero state.  A workgroup owns a strip of 64 channels (a
-// lane each) and walks the steps in tiles: each of its 16 waves forms the map of its run of
-// the tile in registers, the waves exchange the maps through LDS (one barrier a tile), each
-// takes its run's first state through the maps before it and goes over its registers again
-// for the outputs.  All of a tile's rows are loaded while the one before is worked on, so
-// that every tensor is read once.  Strips alone fill the chip from 256 on; fewer are cut
-// into segments of the steps, whose maps a pass of its own forms first (gs_plan).
+// its decays and e its end from a zero state.  A workgroup works on tiles: a run of steps of a
+// strip of 64 channels (a lane each).  Each of its waves forms the map of its run of the tile
+// in registers, the waves exchange the maps through LDS (one barrier), each takes its run's
+// first state through the maps before it and goes over its registers again for the outputs.
+// All of a tile's rows are loaded while the one before is worked on, and every tensor is
+// read once.
 //
-// The backward walks the same tiles from the last step with r_t = a_t D_t, the cotangent
+// Enough strips: a workgroup walks the tiles of one strip, the state in a register.  Few
+// strips (gs_plan): the tiles of all strips are handed out in the order of their steps, and a
+// tile takes its first state from messages of the tiles before it in its strip (Chain).
+//
+// The backward goes from the last step with r_t = a_t D_t, the cotangent
 // that leaves step t to earlier ones:
 //     D_t = do_t + r_{t+1},   dx_t = w_t D_t,   dg_t = r_t (h_{t-1} - [coupled] x_t),
 // h inside a tile from the state saved at its start.
@@ -25,26 +28,27 @@ namespace dn {
 
 namespace {
 
-constexpr int kGsWaves = 16;
-constexpr int kGsRun = 16;                        // steps of a wave in a tile, forward
-constexpr int kGsRunB = kGsSaved / kGsWaves;      // and backward: a tile begins at a saved state
-constexpr int kGsTile = kGsWaves * kGsRun;
-constexpr int kGsMaxSeg = 64;
+constexpr int kGsWaves = 16, kGsRun = 16;         // forward, marching: waves, steps of a wave in a tile
+constexpr int kGsWavesC = 8, kGsRunC = 32;        // forward, chained
+constexpr int kGsWavesB = 8;                      // backward: a tile begins at a saved state
+constexpr int kGsRunB = kGsSaved / kGsWavesB;
+constexpr int gs_tile(bool chain) { return chain ? kGsWavesC * kGsRunC : kGsWaves * kGsRun; }
 constexpr int kGsUnits = 256;                     // compute units
-static_assert(kGsTile % kGsSaved == 0, "saved states lie at the starts of runs");
+static_assert(kGsSaved % kGsRun == 0 && kGsSaved % kGsRunC == 0, "saved states lie at the starts of runs");
 constexpr int kRange = 0x7fffff00;                // bytes of a buffer range, at most
 constexpr int kNowhere = 0x7ffffff0;              // an offset past every range: loads give zero, stores do nothing
 
 struct GsArgs {
     int BH, H, T, d;
-    int strips, nseg, seg_len;   // seg_len: steps
+    int strips, tiles;           // tiles of a strip
+    int reach;                   // a chained tile takes at most reach maps before its own
     int flat;                    // channel of a lane: 64 strip + lane of all, else of one head's row
     int NS;                      // saved states of a row
     const void *x, *y;           // y: dout
     const float* g;
     const int* lens;
     const float *first, *states_in;
-    float2* maps;                // [nseg][strips][64] of the segments
+    char* chain;                 // the next tile to hand out, then the messages (Chain)
     void* out;                   // o or dx; NULL: not wanted
     float *dg, *last, *states;
 };
@@ -60,11 +64,11 @@ __device__ __forceinline__ Lane gs_lane(const GsArgs& a, int strip, long& row0) 
     Lane l;
     const int lane = lane_id();
     if (a.flat) {
-        const long n0 = 64L * strip, n = n0 + lane;
+        const unsigned n0 = 64u * strip, n = n0 + lane, row = n / a.d;   // 2^28 channels at most
         row0 = n0 / a.d;
-        l.row = n / a.d;
-        l.c = (int)(n - l.row * a.d);
-        l.on = l.row < a.BH;
+        l.row = row;
+        l.c = n - row * a.d;
+        l.on = row < (unsigned)a.BH;
     } else {
         const int per = (a.d + 63) / 64;
         row0 = l.row = strip / per;
@@ -155,59 +159,133 @@ __device__ __forceinline__ float gs_rest(float g, float a) {
 
 __device__ __forceinline__ int uniform_wave() { return __builtin_amdgcn_readfirstlane(wave_id()); }
 
-// The state that enters the strip's segment, through the maps of the segments before it
-// (REV: behind it), shared by the waves.
-template <bool REV> __device__ __forceinline__ float gs_enter(const GsArgs& a, int strip, int seg, float first,
-                                                              float2 (*part)[64]) {
-    const int w = uniform_wave(), l = lane_id();
-    const int before = REV ? a.nseg - 1 - seg : seg;
-    if (before == 0) return first;
-    const int per = (before + kGsWaves - 1) / kGsWaves;
-    float2 m[kGsMaxSeg / kGsWaves];
-#pragma unroll
-    for (int i = 0; i < kGsMaxSeg / kGsWaves; ++i) {
-        const int s = min(w * per + i, before - 1);
-        m[i] = a.maps[((long)(REV ? a.nseg - 1 - s : s) * a.strips + strip) * 64 + l];
-    }
-    float p = 1.f, e = 0.f;
-#pragma unroll
-    for (int i = 0; i < kGsMaxSeg / kGsWaves; ++i)
-        if (i < per && w * per + i < before) {
-            p *= m[i].x;
-            e = fmaf(m[i].x, e, m[i].y);
-        }
-    part[w][l] = make_float2(p, e);
-    __syncthreads();
-    float h = first;
-#pragma unroll
-    for (int v = 0; v < kGsWaves; ++v) h = fmaf(part[v][l].x, h, part[v][l].y);
-    __syncthreads();
-    return h;
-}
+// Tiles of few strips: message `at` (the tile's place in the order in which they are handed
+// out) holds the 64 lanes' maps, a word of p and e each, and their last states.  A word is valid
+// by itself once it is not kUnset, to which a kernel sets all words before and which no value
+// is written as, so that nothing but the word has to be ordered.  A tile's first state is the last
+// state of the tile `reach` + 1 before it (or the strip's own), through the maps of the tiles
+// between: those need no state, so that tiles in flight at once do not wait for one
+// another's outputs.  The association depends on the tile alone, and so do the bits.
+//
+// Every wait ends: tiles are handed out in order by a counter, a workgroup finishes its own in
+// that order, and a tile waits for earlier ones only, so that the earliest unfinished tile
+// waits for nothing, however few workgroups run.
+struct Chain {
+    static constexpr int kEach = 16;   // maps that a wave gathers
+    static constexpr unsigned kUnset = 0xffffffffu;   // a NaN
+    static constexpr int kMessage = 64 * 8 + 64 * 4, kHead = 256;   // bytes
 
-// Forward.  MAPS: the segment's map only (all but the last segment); else outputs, saved
-// states and the last state, each where wanted.
-template <typename T, bool COUPLED, bool MAPS>
-__global__ __launch_bounds__(64 * kGsWaves) void gated_scan_fwd_kernel(GsArgs a) {
-    __shared__ float2 part[2][kGsWaves][64];
-    const int strip = blockIdx.x % a.strips, seg = blockIdx.x / a.strips;
+    static __device__ __forceinline__ char* message(const GsArgs& a, int at) { return a.chain + kHead + (long)at * kMessage; }
+    static __device__ __forceinline__ unsigned long long* map_of(const GsArgs& a, int at) {
+        return reinterpret_cast<unsigned long long*>(message(a, at)) + lane_id();
+    }
+    static __device__ __forceinline__ unsigned* last_of(const GsArgs& a, int at) {
+        return reinterpret_cast<unsigned*>(message(a, at) + 64 * 8) + lane_id();
+    }
+    static __device__ __forceinline__ unsigned bits(float v) {   // any NaN as the quiet one
+        return v == v ? __builtin_bit_cast(unsigned, v) : 0x7fc00000u;
+    }
+    static __device__ __forceinline__ void put_map(const GsArgs& a, int at, float p, float e) {
+        __hip_atomic_store(map_of(a, at), (unsigned long long)bits(e) << 32 | bits(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    static __device__ __forceinline__ void put_last(const GsArgs& a, int at, float h) {
+        __hip_atomic_store(last_of(a, at), bits(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    static __device__ __forceinline__ unsigned long long get_map(const GsArgs& a, int at) {
+        return __hip_atomic_load(map_of(a, at), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    static __device__ __forceinline__ unsigned get_last(const GsArgs& a, int at) {
+        return __hip_atomic_load(last_of(a, at), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+
+    // The next tile (every lane of the wave gets it), -1: none is left.
+    static __device__ __forceinline__ int claim(const GsArgs& a) {
+        int n = 0;
+        if (lane_id() == 0)
+            n = (int)__hip_atomic_fetch_add(reinterpret_cast<unsigned*>(a.chain), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        n = __builtin_amdgcn_readfirstlane(n);
+        return n < a.strips * a.tiles ? n : -1;
+    }
+    // Waves that gather: the first ones.
+    static __device__ __forceinline__ int gatherers(const GsArgs& a) { return (a.reach + kEach - 1) / kEach; }
+    // Wave w's share of what comes before tile `at`, k-th of its strip: a map, or (wave 0)
+    // the state after its share, from the state before or from `first`.
+    static __device__ __forceinline__ float2 gather(const GsArgs& a, int at, int k, int w, float first) {
+        const int n = min(k, a.reach), lo = w * kEach, m = min(n - lo, kEach);   // m maps, oldest first
+        float p = w == 0 ? 0.f : 1.f, e = 0.f;
+        if (w == 0) {
+            e = first;
+            if (k > n) {
+                const int from = at - (n + 1) * a.strips;
+                unsigned u = get_last(a, from);
+                while (!__all(u != kUnset)) {
+                    __builtin_amdgcn_s_sleep(1);
+                    u = get_last(a, from);
+                }
+                e = __builtin_bit_cast(float, u);
+            }
+        }
+        constexpr int BATCH = 8;
+        for (int i0 = 0; i0 < m; i0 += BATCH) {
+            unsigned long long u[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) u[i] = get_map(a, at - (n - lo - min(i0 + i, m - 1)) * a.strips);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                if (i0 + i >= m) break;
+                while (!__all((unsigned)u[i] != kUnset)) {
+                    __builtin_amdgcn_s_sleep(1);
+                    u[i] = get_map(a, at - (n - lo - (i0 + i)) * a.strips);
+                }
+                const float q = __builtin_bit_cast(float, (unsigned)u[i]);
+                if (w > 0) p *= q;
+                e = fmaf(q, e, __builtin_bit_cast(float, (unsigned)(u[i] >> 32)));
+            }
+        }
+        return make_float2(p, e);
+    }
+};
+
+// Forward.  Outputs, saved states and the last state, each where wanted.
+template <typename T, bool COUPLED, bool CHAIN>
+__global__ __launch_bounds__(64 * (CHAIN ? kGsWavesC : kGsWaves)) void gated_scan_fwd_kernel(GsArgs a) {
+    constexpr int R = CHAIN ? kGsRunC : kGsRun, W = CHAIN ? kGsWavesC : kGsWaves, TILE = W * R;
+    __shared__ float2 part[2][W][64], gathered[CHAIN ? W : 1][64];
+    __shared__ int claimed[2];
     const int w = uniform_wave(), lane = lane_id();
+    const int gatherers = CHAIN ? Chain::gatherers(a) : 0;
+    int at = 0, next = CHAIN ? -1 : a.tiles > 1 ? 1 : -1, after = -1;
+    if (CHAIN) {
+        if (w == 0) at = Chain::claim(a);
+        if (w == 0 && lane == 0) claimed[0] = at;
+        __syncthreads();
+        at = __builtin_amdgcn_readfirstlane(claimed[0]);
+        if (at < 0) return;
+        __syncthreads();
+    } else if (a.tiles == 0) {
+        at = -1;
+    }
     long row0;
-    const Lane l = gs_lane(a, strip, row0);
-    const int begin = seg * a.seg_len, end = min(a.T, begin + a.seg_len), len = min(l.len, end);
-    constexpr int R = kGsRun;
-    float h = !MAPS && a.first && l.on ? a.first[l.row * a.d + l.c] : 0.f, p = 1.f;
-    if (!MAPS) h = gs_enter<false>(a, strip, seg, h, part[0]);
+    Lane l = gs_lane(a, CHAIN ? at % a.strips : blockIdx.x, row0);
+    float h = a.first && l.on ? a.first[l.row * a.d + l.c] : 0.f;
     unsigned gn[R], xn[R];
-    auto fetch = [&](int t) {
-        const bool full = __all(!l.on || len >= t + R);
-        gs_load<float, R>(gn, a.g, a, row0, l, t, len, full);
-        gs_load<T, R>(xn, a.x, a, row0, l, t, len, full);
+    auto fetch = [&](const Lane& l, long row0, int t) {
+        const bool full = __all(!l.on || l.len >= t + R);
+        gs_load<float, R>(gn, a.g, a, row0, l, t, l.len, full);
+        gs_load<T, R>(xn, a.x, a, row0, l, t, l.len, full);
     };
-    int t0 = begin, buf = 0;
-    if (__any(len > t0)) fetch(t0 + w * R);
-    for (; __any(len > t0); t0 += kGsTile, buf ^= 1) {
-        const int t = t0 + w * R;
+    auto prefetch = [&]() {   // the next tile's rows
+        if (CHAIN) {
+            long r;
+            const Lane m = gs_lane(a, next % a.strips, r);
+            fetch(m, r, next / a.strips * TILE + w * R);
+        } else {
+            fetch(l, row0, next * TILE + w * R);
+        }
+    };
+    if (at >= 0) fetch(l, row0, (CHAIN ? at / a.strips : 0) * TILE + w * R);
+    for (int buf = 0; at >= 0; buf ^= 1) {
+        const int k = CHAIN ? at / a.strips : at, t = k * TILE + w * R;
         float f[R], b[R], sum = 0.f, e = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -218,109 +296,104 @@ __global__ __launch_bounds__(64 * kGsWaves) void gated_scan_fwd_kernel(GsArgs a)
             sum += g;
             e = fmaf(f[i], e, b[i]);
         }
-        if (__any(len > t0 + kGsTile)) fetch(t + kGsTile);
+        // a wave that gathers would wait for its rows with the messages: it loads them after
+        bool ahead = next >= 0 && w >= gatherers;
+        if (ahead) prefetch();
         part[buf][w][lane] = make_float2(gs_exp(sum), e);
         __syncthreads();
+        if (CHAIN) {
+            if (w == 0) {
+                float p = 1.f, q = 0.f;
+#pragma unroll
+                for (int v = 0; v < W; ++v) {
+                    const float2 m = part[buf][v][lane];
+                    p *= m.x;
+                    q = fmaf(m.x, q, m.y);
+                }
+                Chain::put_map(a, at, p, q);
+            }
+            if (w == W - 1) {   // tiles to work on after the next
+                const int n = next < 0 ? Chain::claim(a) : -1, m = Chain::claim(a);
+                if (lane == 0) claimed[0] = n, claimed[1] = m;
+            }
+            if (w < gatherers)
+                gathered[w][lane] = Chain::gather(a, at, k, w, a.first && l.on ? a.first[l.row * a.d + l.c] : 0.f);
+            __syncthreads();
+            h = gathered[0][lane].y;
+            for (int v = 1; v < gatherers; ++v) h = fmaf(gathered[v][lane].x, h, gathered[v][lane].y);
+            if (next < 0) next = __builtin_amdgcn_readfirstlane(claimed[0]);
+            after = __builtin_amdgcn_readfirstlane(claimed[1]);
+        } else {
+            after = next >= 0 && next + 1 < a.tiles ? next + 1 : -1;
+        }
         float mine = h;
 #pragma unroll
-        for (int v = 0; v < kGsWaves; ++v) {
+        for (int v = 0; v < W; ++v) {
             const float2 m = part[buf][v][lane];
             if (v == w) mine = h;
             h = fmaf(m.x, h, m.y);
-            if (MAPS) p *= m.x;
         }
-        if (MAPS) continue;
-        if (a.states && l.on && t % kGsSaved == 0 && t < end) a.states[(l.row * a.NS + t / kGsSaved) * a.d + l.c] = mine;
-        if (!a.out) continue;
-        const bool full = __all(!l.on || len >= t + R);
+        if (CHAIN && w == W - 1) Chain::put_last(a, at, h);
+        if (CHAIN && !ahead && next >= 0) prefetch();
+        if (a.states && l.on && t % kGsSaved == 0 && t < a.T) a.states[(l.row * a.NS + t / kGsSaved) * a.d + l.c] = mine;
+        if (a.out) {
+            const bool full = __all(!l.on || l.len >= t + R);
 #pragma unroll
-        for (int i = 0; i < R; ++i) b[i] = mine = fmaf(f[i], mine, b[i]);
-        gs_store<T, R>(b, a.out, a, row0, l, t, len, full);
+            for (int i = 0; i < R; ++i) b[i] = mine = fmaf(f[i], mine, b[i]);
+            gs_store<T, R>(b, a.out, a, row0, l, t, l.len, full);
+        }
+        if (k == a.tiles - 1 && w == 0 && a.last && l.on) a.last[l.row * a.d + l.c] = h;
+        at = next;
+        next = after;
+        if (CHAIN && at >= 0) l = gs_lane(a, at % a.strips, row0);
     }
-    if (MAPS) {
-        if (w == 0) a.maps[((long)seg * a.strips + strip) * 64 + lane] = make_float2(p, h);
-        return;
-    }
-    if (a.out) {   // the tiles that no sequence of the strip reaches
-        float none[R] = {};
-        for (; t0 < end; t0 += kGsTile) gs_store<T, R>(none, a.out, a, row0, l, t0 + w * R, len, false);
-    }
-    if (a.last && seg == a.nseg - 1 && w == 0 && l.on) a.last[l.row * a.d + l.c] = h;
+    if (!CHAIN && a.tiles == 0 && a.last && w == 0 && l.on) a.last[l.row * a.d + l.c] = h;
 }
 
-// The maps of the segments from their last step back: r -> a (r + do).
-template <typename T> __global__ __launch_bounds__(64 * kGsWaves) void gated_scan_back_kernel(GsArgs a) {
-    __shared__ float2 part[2][kGsWaves][64];
-    const int strip = blockIdx.x % a.strips, seg = blockIdx.x / a.strips + 1;
+// Backward: tiles from the last step on, k the number of tiles behind this one.
+template <typename T, bool COUPLED, bool CHAIN>
+__global__ __launch_bounds__(64 * kGsWavesB) void gated_scan_bwd_kernel(GsArgs a) {
+    constexpr int R = kGsRunB, W = kGsWavesB;
+    __shared__ float2 fore[2][W][64], back[2][W][64], gathered[CHAIN ? W : 1][64];
+    __shared__ int claimed[2];
     const int w = uniform_wave(), lane = lane_id();
-    long row0;
-    const Lane l = gs_lane(a, strip, row0);
-    const int begin = seg * a.seg_len, end = min(a.T, begin + a.seg_len), len = min(l.len, end);
-    constexpr int R = kGsRun;
-    float r = 0.f, p = 1.f;
-    unsigned gn[R], yn[R];
-    auto fetch = [&](int t) {
-        const bool full = __all(!l.on || len >= t + R);
-        gs_load<float, R>(gn, a.g, a, row0, l, t, len, full);
-        gs_load<T, R>(yn, a.y, a, row0, l, t, len, full);
-    };
-    int t0 = begin + (end - begin - 1) / kGsTile * kGsTile, buf = 0;
-    while (t0 >= begin && !__any(len > t0)) t0 -= kGsTile;
-    if (t0 >= begin) fetch(t0 + w * R);
-    for (; t0 >= begin; t0 -= kGsTile, buf ^= 1) {
-        float f[R], y[R], sum = 0.f, e = 0.f;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float g = Bits<float>::value(gn[i]);
-            f[i] = gs_exp(g);
-            y[i] = Bits<T>::value(yn[i]);
-            sum += g;
-        }
-        if (t0 > begin) fetch(t0 - kGsTile + w * R);
-#pragma unroll
-        for (int i = R - 1; i >= 0; --i) e = f[i] * (e + y[i]);
-        part[buf][w][lane] = make_float2(gs_exp(sum), e);
+    const int gatherers = CHAIN ? Chain::gatherers(a) : 0;
+    int at = 0, next = CHAIN ? -1 : a.tiles > 1 ? 1 : -1, after = -1;
+    if (CHAIN) {
+        if (w == 0) at = Chain::claim(a);
+        if (w == 0 && lane == 0) claimed[0] = at;
         __syncthreads();
-#pragma unroll
-        for (int v = kGsWaves - 1; v >= 0; --v) {
-            const float2 m = part[buf][v][lane];
-            r = fmaf(m.x, r, m.y);
-            p *= m.x;
-        }
+        at = __builtin_amdgcn_readfirstlane(claimed[0]);
+        if (at < 0) return;
+        __syncthreads();
+    } else if (a.tiles == 0) {
+        at = -1;
     }
-    if (w == 0) a.maps[((long)seg * a.strips + strip) * 64 + lane] = make_float2(p, r);
-}
-
-template <typename T, bool COUPLED>
-__global__ __launch_bounds__(64 * kGsWaves) void gated_scan_bwd_kernel(GsArgs a) {
-    __shared__ float2 ahead[2][kGsWaves][64], back[2][kGsWaves][64];
-    const int strip = blockIdx.x % a.strips, seg = blockIdx.x / a.strips;
-    const int w = uniform_wave(), lane = lane_id();
     long row0;
-    const Lane l = gs_lane(a, strip, row0);
-    const int begin = seg * a.seg_len, end = min(a.T, begin + a.seg_len), len = min(l.len, end);
-    constexpr int R = kGsRunB;
-    constexpr int TILE = kGsWaves * R;
+    Lane l = gs_lane(a, CHAIN ? at % a.strips : blockIdx.x, row0);
     float r = a.first && l.on ? a.first[l.row * a.d + l.c] : 0.f;
-    r = gs_enter<true>(a, strip, seg, r, back[0]);
     unsigned gn[R], xn[R], yn[R];
-    float hn;
-    auto fetch = [&](int t0) {
-        const int t = t0 + w * R;
-        const bool full = __all(!l.on || len >= t + R);
-        gs_load<float, R>(gn, a.g, a, row0, l, t, len, full);
-        gs_load<T, R>(xn, a.x, a, row0, l, t, len, full);
-        gs_load<T, R>(yn, a.y, a, row0, l, t, len, full);
-        hn = len > t0 ? a.states_in[(l.row * a.NS + t0 / kGsSaved) * a.d + l.c] : 0.f;
+    float hn = 0.f;
+    auto fetch = [&](const Lane& l, long row0, int k) {
+        const int t0 = (a.tiles - 1 - k) * kGsSaved, t = t0 + w * R;
+        const bool full = __all(!l.on || l.len >= t + R);
+        gs_load<float, R>(gn, a.g, a, row0, l, t, l.len, full);
+        gs_load<T, R>(xn, a.x, a, row0, l, t, l.len, full);
+        gs_load<T, R>(yn, a.y, a, row0, l, t, l.len, full);
+        hn = l.len > t0 ? a.states_in[(l.row * a.NS + t0 / kGsSaved) * a.d + l.c] : 0.f;
     };
-    int t0 = begin + (end > begin ? (end - begin - 1) / TILE * TILE : -TILE), buf = 0;
-    for (float none[R] = {}; t0 >= begin && !__any(len > t0); t0 -= TILE) {
-        gs_store<T, R>(none, a.out, a, row0, l, t0 + w * R, len, false);
-        gs_store<float, R>(none, a.dg, a, row0, l, t0 + w * R, len, false);
-    }
-    if (t0 >= begin) fetch(t0);
-    for (; t0 >= begin; t0 -= TILE, buf ^= 1) {
-        const int t = t0 + w * R;
+    auto prefetch = [&]() {
+        if (CHAIN) {
+            long r;
+            const Lane m = gs_lane(a, next % a.strips, r);
+            fetch(m, r, next / a.strips);
+        } else {
+            fetch(l, row0, next);
+        }
+    };
+    if (at >= 0) fetch(l, row0, CHAIN ? at / a.strips : 0);
+    for (int buf = 0; at >= 0; buf ^= 1) {
+        const int k = CHAIN ? at / a.strips : at, t = (a.tiles - 1 - k) * kGsSaved + w * R;
         float f[R], x[R], y[R], wt[R], h = hn, sum = 0.f, e = 0.f, q = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -332,24 +405,52 @@ __global__ __launch_bounds__(64 * kGsWaves) void gated_scan_bwd_kernel(GsArgs a)
             sum += g;
             e = fmaf(f[i], e, wt[i] * x[i]);
         }
-        if (t0 > begin) fetch(t0 - TILE);
+        bool ahead = next >= 0 && w >= gatherers;
+        if (ahead) prefetch();
 #pragma unroll
         for (int i = R - 1; i >= 0; --i) q = f[i] * (q + y[i]);
         const float p = gs_exp(sum);
-        ahead[buf][w][lane] = make_float2(p, e);
+        fore[buf][w][lane] = make_float2(p, e);
         back[buf][w][lane] = make_float2(p, q);
         __syncthreads();
+        if (CHAIN) {
+            if (w == 0) {
+                float p = 1.f, q = 0.f;
+#pragma unroll
+                for (int v = W - 1; v >= 0; --v) {
+                    const float2 m = back[buf][v][lane];
+                    p *= m.x;
+                    q = fmaf(m.x, q, m.y);
+                }
+                Chain::put_map(a, at, p, q);
+            }
+            if (w == W - 1) {
+                const int n = next < 0 ? Chain::claim(a) : -1, m = Chain::claim(a);
+                if (lane == 0) claimed[0] = n, claimed[1] = m;
+            }
+            if (w < gatherers)
+                gathered[w][lane] = Chain::gather(a, at, k, w, a.first && l.on ? a.first[l.row * a.d + l.c] : 0.f);
+            __syncthreads();
+            r = gathered[0][lane].y;
+            for (int v = 1; v < gatherers; ++v) r = fmaf(gathered[v][lane].x, r, gathered[v][lane].y);
+            if (next < 0) next = __builtin_amdgcn_readfirstlane(claimed[0]);
+            after = __builtin_amdgcn_readfirstlane(claimed[1]);
+        } else {
+            after = next >= 0 && next + 1 < a.tiles ? next + 1 : -1;
+        }
         float mine = r;
 #pragma unroll
-        for (int v = kGsWaves - 1; v >= 0; --v) {
+        for (int v = W - 1; v >= 0; --v) {
             const float2 m = back[buf][v][lane];
             if (v == w) mine = r;
             r = fmaf(m.x, r, m.y);
         }
+        if (CHAIN && w == W - 1) Chain::put_last(a, at, r);
+        if (CHAIN && !ahead && next >= 0) prefetch();
 #pragma unroll
-        for (int v = 0; v < kGsWaves - 1; ++v)
+        for (int v = 0; v < W - 1; ++v)
             if (v < w) {
-                const float2 m = ahead[buf][v][lane];
+                const float2 m = fore[buf][v][lane];
                 h = fmaf(m.x, h, m.y);
             }
         float before[R];
@@ -365,11 +466,23 @@ __global__ __launch_bounds__(64 * kGsWaves) void gated_scan_bwd_kernel(GsArgs a)
             x[i] = COUPLED ? wt[i] * D : D;
             y[i] = mine * before[i];
         }
-        const bool full = __all(!l.on || len >= t + R);
-        gs_store<T, R>(x, a.out, a, row0, l, t, len, full);
-        gs_store<float, R>(y, a.dg, a, row0, l, t, len, full);
+        const bool full = __all(!l.on || l.len >= t + R);
+        gs_store<T, R>(x, a.out, a, row0, l, t, l.len, full);
+        gs_store<float, R>(y, a.dg, a, row0, l, t, l.len, full);
+        if (k == a.tiles - 1 && w == 0 && a.last && l.on) a.last[l.row * a.d + l.c] = r;
+        at = next;
+        next = after;
+        if (CHAIN && at >= 0) l = gs_lane(a, at % a.strips, row0);
     }
-    if (a.last && seg == 0 && w == 0 && l.on) a.last[l.row * a.d + l.c] = r;
+    if (!CHAIN && a.tiles == 0 && a.last && w == 0 && l.on) a.last[l.row * a.d + l.c] = r;
+}
+
+// Before a chain: the counter is zero, every word of the messages unset.
+__global__ __launch_bounds__(256) void gated_scan_clear_kernel(uint4* p, long n) {
+    for (long i = blockIdx.x * 256L + threadIdx.x; i < n; i += gridDim.x * 256L) {
+        const unsigned v = i < Chain::kHead / 16 ? 0u : Chain::kUnset;
+        p[i] = make_uint4(v, v, v, v);
+    }
 }
 
 // Recurrent form: a thread a channel, the state in a register over the steps; bytes and
@@ -394,7 +507,7 @@ __global__ __launch_bounds__(256) void gated_scan_recurrent_kernel(const T* x, c
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct GsPlan {
-    int flat, nseg, seg_len;
+    int flat, chain, tiles, reach;
     long strips;
 };
 
@@ -406,26 +519,27 @@ void gs_strips(const GsProblem& pr, GsPlan* p) {
     p->flat = rows * pr.T < kRange / 4 / pr.d;
     p->strips = p->flat ? (BH * pr.d + 63) / 64 : BH * ((pr.d + 63) / 64);
 }
-GsPlan gs_plan(const GsProblem& pr) {
-    GsPlan p;
+GsPlan gs_plan(const GsProblem& pr, bool bwd) {
+    GsPlan p{};
     gs_strips(pr, &p);
-    const int tiles = (int)(((long)pr.T + kGsTile - 1) / kGsTile);
-    int nseg = 1;
-    if (p.strips > 0 && p.strips < kGsUnits && tiles >= 4)
-        nseg = (int)std::min<long>({kGsMaxSeg, tiles / 2, (kGsUnits + p.strips - 1) / p.strips});
-    const int len = tiles > 0 ? (tiles + nseg - 1) / nseg : 1;
-    p.nseg = tiles > 0 ? (tiles + len - 1) / len : 1;
-    p.seg_len = (int)std::min<long>((long)len * kGsTile, 0x7fffff00);
+    p.chain = p.strips > 0 && p.strips < kGsUnits && pr.T > 2 * (bwd ? kGsSaved : gs_tile(true));
+    const int tile = bwd ? kGsSaved : gs_tile(p.chain);
+    p.tiles = (int)(((long)pr.T + tile - 1) / tile);
+    // the tiles of a strip that are in flight at once
+    if (p.chain) p.reach = (int)std::min<long>((bwd ? kGsWavesB : kGsWavesC) * Chain::kEach, std::max<long>(4, kGsUnits / p.strips));
     return p;
 }
 
+size_t gs_chain_bytes(const GsPlan& p) { return p.chain ? Chain::kHead + (size_t)p.strips * p.tiles * Chain::kMessage : 0; }
+
 struct GsWs {
-    size_t maps, states, total;
+    size_t states, total;   // the messages lie at the start
 };
 GsWs gs_ws(const GsProblem& pr, int pass) {
-    const GsPlan p = gs_plan(pr);
     GsWs w{};
-    w.states = p.nseg > 1 ? al256((size_t)p.nseg * p.strips * 64 * 8) : 0;
+    if (pass != 1) w.states = gs_chain_bytes(gs_plan(pr, false));
+    if (pass != 0) w.states = std::max(w.states, gs_chain_bytes(gs_plan(pr, true)));
+    w.states = al256(w.states);
     w.total = w.states + (pass == 2 ? al256(gs_states_bytes(pr)) : 0);
     return w;
 }
@@ -437,52 +551,62 @@ GsArgs gs_args(const GsProblem& pr, const GsPlan& p, const void* x, const float*
     a.T = pr.T;
     a.d = pr.d;
     a.strips = (int)p.strips;
-    a.nseg = p.nseg;
-    a.seg_len = p.seg_len;
+    a.tiles = p.tiles;
+    a.reach = p.reach;
     a.flat = p.flat;
     a.NS = (int)(((long)pr.T + kGsSaved - 1) / kGsSaved);
     a.x = x;
     a.g = g;
     a.lens = lens;
-    a.maps = reinterpret_cast<float2*>(ws);
+    a.chain = ws;
     return a;
 }
 
-template <typename T, bool COUPLED> hipError_t fwd_launch(const GsArgs& a, hipStream_t s) {
-    const dim3 block(64 * kGsWaves);
-    if (a.nseg > 1) {
-        prof_begin(s, "gated_scan_maps");
-        hipLaunchKernelGGL((gated_scan_fwd_kernel<T, COUPLED, true>), dim3(a.strips * (a.nseg - 1)), block, 0, s, a);
-        prof_end(s);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
+hipError_t clear_chain(const GsPlan& p, char* ws, hipStream_t s) {
+    const long n = (long)(gs_chain_bytes(p) / 16);
+    prof_begin(s, "gated_scan_clear");
+    hipLaunchKernelGGL(gated_scan_clear_kernel, dim3((unsigned)std::min<long>((n + 255) / 256, 4 * kGsUnits)), dim3(256), 0, s,
+                       reinterpret_cast<uint4*>(ws), n);
+    prof_end(s);
+    return hipGetLastError();
+}
+unsigned gs_grid(const GsPlan& p) { return (unsigned)(p.chain ? std::min<long>(p.strips * p.tiles, kGsUnits) : p.strips); }
+
+template <typename T, bool COUPLED> hipError_t fwd_launch(const GsPlan& p, const GsArgs& a, hipStream_t s) {
+    const dim3 grid(gs_grid(p)), block(64 * (p.chain ? kGsWavesC : kGsWaves));
     prof_begin(s, "gated_scan_fwd");
-    hipLaunchKernelGGL((gated_scan_fwd_kernel<T, COUPLED, false>), dim3(a.strips * a.nseg), block, 0, s, a);
+    if (p.chain)
+        hipLaunchKernelGGL((gated_scan_fwd_kernel<T, COUPLED, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((gated_scan_fwd_kernel<T, COUPLED, false>), grid, block, 0, s, a);
     prof_end(s);
     return hipGetLastError();
 }
-template <typename T, bool COUPLED> hipError_t bwd_launch(const GsArgs& a, hipStream_t s) {
-    const dim3 block(64 * kGsWaves);
-    if (a.nseg > 1) {
-        prof_begin(s, "gated_scan_back");
-        hipLaunchKernelGGL((gated_scan_back_kernel<T>), dim3(a.strips * (a.nseg - 1)), block, 0, s, a);
-        prof_end(s);
-        const hipError_t e = hipGetLastError();
+template <typename T, bool COUPLED> hipError_t bwd_launch(const GsPlan& p, const GsArgs& a, hipStream_t s) {
+    const dim3 grid(gs_grid(p)), block(64 * kGsWavesB);
+    prof_begin(s, "gated_scan_bwd");
+    if (p.chain)
+        hipLaunchKernelGGL((gated_scan_bwd_kernel<T, COUPLED, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((gated_scan_bwd_kernel<T, COUPLED, false>), grid, block, 0, s, a);
+    prof_end(s);
+    return hipGetLastError();
+}
+hipError_t fwd_any(const GsProblem& pr, const GsPlan& p, const GsArgs& a, hipStream_t s) {
+    if (p.chain) {
+        const hipError_t e = clear_chain(p, a.chain, s);
         if (e != hipSuccess) return e;
     }
-    prof_begin(s, "gated_scan_bwd");
-    hipLaunchKernelGGL((gated_scan_bwd_kernel<T, COUPLED>), dim3(a.strips * a.nseg), block, 0, s, a);
-    prof_end(s);
-    return hipGetLastError();
+    if (pr.bf16) return pr.coupled ? fwd_launch<bf16, true>(p, a, s) : fwd_launch<bf16, false>(p, a, s);
+    return pr.coupled ? fwd_launch<float, true>(p, a, s) : fwd_launch<float, false>(p, a, s);
 }
-hipError_t fwd_any(const GsProblem& pr, const GsArgs& a, hipStream_t s) {
-    if (pr.bf16) return pr.coupled ? fwd_launch<bf16, true>(a, s) : fwd_launch<bf16, false>(a, s);
-    return pr.coupled ? fwd_launch<float, true>(a, s) : fwd_launch<float, false>(a, s);
-}
-hipError_t bwd_any(const GsProblem& pr, const GsArgs& a, hipStream_t s) {
-    if (pr.bf16) return pr.coupled ? bwd_launch<bf16, true>(a, s) : bwd_launch<bf16, false>(a, s);
-    return pr.coupled ? bwd_launch<float, true>(a, s) : bwd_launch<float, false>(a, s);
+hipError_t bwd_any(const GsProblem& pr, const GsPlan& p, const GsArgs& a, hipStream_t s) {
+    if (p.chain) {
+        const hipError_t e = clear_chain(p, a.chain, s);
+        if (e != hipSuccess) return e;
+    }
+    if (pr.bf16) return pr.coupled ? bwd_launch<bf16, true>(p, a, s) : bwd_launch<bf16, false>(p, a, s);
+    return pr.coupled ? bwd_launch<float, true>(p, a, s) : bwd_launch<float, false>(p, a, s);
 }
 
 }  // namespace
@@ -500,27 +624,29 @@ bool gs_fits(const GsProblem& pr) {
 
 hipError_t launch_gated_scan_fwd(const GsProblem& pr, const GsFwd& f, char* ws, hipStream_t s) {
     if (pr.B == 0 || pr.H == 0) return hipSuccess;
-    GsArgs a = gs_args(pr, gs_plan(pr), f.x, f.g, f.lens, ws);
+    const GsPlan p = gs_plan(pr, false);
+    GsArgs a = gs_args(pr, p, f.x, f.g, f.lens, ws);
     a.first = f.h0;
     a.out = f.o;
     a.last = f.hT;
     a.states = f.states;
-    return fwd_any(pr, a, s);
+    return fwd_any(pr, p, a, s);
 }
 
 hipError_t launch_gated_scan_bwd(const GsProblem& pr, const GsBwd& f, char* ws, hipStream_t s) {
     if (pr.B == 0 || pr.H == 0) return hipSuccess;
-    const GsPlan p = gs_plan(pr);
     const float* states = f.states;
-    if (!states) {
+    if (!states && pr.T > 0) {
         float* again = reinterpret_cast<float*>(ws + gs_ws(pr, 2).states);
+        const GsPlan p = gs_plan(pr, false);
         GsArgs a = gs_args(pr, p, f.x, f.g, f.lens, ws);
         a.first = f.h0;
         a.states = again;
-        const hipError_t e = fwd_any(pr, a, s);
+        const hipError_t e = fwd_any(pr, p, a, s);
         if (e != hipSuccess) return e;
         states = again;
     }
+    const GsPlan p = gs_plan(pr, true);
     GsArgs a = gs_args(pr, p, f.x, f.g, f.lens, ws);
     a.y = f.dout;
     a.first = f.dhT;
@@ -528,7 +654,7 @@ hipError_t launch_gated_scan_bwd(const GsProblem& pr, const GsBwd& f, char* ws, 
     a.out = f.dx;
     a.dg = f.dg;
     a.last = f.dh0;
-    return bwd_any(pr, a, s);
+    return bwd_any(pr, p, a, s);
 }
 
 hipError_t launch_gated_scan_recurrent(const GsProblem& pr, const void* x, const float* g, float* state, void* o,
