@@ -66,8 +66,8 @@ class QKShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32), ("T", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("dtype", ctypes.c_int32), ("norm", ctypes.c_int32),
                 ("layout", ctypes.c_int32), ("pos_kind", ctypes.c_int32), ("eps", ctypes.c_float),
-                ("amplitude", ctypes.c_float), ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
-                ("dq_stride", ctypes.c_int64 * 3), ("dk_stride", ctypes.c_int64 * 3)]
+                ("amplitude", ctypes.c_float)] + [   # four int64_t[3], entry by entry: an array object costs 0.4 us
+                    (f"{n}_stride{i}", ctypes.c_int64) for n in ("q", "k", "dq", "dk") for i in range(3)]
 
 
 _lib = None
@@ -922,30 +922,40 @@ def rotary_freqs(rot, base=10000.0, scaling=None, factor=1.0, trained=None, fast
 _NORMS = {"l2": DN_NORM_L2, "rms": DN_NORM_RMS}
 
 
-def _qk_args(sides, weights, norm, eps, freqs, pos, interleaved, amplitude, lens, grads=()):
-    """Shape descriptor of checked tensors.  ``sides``: (name, q or k or None), rows [B,heads,T,d] in any order of the
-    dimensions but the last; ``grads``: (name, tensor, dense like that side)."""
-    (qn, q), (kn, k) = sides
-    one = q if q is not None else k
+def _qk_args(q, k, wq, wk, norm, eps, freqs, pos, interleaved, amplitude, lens, dyq=None, dyk=None, dq=None, dk=None,
+             names=("q", "k")):
+    """Shape descriptor of checked tensors: rows q, k [B,heads,T,d] (either None) in any order of the dimensions but the
+    last, dyq, dyk dense like them; dq, dk give the backward's output strides."""
+    one = k if q is None else q
     if one is None:
-        raise ValueError(f"{qn} or {kn} must be given")
+        raise ValueError(f"{names[0]} or {names[1]} must be given")
     if one.dim() != 4:
-        raise ValueError(f"{qn} and {kn} must be [B,heads,T,d], got shape {tuple(one.shape)}")
+        raise ValueError(f"{names[0]} and {names[1]} must be [B,heads,T,d], got shape {tuple(one.shape)}")
     B, _, T, d = one.shape
     io, dev = one.dtype, one.device
     if io not in _IO_DTYPES:
-        raise ValueError(f"{qn} and {kn} must be float32 or bfloat16, got {io}")
-    for n, t in sides:
+        raise ValueError(f"{names[0]} and {names[1]} must be float32 or bfloat16, got {io}")
+    rows = []
+    for n, t, dy in ((names[0], q, dyq), (names[1], k, dyk)):
         if t is None:
+            rows += (0, (0, 0, 0))
             continue
-        if t.dim() != 4 or (t.shape[0], t.shape[2], t.shape[3]) != (B, T, d):
+        if t.dim() != 4:
+            raise ValueError(f"{n} must be [{B},heads,{T},{d}], got shape {tuple(t.shape)}")
+        b, heads, steps, width = t.shape
+        if b != B or steps != T or width != d:
             raise ValueError(f"{n} must be [{B},heads,{T},{d}], got shape {tuple(t.shape)}")
         if t.dtype != io:
             raise ValueError(f"{n} must be {io}, got {t.dtype}")
         if t.device != dev:
             raise ValueError(f"every tensor must be on {dev}, found one on {t.device}")
-        if t.stride(3) != 1 and d > 1:
+        st = t.stride()
+        if st[3] != 1 and d > 1:
             raise ValueError(f"the rows of {n} must be dense")
+        rows += (heads, st[:3])
+        if dy is not None and (dy.dtype != io or dy.shape != t.shape or not dy.is_contiguous() or dy.device != dev):
+            raise ValueError(f"d{'y' + n} must be contiguous {io} of shape {tuple(t.shape)} on {dev}, got {dy.dtype}, "
+                             f"{tuple(dy.shape)} on {dy.device}")
     rot, kind = 0, DN_POS_STEP
     if freqs is not None:
         if freqs.dim() != 1:
@@ -958,13 +968,21 @@ def _qk_args(sides, weights, norm, eps, freqs, pos, interleaved, amplitude, lens
     elif pos is not None:
         raise ValueError("pos without freqs")
     f32, i32 = torch.float32, torch.int32
-    _check_tensors(dev, *((n, t, f32, (d,)) for n, t in weights), ("freqs", freqs, torch.float64, (rot // 2,)),
-                   ("pos", pos, i32, (B, T) if kind == DN_POS_EACH else (B,)), ("lens", lens, i32, (B,)),
-                   *((n, t, io, like.shape) for n, t, like in grads))
-    strides = [(ctypes.c_int64 * 3)(*(0, 0, 0) if t is None else t.stride()[:3]) for t in (q, k)]
-    return QKShape(B, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], T, d, rot,
-                   DN_BF16 if io == torch.bfloat16 else DN_F32, norm, DN_ROT_NEIGHBOURS if interleaved else DN_ROT_HALVES,
-                   kind, float(eps), float(amplitude), *strides)
+    want = []   # of what is given: a checked tensor costs 0.6 us
+    if freqs is not None:
+        want.append(("freqs", freqs, torch.float64, (rot // 2,)))
+    if pos is not None:
+        want.append(("pos", pos, i32, (B, T) if kind == DN_POS_EACH else (B,)))
+    if wq is not None:
+        want.append(("wq", wq, f32, (d,)))
+    if wk is not None:
+        want.append(("wk", wk, f32, (d,)))
+    if lens is not None:
+        want.append(("lens", lens, i32, (B,)))
+    _check_tensors(dev, *want)
+    return QKShape(B, rows[0], rows[2], T, d, rot, DN_BF16 if io == torch.bfloat16 else DN_F32, norm,
+                   DN_ROT_NEIGHBOURS if interleaved else DN_ROT_HALVES, kind, eps, amplitude, *rows[1], *rows[3],
+                   *((0, 0, 0) if dq is None else dq.stride()[:3]), *((0, 0, 0) if dk is None else dk.stride()[:3]))
 
 
 def _qk_norm(norm):
@@ -974,7 +992,7 @@ def _qk_norm(norm):
 
 
 def _rows_like(t):
-    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def qk_norm_fwd(q, k, wq=None, wk=None, norm="l2", eps=1e-6, freqs=None, pos=None, interleaved=False, amplitude=1.0,
@@ -984,8 +1002,7 @@ def qk_norm_fwd(q, k, wq=None, wk=None, norm="l2", eps=1e-6, freqs=None, pos=Non
     q [B,Hq,T,d], k [B,Hk,T,d] (either None): any order of the dimensions but the last, as the transposed views of a
     projection's [B,T,heads,d], slices of a fused one among them.  Rotation, positions and ``lens`` as for
     rotary_fwd.  Returns (yq, yk), contiguous, as the operators above take them."""
-    sh = _qk_args((("q", q), ("k", k)), (("wq", wq), ("wk", wk)), _qk_norm(norm), eps, freqs, pos, interleaved,
-                  amplitude, lens)
+    sh = _qk_args(q, k, wq, wk, _qk_norm(norm), eps, freqs, pos, interleaved, amplitude, lens)
     with _allocating(stream):
         yq, yk = _rows_like(q), _rows_like(k)
     _check(dn_qk_fwd(sh, q, k, wq, wk, freqs, pos, lens, yq, yk, stream))
@@ -996,16 +1013,12 @@ def qk_norm_bwd(q, k, dyq, dyk, wq=None, wk=None, norm="l2", eps=1e-6, freqs=Non
                 amplitude=1.0, lens=None, want_dw=True, stream=None):
     """Backward of qk_norm_fwd from contiguous dyq, dyk.  Returns dict dq, dk (in the order of q's and k's dimensions),
     dwq, dwk (fp32 [d]; None without that weight)."""
-    sh = _qk_args((("q", q), ("k", k)), (("wq", wq), ("wk", wk)), _qk_norm(norm), eps, freqs, pos, interleaved,
-                  amplitude, lens, [(n, t, x) for n, t, x in (("dyq", dyq, q), ("dyk", dyk, k)) if x is not None])
     with _allocating(stream):
         dq, dk = (None if t is None else torch.empty_like(t) for t in (q, k))
+        sh = _qk_args(q, k, wq, wk, _qk_norm(norm), eps, freqs, pos, interleaved, amplitude, lens, dyq, dyk, dq, dk)
         dwq, dwk = (torch.empty_like(w) if want_dw and w is not None else None for w in (wq, wk))
         n = dn_qk_workspace_bytes(sh) if dwq is not None or dwk is not None else 0
         ws = torch.empty(n, dtype=torch.uint8, device=(q if q is not None else k).device) if n else None
-    for to, t in ((sh.dq_stride, dq), (sh.dk_stride, dk)):
-        if t is not None:
-            to[:] = t.stride()[:3]
     _check(dn_qk_bwd(sh, q, k, dyq, dyk, wq, wk, freqs, pos, lens, dq, dk, dwq, dwk, ws, n, stream))
     return {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
 
@@ -1016,7 +1029,7 @@ def rotary_fwd(q, k, freqs, pos=None, interleaved=False, amplitude=1.0, lens=Non
     rotary_freqs); the others stay.  q [B,Hq,T,d], k [B,Hk,T,d] (either None), any order of the dimensions but the last;
     ``pos``: None (the step), int32 [B] (the position of the first step) or int32 [B,T]; ``lens``: int32 [B], rows from
     there on are zero.  Returns (yq, yk), contiguous."""
-    sh = _qk_args((("q", q), ("k", k)), (), DN_NORM_NONE, 0.0, freqs, pos, interleaved, amplitude, lens)
+    sh = _qk_args(q, k, None, None, DN_NORM_NONE, 0.0, freqs, pos, interleaved, amplitude, lens)
     with _allocating(stream):
         yq, yk = _rows_like(q), _rows_like(k)
     _check(dn_qk_fwd(sh, q, k, None, None, freqs, pos, lens, yq, yk, stream))
@@ -1026,13 +1039,11 @@ def rotary_fwd(q, k, freqs, pos=None, interleaved=False, amplitude=1.0, lens=Non
 def rotary_bwd(dyq, dyk, freqs, pos=None, interleaved=False, amplitude=1.0, lens=None, stream=None):
     """Backward of rotary_fwd (the rotation back) from contiguous dyq [B,Hq,T,d], dyk [B,Hk,T,d].  Returns (dq, dk),
     contiguous."""
-    sh = _qk_args((("dyq", dyq), ("dyk", dyk)), (), DN_NORM_NONE, 0.0, freqs, pos, interleaved, amplitude, lens)
     _contig(dyq, dyk)
     with _allocating(stream):
         dq, dk = _rows_like(dyq), _rows_like(dyk)
-    for to, t in ((sh.dq_stride, dq), (sh.dk_stride, dk)):
-        if t is not None:
-            to[:] = t.stride()[:3]
+    sh = _qk_args(dyq, dyk, None, None, DN_NORM_NONE, 0.0, freqs, pos, interleaved, amplitude, lens, dq=dq, dk=dk,
+                  names=("dyq", "dyk"))
     _check(dn_qk_bwd(sh, None, None, dyq, dyk, None, None, freqs, pos, lens, dq, dk, None, None, None, 0, stream))
     return dq, dk
 

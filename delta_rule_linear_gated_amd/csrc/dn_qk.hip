@@ -12,21 +12,30 @@ namespace {
 
 constexpr int kQkUnits = 256;   // compute units
 
-// Sum of the workgroups' partial dw: 16 channels a workgroup, 16 lanes (x 16 rows) over the entries.
-__global__ __launch_bounds__(256) void qk_dw_kernel(QkArgs a) {
-    __shared__ float part[16][17];
+// Sum of the workgroups' partial dw: 16 channels a workgroup, 64 threads a channel over the
+// entries, eight loads in flight each (the sums are a chain of latencies: 16 threads with one
+// load in flight took 29 us for 1024 entries).
+__global__ __launch_bounds__(1024) void qk_dw_kernel(QkArgs a) {
+    __shared__ float part[64][17];
     const int blocks = a.d / 16, sd = blockIdx.x / blocks, j = blockIdx.x % blocks * 16 + threadIdx.x % 16;
     if (!a.side[sd].dw) return;
     const int r = threadIdx.x / 16;
     const long first = sd ? (long)a.groups[0] * a.tiles : 0, n = (long)a.groups[sd] * a.tiles;
     float sum = 0.f;
-    for (long i = r; i < n; i += 16) sum += a.parts[(first + i) * a.d + j];
+    constexpr int AHEAD = 8;
+    for (long i0 = r; i0 < n; i0 += 64 * AHEAD) {
+        float v[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) v[i] = a.parts[(first + min(i0 + 64 * i, n - 1)) * a.d + j];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) sum += i0 + 64 * i < n ? v[i] : 0.f;
+    }
     part[r][threadIdx.x % 16] = sum;
     __syncthreads();
     if (r) return;
     sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum += part[i][threadIdx.x];
+    for (int i = 0; i < 64; ++i) sum += part[i][threadIdx.x];
     a.side[sd].dw[j] = sum;
 }
 
@@ -84,7 +93,7 @@ hipError_t launch_qk_bwd(QkArgs a, char* ws, hipStream_t s) {
     }
     if (e != hipSuccess || !(a.side[0].dw || a.side[1].dw)) return e;
     prof_begin(s, "qk_dw");
-    hipLaunchKernelGGL(qk_dw_kernel, dim3(2 * a.d / 16), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(qk_dw_kernel, dim3(2 * a.d / 16), dim3(1024), 0, s, a);
     prof_end(s);
     return hipGetLastError();
 }

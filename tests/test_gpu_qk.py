@@ -269,11 +269,11 @@ def test_writes_stay_in_their_tensors():
     Bn, H, T, d = 2, 3, 21, 64
     s = rows(Bn, H, H, T, d, torch.bfloat16, seed=3)
     f, _ = B.rotary_freqs(32, device="cuda")
-    sh = B._qk_args((("q", s["q"]), ("k", s["k"])), (), B.DN_NORM_L2, 1e-6, f, None, False, 1.0, None)
     whole = {n: torch.full((Bn * T * (H + 2) * d + 4096,), 7.0, dtype=torch.bfloat16, device="cuda") for n in ("q", "k")}
     # rows of a [B, T, heads + 2, d] tensor, two heads left alone
     part = {n: w[2048:-2048].view(Bn, T, H + 2, d)[:, :, 1:-1].transpose(1, 2) for n, w in whole.items()}
-    sh.dq_stride[:], sh.dk_stride[:] = part["q"].stride()[:3], part["k"].stride()[:3]
+    sh = B.QKShape(Bn, H, H, T, d, 32, B.DN_BF16, B.DN_NORM_L2, B.DN_ROT_HALVES, B.DN_POS_STEP, 1e-6, 1.0,
+                   *(x for t in (s["q"], s["k"], part["q"], part["k"]) for x in t.stride()[:3]))
     dw = torch.full((2, 3 * d), 7.0, device="cuda")
     ws = torch.full((B.dn_qk_workspace_bytes(sh) + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
     n = ws.numel() - 4096

@@ -100,7 +100,8 @@ def qk(**over):
              amplitude=1.0, q_stride=(5 * 320, 64, 320), k_stride=(5 * 320, 64, 320), dq_stride=(960, 64, 192),
              dk_stride=(640, 320, 64))
     a.update(over)
-    return B.QKShape(*(a[n] if "stride" not in n else B.ctypes.c_int64.__mul__(3)(*a[n]) for n, _ in B.QKShape._fields_))
+    strides = [a.pop(n + "_stride") for n in ("q", "k", "dq", "dk")]
+    return B.QKShape(*a.values(), *(x for s in strides for x in s))
 
 
 def qfwd(s, **over):
