@@ -987,7 +987,7 @@ dn_status scan_shape(const dn_shape* s, dn::GsProblem* pr, ScanBytes* n) {
     if (s->flags & ~DN_FLAG_COUPLED) return fail(DN_ERR_INVALID, "unknown flags 0x%x", s->flags);
     if (s->gate != DN_GATE_VECTOR) return fail(DN_ERR_UNSUPPORTED, "the gated scan has a gate per channel");
     if (s->T > (1 << 30)) return fail(DN_ERR_UNSUPPORTED, "T must be <= 2^30");
-    if (s->dv > (1 << 22)) return fail(DN_ERR_UNSUPPORTED, "dv must be <= 2^22");
+    if (s->dv > (1 << 21)) return fail(DN_ERR_UNSUPPORTED, "dv must be <= 2^21");
     *pr = dn::GsProblem{s->B, s->H, s->T, s->dv, s->dtype == DN_BF16, (s->flags & DN_FLAG_COUPLED) ? 1 : 0};
     if (!dn::gs_fits(*pr)) return fail(DN_ERR_UNSUPPORTED, "B*H*dv too large");
     const size_t rows = (size_t)s->B * s->H * s->dv;

@@ -8,11 +8,14 @@
 // in registers, the waves exchange the maps through LDS (one barrier), each takes its run's
 // first state through the maps before it and goes over its registers again for the outputs.
 // All of a tile's rows are loaded while the one before is worked on, and every tensor is
-// read once.
+// read once: the bytes bound it (8 x 16 heads of 128, 4096 steps, bf16: forward 113 us, 4.8 TB/s;
+// backward 199 us, 4.7 TB/s; a large copy runs at 5.1).  Waves and runs were chosen by
+// measurement: forward 16 x 16 steps (8 x 16: 139 us, 8 x 32: 126, 16 x 8: 138), backward 8 x 16
+// (16 x 8: 225, 4 x 32: 211).
 //
-// Enough strips: a workgroup walks the tiles of one strip, the state in a register.  Few
-// strips (gs_plan): the tiles of all strips are handed out in the order of their steps, and a
-// tile takes its first state from messages of the tiles before it in its strip (Chain).
+// Marching, a workgroup walks the tiles of one strip, the state in a register.  Where the strips
+// do not fill the chip (gs_plan), the tiles of all strips are handed out in the order of their
+// steps, and a tile takes its first state from messages of the tiles before it in its strip (Chain).
 //
 // The backward goes from the last step with r_t = a_t D_t, the cotangent
 // that leaves step t to earlier ones:
@@ -28,13 +31,12 @@ namespace dn {
 
 namespace {
 
-constexpr int kGsWaves = 16, kGsRun = 16;         // forward, marching: waves, steps of a wave in a tile
-constexpr int kGsWavesC = 8, kGsRunC = 32;        // forward, chained
+constexpr int kGsWaves = 16, kGsRun = 16;         // forward: waves, steps of a run
+constexpr int kGsWavesC = 12;                     // forward, chained
 constexpr int kGsWavesB = 8;                      // backward: a tile begins at a saved state
 constexpr int kGsRunB = kGsSaved / kGsWavesB;
-constexpr int gs_tile(bool chain) { return chain ? kGsWavesC * kGsRunC : kGsWaves * kGsRun; }
 constexpr int kGsUnits = 256;                     // compute units
-static_assert(kGsSaved % kGsRun == 0 && kGsSaved % kGsRunC == 0, "saved states lie at the starts of runs");
+static_assert(kGsSaved % kGsRun == 0, "saved states lie at the starts of runs");
 constexpr int kRange = 0x7fffff00;                // bytes of a buffer range, at most
 constexpr int kNowhere = 0x7ffffff0;              // an offset past every range: loads give zero, stores do nothing
 
@@ -53,31 +55,42 @@ struct GsArgs {
     float *dg, *last, *states;
 };
 
-// The channel of a lane, and where its row begins in the strip.
+// A lane's channel and steps: a strip is 64 / G channels, and a wave's lanes take G runs of R
+// steps of each, one after the other.
 struct Lane {
     long row;      // (b, h)
-    int c, off;    // channel; elements from the strip's first row to the lane's channel
+    int c, off;    // channel; elements from the wave's first step of the strip's first row to the lane's
+    int ahead;     // steps from the wave's first to the lane's
     int len;       // steps of its sequence, 0 for an idle lane
     bool on;
 };
-__device__ __forceinline__ Lane gs_lane(const GsArgs& a, int strip, long& row0) {
+template <int G, int R>
+__device__ __forceinline__ Lane gs_lane(const GsArgs& a, int strip, long& row0, const int* len = nullptr) {   // len: known
+    constexpr int C = 64 / G;
     Lane l;
-    const int lane = lane_id();
+    const int lane = lane_id() % C;
     if (a.flat) {
-        const unsigned n0 = 64u * strip, n = n0 + lane, row = n / a.d;   // 2^28 channels at most
+        const unsigned n0 = (unsigned)C * strip, n = n0 + lane, row = n / a.d;   // 2^28 channels at most
         row0 = n0 / a.d;
         l.row = row;
         l.c = n - row * a.d;
         l.on = row < (unsigned)a.BH;
     } else {
-        const int per = (a.d + 63) / 64;
+        const int per = (a.d + C - 1) / C;
         row0 = l.row = strip / per;
-        l.c = strip % per * 64 + lane;
+        l.c = strip % per * C + lane;
         l.on = l.c < a.d;
     }
-    l.off = l.on ? (int)(l.row - row0) * a.T * a.d + l.c : 0;
-    l.len = !l.on ? 0 : a.lens ? min(max(a.lens[l.row / a.H], 0), a.T) : a.T;
+    l.ahead = lane_id() / C * R;
+    l.off = l.on ? (int)(((unsigned)(l.row - row0) * a.T + l.ahead) * a.d + l.c) : 0;
+    l.len = len ? *len : !l.on ? 0 : a.lens ? min(max(a.lens[l.row / a.H], 0), a.T) : a.T;
     return l;
+}
+// Strips marched by a workgroup each: the G strips of 64 channels go to one XCD (workgroups go
+// to the XCDs in turn), whose L2 then reads each line once for all of them.
+template <int G> __device__ __forceinline__ int gs_strip() {
+    const int x = blockIdx.x % kXcds, j = blockIdx.x / kXcds;
+    return (j / G * kXcds + x) * G + j % G;
 }
 
 // What lies from element `at` on of a tensor of n elements, as a buffer.
@@ -107,37 +120,40 @@ template <> struct Bits<bf16> {
     }
 };
 
-// R rows of a strip from step t on, a step's value in a register.  Rows past a lane's `end`
-// read as zero (g: a factor of one) and are not written.  All of a wave's lanes full (the
-// wave asks with __all): the steps are scalar offsets, else selects.
+// A lane's R rows, a step's value in a register; t: the wave's first step.  Rows past a lane's
+// length read as zero (g: a factor of one) and are written as zero.  All of a wave's lanes full
+// (the wave asks with __all): the steps are scalar offsets, else selects.
 template <typename T, int R>
-__device__ __forceinline__ void gs_load(unsigned (&v)[R], const void* p, const GsArgs& a, long row0, const Lane& l,
-                                        int t, int end, bool full) {
+__device__ __forceinline__ void gs_load(unsigned (&v)[R], const void* p, const GsArgs& a, long row0, const Lane& l, int t,
+                                        bool full) {
     const long n = (long)a.BH * a.T * a.d, at = (row0 * a.T + t) * a.d;
     const auto r = gs_range<T>(p, n, at);
-    const int step = a.d * (int)sizeof(T), off = l.on ? l.off * (int)sizeof(T) : kNowhere;
+    const int step = a.d * (int)sizeof(T), off = l.on ? (int)((unsigned)l.off * (unsigned)sizeof(T)) : kNowhere;
     if (full) {
 #pragma unroll
         for (int i = 0; i < R; ++i) v[i] = Bits<T>::load(r, off, i * step);
     } else {
 #pragma unroll
-        for (int i = 0; i < R; ++i) v[i] = Bits<T>::load(r, t + i < end ? off + i * step : kNowhere, 0);
+        for (int i = 0; i < R; ++i)
+            v[i] = Bits<T>::load(r, t + l.ahead + i < l.len ? (int)((unsigned)off + (unsigned)(i * step)) : kNowhere, 0);
     }
 }
-// A lane's rows from its `end` up to T are written as zero.
 template <typename T, int R>
 __device__ __forceinline__ void gs_store(const float (&v)[R], void* p, const GsArgs& a, long row0, const Lane& l, int t,
-                                         int end, bool full) {
+                                         bool full) {
     const long n = (long)a.BH * a.T * a.d, at = (row0 * a.T + t) * a.d;
     const auto r = gs_range<T>(p, n, at);
-    const int step = a.d * (int)sizeof(T), off = l.on ? l.off * (int)sizeof(T) : kNowhere;
+    const int step = a.d * (int)sizeof(T), off = l.on ? (int)((unsigned)l.off * (unsigned)sizeof(T)) : kNowhere;
     if (full) {
 #pragma unroll
         for (int i = 0; i < R; ++i) Bits<T>::store(v[i], r, off, i * step);
     } else {
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-            Bits<T>::store(t + i < end ? v[i] : 0.f, r, l.on && t + i < a.T ? off + i * step : kNowhere, 0);
+        for (int i = 0; i < R; ++i) {
+            const int s = t + l.ahead + i;
+            Bits<T>::store(s < l.len ? v[i] : 0.f, r, l.on && s < a.T ? (int)((unsigned)off + (unsigned)(i * step)) : kNowhere,
+                           0);
+        }
     }
 }
 
@@ -157,6 +173,26 @@ __device__ __forceinline__ float gs_rest(float g, float a) {
     return fabsf(g) < 0.5f ? -g * s : 1.f - a;
 }
 
+// Maps of a wave's runs: {p, e} of a lane's run becomes that of all of its channel's runs up to
+// and with it (REV: from it on), and `out` the map of the runs before (REV: behind) it.
+template <int G, bool REV> __device__ __forceinline__ void gs_join(float& p, float& e, float2& out) {
+    constexpr int C = 64 / G;
+    const int l = lane_id();
+#pragma unroll
+    for (int s = C; s < 64; s *= 2) {
+        const float q = REV ? __shfl_down(p, s) : __shfl_up(p, s), f = REV ? __shfl_down(e, s) : __shfl_up(e, s);
+        if (REV ? l + s < 64 : l >= s) {
+            e = fmaf(p, f, e);
+            p *= q;
+        }
+    }
+    out = make_float2(1.f, 0.f);
+    if (G > 1) {
+        const float q = REV ? __shfl_down(p, C) : __shfl_up(p, C), f = REV ? __shfl_down(e, C) : __shfl_up(e, C);
+        if (REV ? l + C < 64 : l >= C) out = make_float2(q, f);
+    }
+}
+
 __device__ __forceinline__ int uniform_wave() { return __builtin_amdgcn_readfirstlane(wave_id()); }
 
 // Tiles of few strips: message `at` (the tile's place in the order in which they are handed
@@ -171,7 +207,7 @@ __device__ __forceinline__ int uniform_wave() { return __builtin_amdgcn_readfirs
 // that order, and a tile waits for earlier ones only, so that the earliest unfinished tile
 // waits for nothing, however few workgroups run.
 struct Chain {
-    static constexpr int kEach = 16;   // maps that a wave gathers
+    static constexpr int kEach = 8;    // maps that a wave gathers
     static constexpr unsigned kUnset = 0xffffffffu;   // a NaN
     static constexpr int kMessage = 64 * 8 + 64 * 4, kHead = 256;   // bytes
 
@@ -185,8 +221,8 @@ struct Chain {
     static __device__ __forceinline__ unsigned bits(float v) {   // any NaN as the quiet one
         return v == v ? __builtin_bit_cast(unsigned, v) : 0x7fc00000u;
     }
-    static __device__ __forceinline__ void put_map(const GsArgs& a, int at, float p, float e) {
-        __hip_atomic_store(map_of(a, at), (unsigned long long)bits(e) << 32 | bits(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    static __device__ __forceinline__ void put_map(const GsArgs& a, int at, float2 m) {
+        __hip_atomic_store(map_of(a, at), (unsigned long long)bits(m.y) << 32 | bits(m.x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     static __device__ __forceinline__ void put_last(const GsArgs& a, int at, float h) {
         __hip_atomic_store(last_of(a, at), bits(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -206,86 +242,94 @@ struct Chain {
         n = __builtin_amdgcn_readfirstlane(n);
         return n < a.strips * a.tiles ? n : -1;
     }
+    // A workgroup's first tile; slot: LDS.
+    static __device__ __forceinline__ int first(const GsArgs& a, int* slot) {
+        if (wave_id() == 0) {
+            const int n = claim(a);
+            if (lane_id() == 0) *slot = n;
+        }
+        __syncthreads();
+        const int n = __builtin_amdgcn_readfirstlane(*slot);
+        __syncthreads();
+        return n;
+    }
+    static __device__ __forceinline__ float2 then(float2 m, float2 n) { return make_float2(n.x * m.x, fmaf(n.x, m.y, n.y)); }
     // Waves that gather: the first ones.
     static __device__ __forceinline__ int gatherers(const GsArgs& a) { return (a.reach + kEach - 1) / kEach; }
-    // Wave w's share of what comes before tile `at`, k-th of its strip: a map, or (wave 0)
-    // the state after its share, from the state before or from `first`.
-    static __device__ __forceinline__ float2 gather(const GsArgs& a, int at, int k, int w, float first) {
-        const int n = min(k, a.reach), lo = w * kEach, m = min(n - lo, kEach);   // m maps, oldest first
-        float p = w == 0 ? 0.f : 1.f, e = 0.f;
-        if (w == 0) {
-            e = first;
-            if (k > n) {
-                const int from = at - (n + 1) * a.strips;
-                unsigned u = get_last(a, from);
-                while (!__all(u != kUnset)) {
-                    __builtin_amdgcn_s_sleep(1);
-                    u = get_last(a, from);
-                }
-                e = __builtin_bit_cast(float, u);
-            }
+    // Wave w's share of what comes before tile `at`: a map, or (wave 0) the state after its share,
+    // from the state before it or the strip's own.  Asked for early, so that the answers are
+    // there when the rows that were on their way before are (loads come back in order).
+    struct Wave {
+        unsigned long long u[kEach];
+        unsigned base;
+        float first;
+
+        __device__ __forceinline__ void share(const GsArgs& a, int at, int w, int& k, int& n, int& m) const {
+            k = at / a.strips;
+            n = min(k, a.reach);
+            m = min(n - w * kEach, kEach);   // maps, oldest first
         }
-        constexpr int BATCH = 8;
-        for (int i0 = 0; i0 < m; i0 += BATCH) {
-            unsigned long long u[BATCH];
+        __device__ __forceinline__ void ask(const GsArgs& a, int at, int w) {
+            int k, n, m;
+            share(a, at, w, k, n, m);
+            first = 0.f;
+            base = 0;
+            if (w == 0 && k > n) base = get_last(a, at - (n + 1) * a.strips);
+            if (w == 0 && k <= n && a.first) {
+                long row0;
+                const Lane l = gs_lane<1, 1>(a, at % a.strips, row0, &k);   // its length does not matter
+                if (l.on) first = a.first[l.row * a.d + l.c];
+            }
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) u[i] = get_map(a, at - (n - lo - min(i0 + i, m - 1)) * a.strips);
+            for (int i = 0; i < kEach; ++i)
+                if (i < m) u[i] = get_map(a, at - (n - w * kEach - i) * a.strips);
+        }
+        __device__ __forceinline__ float2 answer(const GsArgs& a, int at, int w) {
+            int k, n, m;
+            share(a, at, w, k, n, m);
+            float p = w == 0 ? 0.f : 1.f, e = first;
+            if (w == 0 && k > n) {
+                while (!__all(base != kUnset)) {
+                    __builtin_amdgcn_s_sleep(1);
+                    base = get_last(a, at - (n + 1) * a.strips);
+                }
+                e = __builtin_bit_cast(float, base);
+            }
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                if (i0 + i >= m) break;
+            for (int i = 0; i < kEach; ++i) {
+                if (i >= m) break;
                 while (!__all((unsigned)u[i] != kUnset)) {
                     __builtin_amdgcn_s_sleep(1);
-                    u[i] = get_map(a, at - (n - lo - (i0 + i)) * a.strips);
+                    u[i] = get_map(a, at - (n - w * kEach - i) * a.strips);
                 }
                 const float q = __builtin_bit_cast(float, (unsigned)u[i]);
                 if (w > 0) p *= q;
                 e = fmaf(q, e, __builtin_bit_cast(float, (unsigned)(u[i] >> 32)));
             }
+            return make_float2(p, e);
         }
-        return make_float2(p, e);
-    }
+    };
 };
 
-// Forward.  Outputs, saved states and the last state, each where wanted.
-template <typename T, bool COUPLED, bool CHAIN>
-__global__ __launch_bounds__(64 * (CHAIN ? kGsWavesC : kGsWaves)) void gated_scan_fwd_kernel(GsArgs a) {
-    constexpr int R = CHAIN ? kGsRunC : kGsRun, W = CHAIN ? kGsWavesC : kGsWaves, TILE = W * R;
-    __shared__ float2 part[2][W][64], gathered[CHAIN ? W : 1][64];
-    __shared__ int claimed[2];
-    const int w = uniform_wave(), lane = lane_id();
-    const int gatherers = CHAIN ? Chain::gatherers(a) : 0;
-    int at = 0, next = CHAIN ? -1 : a.tiles > 1 ? 1 : -1, after = -1;
-    if (CHAIN) {
-        if (w == 0) at = Chain::claim(a);
-        if (w == 0 && lane == 0) claimed[0] = at;
-        __syncthreads();
-        at = __builtin_amdgcn_readfirstlane(claimed[0]);
-        if (at < 0) return;
-        __syncthreads();
-    } else if (a.tiles == 0) {
-        at = -1;
-    }
+// Forward, marching.  Outputs, saved states and the last state, each where wanted.
+template <typename T, bool COUPLED, int G>
+__global__ __launch_bounds__(64 * kGsWaves) void gated_scan_fwd_kernel(GsArgs a) {
+    constexpr int R = kGsRun, W = kGsWaves, TILE = W * G * R, C = 64 / G;
+    __shared__ float2 part[2][W][C];
+    const int w = uniform_wave(), lane = lane_id(), c = lane % C, strip = gs_strip<G>();
+    if (strip >= a.strips) return;
     long row0;
-    Lane l = gs_lane(a, CHAIN ? at % a.strips : blockIdx.x, row0);
+    const Lane l = gs_lane<G, R>(a, strip, row0);
     float h = a.first && l.on ? a.first[l.row * a.d + l.c] : 0.f;
     unsigned gn[R], xn[R];
-    auto fetch = [&](const Lane& l, long row0, int t) {
-        const bool full = __all(!l.on || l.len >= t + R);
-        gs_load<float, R>(gn, a.g, a, row0, l, t, l.len, full);
-        gs_load<T, R>(xn, a.x, a, row0, l, t, l.len, full);
+    auto fetch = [&](int t) {
+        const bool full = __all(!l.on || l.len >= t + l.ahead + R);
+        gs_load<float, R>(gn, a.g, a, row0, l, t, full);
+        gs_load<T, R>(xn, a.x, a, row0, l, t, full);
     };
-    auto prefetch = [&]() {   // the next tile's rows
-        if (CHAIN) {
-            long r;
-            const Lane m = gs_lane(a, next % a.strips, r);
-            fetch(m, r, next / a.strips * TILE + w * R);
-        } else {
-            fetch(l, row0, next * TILE + w * R);
-        }
-    };
-    if (at >= 0) fetch(l, row0, (CHAIN ? at / a.strips : 0) * TILE + w * R);
-    for (int buf = 0; at >= 0; buf ^= 1) {
-        const int k = CHAIN ? at / a.strips : at, t = k * TILE + w * R;
+    if (a.tiles > 0) fetch(w * G * R);
+    for (int k = 0; k < a.tiles; ++k) {
+        const int t = k * TILE + w * G * R, tl = t + l.ahead;
         float f[R], b[R], sum = 0.f, e = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -296,104 +340,144 @@ __global__ __launch_bounds__(64 * (CHAIN ? kGsWavesC : kGsWaves)) void gated_sca
             sum += g;
             e = fmaf(f[i], e, b[i]);
         }
-        // a wave that gathers would wait for its rows with the messages: it loads them after
-        bool ahead = next >= 0 && w >= gatherers;
-        if (ahead) prefetch();
-        part[buf][w][lane] = make_float2(gs_exp(sum), e);
+        if (k + 1 < a.tiles) fetch(t + TILE);
+        float p = gs_exp(sum);
+        float2 own;
+        gs_join<G, false>(p, e, own);
+        if (lane >= 64 - C) part[k & 1][w][c] = make_float2(p, e);
         __syncthreads();
-        if (CHAIN) {
-            if (w == 0) {
-                float p = 1.f, q = 0.f;
-#pragma unroll
-                for (int v = 0; v < W; ++v) {
-                    const float2 m = part[buf][v][lane];
-                    p *= m.x;
-                    q = fmaf(m.x, q, m.y);
-                }
-                Chain::put_map(a, at, p, q);
-            }
-            if (w == W - 1) {   // tiles to work on after the next
-                const int n = next < 0 ? Chain::claim(a) : -1, m = Chain::claim(a);
-                if (lane == 0) claimed[0] = n, claimed[1] = m;
-            }
-            if (w < gatherers)
-                gathered[w][lane] = Chain::gather(a, at, k, w, a.first && l.on ? a.first[l.row * a.d + l.c] : 0.f);
-            __syncthreads();
-            h = gathered[0][lane].y;
-            for (int v = 1; v < gatherers; ++v) h = fmaf(gathered[v][lane].x, h, gathered[v][lane].y);
-            if (next < 0) next = __builtin_amdgcn_readfirstlane(claimed[0]);
-            after = __builtin_amdgcn_readfirstlane(claimed[1]);
-        } else {
-            after = next >= 0 && next + 1 < a.tiles ? next + 1 : -1;
-        }
         float mine = h;
 #pragma unroll
         for (int v = 0; v < W; ++v) {
-            const float2 m = part[buf][v][lane];
+            const float2 m = part[k & 1][v][c];
             if (v == w) mine = h;
             h = fmaf(m.x, h, m.y);
         }
-        if (CHAIN && w == W - 1) Chain::put_last(a, at, h);
-        if (CHAIN && !ahead && next >= 0) prefetch();
-        if (a.states && l.on && t % kGsSaved == 0 && t < a.T) a.states[(l.row * a.NS + t / kGsSaved) * a.d + l.c] = mine;
-        if (a.out) {
-            const bool full = __all(!l.on || l.len >= t + R);
+        if (G > 1) mine = fmaf(own.x, mine, own.y);
+        if (a.states && l.on && tl % kGsSaved == 0 && tl < a.T) a.states[(l.row * a.NS + tl / kGsSaved) * a.d + l.c] = mine;
+        if (!a.out) continue;
+        const bool full = __all(!l.on || l.len >= tl + R);
 #pragma unroll
-            for (int i = 0; i < R; ++i) b[i] = mine = fmaf(f[i], mine, b[i]);
-            gs_store<T, R>(b, a.out, a, row0, l, t, l.len, full);
-        }
-        if (k == a.tiles - 1 && w == 0 && a.last && l.on) a.last[l.row * a.d + l.c] = h;
-        at = next;
-        next = after;
-        if (CHAIN && at >= 0) l = gs_lane(a, at % a.strips, row0);
+        for (int i = 0; i < R; ++i) b[i] = mine = fmaf(f[i], mine, b[i]);
+        gs_store<T, R>(b, a.out, a, row0, l, t, full);
     }
-    if (!CHAIN && a.tiles == 0 && a.last && w == 0 && l.on) a.last[l.row * a.d + l.c] = h;
+    if (a.last && w == 0 && lane < C && l.on) a.last[l.row * a.d + l.c] = h;
 }
 
-// Backward: tiles from the last step on, k the number of tiles behind this one.
-template <typename T, bool COUPLED, bool CHAIN>
-__global__ __launch_bounds__(64 * kGsWavesB) void gated_scan_bwd_kernel(GsArgs a) {
-    constexpr int R = kGsRunB, W = kGsWavesB;
-    __shared__ float2 fore[2][W][64], back[2][W][64], gathered[CHAIN ? W : 1][64];
-    __shared__ int claimed[2];
-    const int w = uniform_wave(), lane = lane_id();
-    const int gatherers = CHAIN ? Chain::gatherers(a) : 0;
-    int at = 0, next = CHAIN ? -1 : a.tiles > 1 ? 1 : -1, after = -1;
-    if (CHAIN) {
-        if (w == 0) at = Chain::claim(a);
-        if (w == 0 && lane == 0) claimed[0] = at;
+// Forward, chained: outputs are a tile behind the maps, so that a tile's map has been on its
+// way to the others for as long as a tile takes when they ask for it.
+template <typename T, bool COUPLED> __global__ __launch_bounds__(64 * kGsWavesC) void gated_scan_fwd_chain_kernel(GsArgs a) {
+    constexpr int R = kGsRun, W = kGsWavesC, TILE = W * R;
+    __shared__ float2 part[2][W][64], gathered[2][W][64];
+    __shared__ int claimed[2][2];
+    const int w = uniform_wave(), lane = lane_id(), gatherers = Chain::gatherers(a);
+    // tiles: outputs to write, map to form (its rows on the way), rows to load
+    int cur = -1, nxt = Chain::first(a, &claimed[1][0]), nx2 = -1;
+    if (nxt < 0) return;
+    unsigned gn[R], xn[R];
+    int len0 = 0, len1 = 0, len2 = 0;   // lengths of the lanes of cur, nxt, nx2
+    auto fetch = [&](int at, int& len) {
+        long row0;
+        const Lane l = gs_lane<1, R>(a, at % a.strips, row0);
+        const int t = at / a.strips * TILE + w * R;
+        const bool full = __all(!l.on || l.len >= t + R);
+        gs_load<float, R>(gn, a.g, a, row0, l, t, full);
+        gs_load<T, R>(xn, a.x, a, row0, l, t, full);
+        len = l.len;
+    };
+    fetch(nxt, len1);
+    float f0[R], b0[R];
+    float2 before0 = make_float2(1.f, 0.f), all0 = before0;   // cur's maps: of the waves before this one; whole (last wave)
+    for (int n = 0; cur >= 0 || nxt >= 0; ++n) {
+        const int buf = n & 1;
+        Chain::Wave in;
+        if (cur >= 0 && w < gatherers) in.ask(a, cur, w);
+        int c0 = -1, c1 = -1;
+        if (w == W - 1) {
+            if (n == 0) c0 = Chain::claim(a);
+            if (n == 0 || nx2 >= 0) c1 = Chain::claim(a);
+        }
+        float f1[R], b1[R], sum = 0.f, e = 0.f;
+        if (nxt >= 0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float g = Bits<float>::value(gn[i]);
+                b1[i] = Bits<T>::value(xn[i]);
+                f1[i] = gs_exp(g);
+                if (COUPLED) b1[i] *= gs_rest(g, f1[i]);
+                sum += g;
+                e = fmaf(f1[i], e, b1[i]);
+            }
+            part[buf][w][lane] = make_float2(gs_exp(sum), e);
+        }
+        if (cur >= 0 && w < gatherers) gathered[buf][w][lane] = in.answer(a, cur, w);
+        const bool fetched = nx2 >= 0;
+        if (fetched) fetch(nx2, len2);
+        if (w == W - 1 && lane == 0) claimed[buf][0] = c0, claimed[buf][1] = c1;
         __syncthreads();
-        at = __builtin_amdgcn_readfirstlane(claimed[0]);
-        if (at < 0) return;
-        __syncthreads();
-    } else if (a.tiles == 0) {
-        at = -1;
+        if (n == 0) nx2 = __builtin_amdgcn_readfirstlane(claimed[buf][0]);
+        const int nx3 = __builtin_amdgcn_readfirstlane(claimed[buf][1]);
+        if (!fetched && nx2 >= 0) fetch(nx2, len2);
+        float2 before1 = make_float2(1.f, 0.f), all1 = before1;
+        if (nxt >= 0) {
+            for (int v = 0; v < w; ++v) before1 = Chain::then(before1, part[buf][v][lane]);
+            if (w == W - 1) {
+                all1 = Chain::then(before1, part[buf][w][lane]);
+                Chain::put_map(a, nxt, all1);
+            }
+        }
+        if (cur >= 0) {
+            float h = gathered[buf][0][lane].y;
+            for (int v = 1; v < gatherers; ++v) h = fmaf(gathered[buf][v][lane].x, h, gathered[buf][v][lane].y);
+            long row0;
+            const Lane l = gs_lane<1, R>(a, cur % a.strips, row0, &len0);
+            const int k = cur / a.strips, t = k * TILE + w * R;
+            if (w == W - 1) {
+                const float last = fmaf(all0.x, h, all0.y);
+                Chain::put_last(a, cur, last);
+                if (k == a.tiles - 1 && a.last && l.on) a.last[l.row * a.d + l.c] = last;
+            }
+            h = fmaf(before0.x, h, before0.y);
+            if (a.states && l.on && t % kGsSaved == 0 && t < a.T) a.states[(l.row * a.NS + t / kGsSaved) * a.d + l.c] = h;
+            if (a.out) {
+                const bool full = __all(!l.on || l.len >= t + R);
+#pragma unroll
+                for (int i = 0; i < R; ++i) b0[i] = h = fmaf(f0[i], h, b0[i]);
+                gs_store<T, R>(b0, a.out, a, row0, l, t, full);
+            }
+        }
+        cur = nxt, nxt = nx2, nx2 = nx3;
+        len0 = len1, len1 = len2;
+        before0 = before1, all0 = all1;
+#pragma unroll
+        for (int i = 0; i < R; ++i) f0[i] = f1[i], b0[i] = b1[i];
     }
+}
+
+// Backward, marching from the last step; k: tiles behind this one.
+template <typename T, bool COUPLED, int G>
+__global__ __launch_bounds__(64 * kGsWavesB) void gated_scan_bwd_kernel(GsArgs a) {
+    constexpr int R = kGsRunB, W = kGsWavesB, TILE = W * G * R, C = 64 / G;
+    constexpr int SHARE = W / G;   // waves on the steps of one saved state
+    __shared__ float2 fore[2][W][C], back[2][W][C];
+    const int w = uniform_wave(), lane = lane_id(), c = lane % C, strip = gs_strip<G>();
+    if (strip >= a.strips) return;
     long row0;
-    Lane l = gs_lane(a, CHAIN ? at % a.strips : blockIdx.x, row0);
+    const Lane l = gs_lane<G, R>(a, strip, row0);
     float r = a.first && l.on ? a.first[l.row * a.d + l.c] : 0.f;
     unsigned gn[R], xn[R], yn[R];
     float hn = 0.f;
-    auto fetch = [&](const Lane& l, long row0, int k) {
-        const int t0 = (a.tiles - 1 - k) * kGsSaved, t = t0 + w * R;
-        const bool full = __all(!l.on || l.len >= t + R);
-        gs_load<float, R>(gn, a.g, a, row0, l, t, l.len, full);
-        gs_load<T, R>(xn, a.x, a, row0, l, t, l.len, full);
-        gs_load<T, R>(yn, a.y, a, row0, l, t, l.len, full);
-        hn = l.len > t0 ? a.states_in[(l.row * a.NS + t0 / kGsSaved) * a.d + l.c] : 0.f;
+    auto fetch = [&](int t) {
+        const int saved = t / kGsSaved;
+        const bool full = __all(!l.on || l.len >= t + l.ahead + R);
+        gs_load<float, R>(gn, a.g, a, row0, l, t, full);
+        gs_load<T, R>(xn, a.x, a, row0, l, t, full);
+        gs_load<T, R>(yn, a.y, a, row0, l, t, full);
+        hn = l.len > saved * kGsSaved ? a.states_in[(l.row * a.NS + saved) * a.d + l.c] : 0.f;
     };
-    auto prefetch = [&]() {
-        if (CHAIN) {
-            long r;
-            const Lane m = gs_lane(a, next % a.strips, r);
-            fetch(m, r, next / a.strips);
-        } else {
-            fetch(l, row0, next);
-        }
-    };
-    if (at >= 0) fetch(l, row0, CHAIN ? at / a.strips : 0);
-    for (int buf = 0; at >= 0; buf ^= 1) {
-        const int k = CHAIN ? at / a.strips : at, t = (a.tiles - 1 - k) * kGsSaved + w * R;
+    if (a.tiles > 0) fetch((a.tiles - 1) * TILE + w * G * R);
+    for (int k = 0; k < a.tiles; ++k) {
+        const int t = (a.tiles - 1 - k) * TILE + w * G * R;
         float f[R], x[R], y[R], wt[R], h = hn, sum = 0.f, e = 0.f, q = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -405,54 +489,31 @@ __global__ __launch_bounds__(64 * kGsWavesB) void gated_scan_bwd_kernel(GsArgs a
             sum += g;
             e = fmaf(f[i], e, wt[i] * x[i]);
         }
-        bool ahead = next >= 0 && w >= gatherers;
-        if (ahead) prefetch();
+        if (k + 1 < a.tiles) fetch(t - TILE);
 #pragma unroll
         for (int i = R - 1; i >= 0; --i) q = f[i] * (q + y[i]);
-        const float p = gs_exp(sum);
-        fore[buf][w][lane] = make_float2(p, e);
-        back[buf][w][lane] = make_float2(p, q);
+        float p = gs_exp(sum), pr = p;
+        float2 own, ownr;
+        gs_join<G, false>(p, e, own);
+        gs_join<G, true>(pr, q, ownr);
+        if (SHARE > 1 && lane >= 64 - C) fore[k & 1][w][c] = make_float2(p, e);
+        if (lane < C) back[k & 1][w][c] = make_float2(pr, q);
         __syncthreads();
-        if (CHAIN) {
-            if (w == 0) {
-                float p = 1.f, q = 0.f;
-#pragma unroll
-                for (int v = W - 1; v >= 0; --v) {
-                    const float2 m = back[buf][v][lane];
-                    p *= m.x;
-                    q = fmaf(m.x, q, m.y);
-                }
-                Chain::put_map(a, at, p, q);
-            }
-            if (w == W - 1) {
-                const int n = next < 0 ? Chain::claim(a) : -1, m = Chain::claim(a);
-                if (lane == 0) claimed[0] = n, claimed[1] = m;
-            }
-            if (w < gatherers)
-                gathered[w][lane] = Chain::gather(a, at, k, w, a.first && l.on ? a.first[l.row * a.d + l.c] : 0.f);
-            __syncthreads();
-            r = gathered[0][lane].y;
-            for (int v = 1; v < gatherers; ++v) r = fmaf(gathered[v][lane].x, r, gathered[v][lane].y);
-            if (next < 0) next = __builtin_amdgcn_readfirstlane(claimed[0]);
-            after = __builtin_amdgcn_readfirstlane(claimed[1]);
-        } else {
-            after = next >= 0 && next + 1 < a.tiles ? next + 1 : -1;
-        }
         float mine = r;
 #pragma unroll
         for (int v = W - 1; v >= 0; --v) {
-            const float2 m = back[buf][v][lane];
+            const float2 m = back[k & 1][v][c];
             if (v == w) mine = r;
             r = fmaf(m.x, r, m.y);
         }
-        if (CHAIN && w == W - 1) Chain::put_last(a, at, r);
-        if (CHAIN && !ahead && next >= 0) prefetch();
+        if (G > 1) mine = fmaf(ownr.x, mine, ownr.y);
 #pragma unroll
-        for (int v = 0; v < W - 1; ++v)
-            if (v < w) {
-                const float2 m = fore[buf][v][lane];
+        for (int v = 0; v < SHARE - 1; ++v)
+            if (v < w % SHARE) {
+                const float2 m = fore[k & 1][w / SHARE * SHARE + v][c];
                 h = fmaf(m.x, h, m.y);
             }
+        if (G > 1) h = fmaf(own.x, h, own.y);
         float before[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -466,15 +527,121 @@ __global__ __launch_bounds__(64 * kGsWavesB) void gated_scan_bwd_kernel(GsArgs a
             x[i] = COUPLED ? wt[i] * D : D;
             y[i] = mine * before[i];
         }
-        const bool full = __all(!l.on || l.len >= t + R);
-        gs_store<T, R>(x, a.out, a, row0, l, t, l.len, full);
-        gs_store<float, R>(y, a.dg, a, row0, l, t, l.len, full);
-        if (k == a.tiles - 1 && w == 0 && a.last && l.on) a.last[l.row * a.d + l.c] = r;
-        at = next;
-        next = after;
-        if (CHAIN && at >= 0) l = gs_lane(a, at % a.strips, row0);
+        const bool full = __all(!l.on || l.len >= t + l.ahead + R);
+        gs_store<T, R>(x, a.out, a, row0, l, t, full);
+        gs_store<float, R>(y, a.dg, a, row0, l, t, full);
     }
-    if (!CHAIN && a.tiles == 0 && a.last && w == 0 && l.on) a.last[l.row * a.d + l.c] = r;
+    if (a.last && w == 0 && lane < C && l.on) a.last[l.row * a.d + l.c] = r;
+}
+
+// Backward, chained from the last tile of every strip; results are a tile behind the maps.  The
+// states inside a tile come from the saved one at its start and wait for no other tile.
+template <typename T, bool COUPLED> __global__ __launch_bounds__(64 * kGsWavesB) void gated_scan_bwd_chain_kernel(GsArgs a) {
+    constexpr int R = kGsRunB, W = kGsWavesB, TILE = W * R;
+    static_assert(TILE == kGsSaved, "a tile begins at a saved state");
+    __shared__ float2 fore[2][W][64], back[2][W][64], gathered[2][W][64];
+    __shared__ int claimed[2][2];
+    const int w = uniform_wave(), lane = lane_id(), gatherers = Chain::gatherers(a);
+    int cur = -1, nxt = Chain::first(a, &claimed[1][0]), nx2 = -1;
+    if (nxt < 0) return;
+    unsigned gn[R], xn[R], yn[R];
+    float hn = 0.f;
+    int len0 = 0, len1 = 0, len2 = 0;
+    auto fetch = [&](int at, int& len) {
+        long row0;
+        const Lane l = gs_lane<1, R>(a, at % a.strips, row0);
+        const int saved = a.tiles - 1 - at / a.strips, t = saved * TILE + w * R;
+        const bool full = __all(!l.on || l.len >= t + R);
+        gs_load<float, R>(gn, a.g, a, row0, l, t, full);
+        gs_load<T, R>(xn, a.x, a, row0, l, t, full);
+        gs_load<T, R>(yn, a.y, a, row0, l, t, full);
+        hn = l.len > saved * TILE ? a.states_in[(l.row * a.NS + saved) * a.d + l.c] : 0.f;
+        len = l.len;
+    };
+    fetch(nxt, len1);
+    float f0[R], w0[R], y0[R], s0[R];   // s: h_{t-1}, less x_t if coupled
+    float2 behind0 = make_float2(1.f, 0.f), all0 = behind0;   // cur's maps: of the waves behind this one; whole (wave 0)
+    for (int n = 0; cur >= 0 || nxt >= 0; ++n) {
+        const int buf = n & 1;
+        Chain::Wave in;
+        if (cur >= 0 && w < gatherers) in.ask(a, cur, w);
+        int c0 = -1, c1 = -1;
+        if (w == W - 1) {
+            if (n == 0) c0 = Chain::claim(a);
+            if (n == 0 || nx2 >= 0) c1 = Chain::claim(a);
+        }
+        float f1[R], w1[R], y1[R], s1[R], h = 0.f;
+        if (nxt >= 0) {
+            float sum = 0.f, e = 0.f, q = 0.f;
+            h = hn;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float g = Bits<float>::value(gn[i]);
+                s1[i] = Bits<T>::value(xn[i]);
+                y1[i] = Bits<T>::value(yn[i]);
+                f1[i] = gs_exp(g);
+                w1[i] = COUPLED ? gs_rest(g, f1[i]) : 1.f;
+                sum += g;
+                e = fmaf(f1[i], e, w1[i] * s1[i]);
+            }
+#pragma unroll
+            for (int i = R - 1; i >= 0; --i) q = f1[i] * (q + y1[i]);
+            const float p = gs_exp(sum);
+            fore[buf][w][lane] = make_float2(p, e);
+            back[buf][w][lane] = make_float2(p, q);
+        }
+        if (cur >= 0 && w < gatherers) gathered[buf][w][lane] = in.answer(a, cur, w);
+        const bool fetched = nx2 >= 0;
+        if (fetched) fetch(nx2, len2);
+        if (w == W - 1 && lane == 0) claimed[buf][0] = c0, claimed[buf][1] = c1;
+        __syncthreads();
+        if (n == 0) nx2 = __builtin_amdgcn_readfirstlane(claimed[buf][0]);
+        const int nx3 = __builtin_amdgcn_readfirstlane(claimed[buf][1]);
+        if (!fetched && nx2 >= 0) fetch(nx2, len2);
+        float2 behind1 = make_float2(1.f, 0.f), all1 = behind1;
+        if (nxt >= 0) {
+            for (int v = W - 1; v > w; --v) behind1 = Chain::then(behind1, back[buf][v][lane]);
+            if (w == 0) {
+                all1 = Chain::then(behind1, back[buf][w][lane]);
+                Chain::put_map(a, nxt, all1);
+            }
+            for (int v = 0; v < w; ++v) h = fmaf(fore[buf][v][lane].x, h, fore[buf][v][lane].y);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float x = s1[i];
+                s1[i] = COUPLED ? h - x : h;
+                h = fmaf(f1[i], h, w1[i] * x);
+            }
+        }
+        if (cur >= 0) {
+            float r = gathered[buf][0][lane].y;
+            for (int v = 1; v < gatherers; ++v) r = fmaf(gathered[buf][v][lane].x, r, gathered[buf][v][lane].y);
+            long row0;
+            const Lane l = gs_lane<1, R>(a, cur % a.strips, row0, &len0);
+            const int k = cur / a.strips, t = (a.tiles - 1 - k) * TILE + w * R;
+            if (w == 0) {
+                const float last = fmaf(all0.x, r, all0.y);
+                Chain::put_last(a, cur, last);
+                if (k == a.tiles - 1 && a.last && l.on) a.last[l.row * a.d + l.c] = last;
+            }
+            r = fmaf(behind0.x, r, behind0.y);
+#pragma unroll
+            for (int i = R - 1; i >= 0; --i) {
+                const float D = y0[i] + r;
+                r = f0[i] * D;
+                y0[i] = COUPLED ? w0[i] * D : D;
+                s0[i] *= r;
+            }
+            const bool full = __all(!l.on || l.len >= t + R);
+            gs_store<T, R>(y0, a.out, a, row0, l, t, full);
+            gs_store<float, R>(s0, a.dg, a, row0, l, t, full);
+        }
+        cur = nxt, nxt = nx2, nx2 = nx3;
+        len0 = len1, len1 = len2;
+        behind0 = behind1, all0 = all1;
+#pragma unroll
+        for (int i = 0; i < R; ++i) f0[i] = f1[i], w0[i] = w1[i], y0[i] = y1[i], s0[i] = s1[i];
+    }
 }
 
 // Before a chain: the counter is zero, every word of the messages unset.
@@ -507,26 +674,54 @@ __global__ __launch_bounds__(256) void gated_scan_recurrent_kernel(const T* x, c
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct GsPlan {
-    int flat, chain, tiles, reach;
+    int flat, chain, groups, tiles, reach;   // groups: runs of a channel in a wave (G)
     long strips;
 };
 
 // Lanes take the channels of all heads in a row, so that odd widths leave no lane idle but the
 // last strip's; where a strip's rows lie further apart than a 31-bit byte offset, a strip stays
 // in one head's row.
-void gs_strips(const GsProblem& pr, GsPlan* p) {
-    const long BH = (long)pr.B * pr.H, rows = 63 / pr.d + 2;   // a strip touches at most that many
-    p->flat = rows * pr.T < kRange / 4 / pr.d;
-    p->strips = p->flat ? (BH * pr.d + 63) / 64 : BH * ((pr.d + 63) / 64);
+bool gs_flat(const GsProblem& pr) {
+    const long rows = 63 / pr.d + 2;   // a strip touches at most that many
+    return rows * pr.T < kRange / 4 / pr.d;
 }
+long gs_strips(const GsProblem& pr, int groups) {
+    const long BH = (long)pr.B * pr.H, C = 64 / groups;
+    return gs_flat(pr) ? (BH * pr.d + C - 1) / C : BH * ((pr.d + C - 1) / C);
+}
+long gs_blocks(long strips, int groups) {   // G > 1: a whole number of 64-channel groups for every XCD
+    const long all = groups > 1 ? kXcds * groups : 1;
+    return (strips + all - 1) / all * all;
+}
+// Which form.  Measured (us, forward / backward, bf16, coupled; marching with the best G -> chained):
+//     64 strips, 8192 steps        81 / 127 -> 74 / 110      16 strips (fp32), 777 steps   15.4 / 15.5 -> 13.3 / 15.0
+//     157 strips, 4096 steps     110 / 196 -> 94 / 162       4 strips, 4096 steps          19.3 / 26.7 -> 14.6 / 15.5
+//     32 strips, 32768 steps     212 / 300 -> 134 / 205      32 strips, 512 steps             8.8 / 8.6 -> 12.8 / 14.8
+//     256 strips, 32768 of 8 documents   113 / 199 (floor 105 / 183; chained 0.85 and 0.97 of that rate)
+// So: few strips of at most 512 steps march, with as many runs of a channel in a wave as make one
+// tile of them; longer ones are chained where marching would leave more than a fifth of the
+// chip idle; else strips of 64 channels march.
+constexpr int kGsShort = 512;
 GsPlan gs_plan(const GsProblem& pr, bool bwd) {
     GsPlan p{};
-    gs_strips(pr, &p);
-    p.chain = p.strips > 0 && p.strips < kGsUnits && pr.T > 2 * (bwd ? kGsSaved : gs_tile(true));
-    const int tile = bwd ? kGsSaved : gs_tile(p.chain);
-    p.tiles = (int)(((long)pr.T + tile - 1) / tile);
-    // the tiles of a strip that are in flight at once
-    if (p.chain) p.reach = (int)std::min<long>((bwd ? kGsWavesB : kGsWavesC) * Chain::kEach, std::max<long>(4, kGsUnits / p.strips));
+    p.flat = gs_flat(pr);
+    p.groups = 1;
+    p.strips = gs_strips(pr, 1);
+    int tile = bwd ? kGsSaved : kGsWaves * kGsRun;
+    const long rounds = (p.strips + kGsUnits - 1) / kGsUnits;
+    if (pr.T <= kGsShort && p.strips < kGsUnits) {
+        while (tile * p.groups < pr.T) p.groups *= 2;
+        p.strips = gs_strips(pr, p.groups);
+    } else if (pr.T > kGsShort && p.strips * 5 < rounds * kGsUnits * 4) {
+        const int ctile = bwd ? kGsSaved : kGsWavesC * kGsRun;
+        if (p.strips * (((long)pr.T + ctile - 1) / ctile) < (1L << 30)) {
+            p.chain = 1;
+            tile = ctile;
+            // the tiles of a strip that are in flight at once (twice as many: within 2 %)
+            p.reach = (int)std::min<long>((bwd ? kGsWavesB : kGsWavesC) * Chain::kEach, std::max<long>(4, kGsUnits / p.strips));
+        }
+    }
+    p.tiles = (int)(((long)pr.T + (long)tile * p.groups - 1) / ((long)tile * p.groups));
     return p;
 }
 
@@ -570,25 +765,37 @@ hipError_t clear_chain(const GsPlan& p, char* ws, hipStream_t s) {
     prof_end(s);
     return hipGetLastError();
 }
-unsigned gs_grid(const GsPlan& p) { return (unsigned)(p.chain ? std::min<long>(p.strips * p.tiles, kGsUnits) : p.strips); }
+unsigned gs_grid(const GsPlan& p) {
+    return (unsigned)(p.chain ? std::min<long>(p.strips * p.tiles, kGsUnits) : gs_blocks(p.strips, p.groups));
+}
 
 template <typename T, bool COUPLED> hipError_t fwd_launch(const GsPlan& p, const GsArgs& a, hipStream_t s) {
     const dim3 grid(gs_grid(p)), block(64 * (p.chain ? kGsWavesC : kGsWaves));
     prof_begin(s, "gated_scan_fwd");
+#define DN_GS(G) hipLaunchKernelGGL((gated_scan_fwd_kernel<T, COUPLED, G>), grid, block, 0, s, a)
     if (p.chain)
-        hipLaunchKernelGGL((gated_scan_fwd_kernel<T, COUPLED, true>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<T, COUPLED>), grid, block, 0, s, a);
+    else if (p.groups == 1)
+        DN_GS(1);
     else
-        hipLaunchKernelGGL((gated_scan_fwd_kernel<T, COUPLED, false>), grid, block, 0, s, a);
+        DN_GS(2);
+#undef DN_GS
     prof_end(s);
     return hipGetLastError();
 }
 template <typename T, bool COUPLED> hipError_t bwd_launch(const GsPlan& p, const GsArgs& a, hipStream_t s) {
     const dim3 grid(gs_grid(p)), block(64 * kGsWavesB);
     prof_begin(s, "gated_scan_bwd");
+#define DN_GS(G) hipLaunchKernelGGL((gated_scan_bwd_kernel<T, COUPLED, G>), grid, block, 0, s, a)
     if (p.chain)
-        hipLaunchKernelGGL((gated_scan_bwd_kernel<T, COUPLED, true>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<T, COUPLED>), grid, block, 0, s, a);
+    else if (p.groups == 1)
+        DN_GS(1);
+    else if (p.groups == 2)
+        DN_GS(2);
     else
-        hipLaunchKernelGGL((gated_scan_bwd_kernel<T, COUPLED, false>), grid, block, 0, s, a);
+        DN_GS(4);
+#undef DN_GS
     prof_end(s);
     return hipGetLastError();
 }
@@ -617,9 +824,7 @@ size_t gs_states_bytes(const GsProblem& pr) {
 size_t gs_workspace_bytes(const GsProblem& pr, int pass) { return gs_ws(pr, pass).total; }
 bool gs_fits(const GsProblem& pr) {
     if (pr.B == 0 || pr.H == 0) return true;
-    GsPlan p;
-    gs_strips(pr, &p);
-    return (long)pr.B * pr.H <= 0x7fffffffL && p.strips < (1L << 32) / (64 * kGsWaves);
+    return (long)pr.B * pr.H <= 0x7fffffffL && gs_blocks(gs_strips(pr, 1), 1) < (1L << 32) / (64 * kGsWaves);
 }
 
 hipError_t launch_gated_scan_fwd(const GsProblem& pr, const GsFwd& f, char* ws, hipStream_t s) {

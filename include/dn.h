@@ -409,7 +409,7 @@ dn_status dn_tree_commit_counts(const dn_shape* shape, const void* k, const floa
  *     h_t = exp(g_t) h_{t-1} + w_t x_t,   o_t = h_t,   h_0 = h0, hT = h_T,
  *     w_t = 1, or 1 - exp(g_t) with DN_FLAG_COUPLED,
  * over whole sequences, its gradients and its recurrent form.
- *   shape  : B, H >= 0, 0 <= T <= 2^30; dv in 1 .. 2^22, the channels of a head (any
+ *   shape  : B, H >= 0, 0 <= T <= 2^30; dv in 1 .. 2^21, the channels of a head (any
  *            number; H = 1 for channels without heads); dk, C, eps unused; dtype; gate
  *            must be DN_GATE_VECTOR; flags 0 or DN_FLAG_COUPLED (others: DN_ERR_INVALID);
  *            fewer than 2^28 channels in all (B*H*dv, each head's rounded up to 64)

@@ -10,9 +10,10 @@ U16, U32 = 2.0 ** -8, 2.0 ** -24   # half a step of bf16 and of fp32, relative
 # terms' absolute values: the decay's exponential 2 (one unit of its instruction) and its
 # argument's rounding |g| e^-|g| * 1.5 < 1, the series or difference of the coupled weight 4
 # and its product 1, the step's own multiply-add 1; and once in a run of 16 steps the run's
-# decay, whose argument is a sum of 16 gates: 16 |G| e^-|G| < 6, its exponential 2, two
-# multiply-adds 2.  Together 19.
-STEP = 20
+# decay, whose argument is a sum of 16 gates: 16 |G| e^-|G| < 6, its exponential 2; joining it
+# to the runs before it in its tile 2, the tile's map to the state 2, the state to the run 1.
+# Together 22.
+STEP = 24
 
 
 def reference(x, g, h0=None, lens=None, coupled=False, do=None, dhT=None):

@@ -53,11 +53,13 @@ def test_against_the_definition(size, dtype, coupled):
 
 
 @pytest.mark.parametrize("coupled", [False, True])
-@pytest.mark.parametrize("size", [(1, 1, 5000, 33), (2, 1, 4097, 70), (1, 3, 1025, 64), (3, 1, 16384, 64)], ids=str)
-def test_segments(size, coupled):
-    """Few channels: the steps are split."""
+@pytest.mark.parametrize("size", [(1, 1, 513, 1), (1, 1, 5000, 33), (2, 1, 4097, 70), (1, 3, 1025, 64), (3, 1, 16384, 64),
+                                  (2, 70, 520, 130)], ids=str)
+def test_chained_tiles(size, coupled):
+    """Channels that do not fill the chip by themselves: the tiles of the steps run at once."""
     Bn, H, T, d = size
-    assert B.dn_gated_scan_workspace_bytes(B.make_shape(Bn, H, T, d, d, 64, "fp32", "vector"), B.DN_PASS_FWD) > 0
+    sh = B.make_shape(Bn, H, T, d, d, 64, "fp32", "vector")
+    assert B.dn_gated_scan_workspace_bytes(sh, B.DN_PASS_FWD) > 0 and B.dn_gated_scan_workspace_bytes(sh, B.DN_PASS_BWD) > 0
     for dtype in (torch.float32, torch.bfloat16):
         s = inputs(*size, dtype=dtype, seed=T)
         lens = torch.tensor([T, 0, T // 3][:Bn], dtype=torch.int32).cuda() if Bn > 1 else None
@@ -66,12 +68,23 @@ def test_segments(size, coupled):
         check(run(s, lens, coupled, saved=False), *ref, label=f"{size} recomputed")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_channels(dtype):
+    """A workgroup for each strip of channels, several tiles."""
+    s = inputs(4, 64, 600, 64, dtype=dtype, seed=12)
+    assert B.dn_gated_scan_workspace_bytes(B.make_shape(4, 64, 600, 64, 64, 64, "fp32", "vector"), B.DN_PASS_BWD) == 0
+    lens = torch.tensor([600, 511, 100, 0], dtype=torch.int32).cuda()
+    ref = reference(s["x"], s["g"], s["h0"], lens, True, s["do"], s["dhT"])
+    check(run(s, lens, True), *ref, label="saved")
+    check(run(s, lens, True, saved=False), *ref, label="recomputed")
+
+
+@pytest.mark.parametrize("T", [420, 530])
 @pytest.mark.parametrize("d", [7, 64, 100])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-def test_lengths(dtype, d):
+def test_lengths(dtype, d, T):
     """Every kind of length in one batch, several sequences in a strip of 64 channels too; what lies
     behind an end is not used and its results are zero."""
-    T = 530
     lens = [T, 0, 1, 127, 128, 129, 256, 400, T - 1, -3, T + 9]
     s = inputs(len(lens), 2, T, d, dtype=dtype, seed=d)
     for b, n in enumerate(lens):

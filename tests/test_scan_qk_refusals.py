@@ -51,8 +51,8 @@ def test_scan_shapes(f):
         assert f(sh(gate=gate)) == UNSUPPORTED
     for flags in (B.DN_FLAG_KACZMARZ, B.DN_FLAG_NO_SCAN, 8):
         assert f(sh(flags=flags)) == INVALID
-    assert f(sh(T=2 ** 30 + 1)) == UNSUPPORTED and f(sh(dv=2 ** 22 + 1)) == UNSUPPORTED
-    for B_, H, d in ((2 ** 28, 1, 1), (2 ** 22, 1, 64), (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 22), (1, 64, 2 ** 22)):
+    assert f(sh(T=2 ** 30 + 1)) == UNSUPPORTED and f(sh(dv=2 ** 21 + 1)) == UNSUPPORTED
+    for B_, H, d in ((2 ** 28, 1, 1), (2 ** 22, 1, 64), (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 21), (1, 128, 2 ** 21)):
         assert f(sh(B=B_, H=H, dv=d, T=1)) == UNSUPPORTED and "B*H*dv" in B.dn_last_error()
     assert f(sh(B=2 ** 28 - 64, H=1, dv=1, T=1), x=None) == INVALID   # the most that one launch holds
 
