@@ -678,33 +678,37 @@ struct GsPlan {
     long strips;
 };
 
-// Lanes take the channels of all heads in a row, so that odd widths leave no lane idle but the
-// last strip's; where a strip's rows lie further apart than a 31-bit byte offset, a strip stays
-// in one head's row.
-bool gs_flat(const GsProblem& pr) {
-    const long rows = 63 / pr.d + 2;   // a strip touches at most that many
-    return rows * pr.T < kRange / 4 / pr.d;
+// Strips of 64 / G channels: of one head's row, or (flat) of the channels of all heads in a row, so
+// that odd widths leave no lane idle, but lanes of two heads read twice the cache lines.  Measured
+// (us, forward, one head's -> flat): d 67 (47 % of the lanes idle), 2000 steps 99 -> 81; d 100 (22 %)
+// 65 -> 72; 777 steps of 15 heads as one tile (few strips either way), d 67 10.1 -> 13.9, but of 150
+// heads of 24, 300 strips -> 225, 15.1 -> 12.4.  So flat where more than a quarter of the lanes
+// would idle, or several runs a wave would take more than one round of the chip; never
+// where a strip's rows lie further apart than a 31-bit byte offset.
+bool gs_flat(const GsProblem& pr, int groups) {
+    const long C = 64 / groups, per = (pr.d + C - 1) / C, rows = 63 / pr.d + 2;   // a strip touches at most that many
+    if (rows * pr.T >= kRange / 4 / pr.d) return false;
+    return groups > 1 ? (long)pr.B * pr.H * per > kGsUnits : 4 * pr.d < 3 * per * C;
 }
 long gs_strips(const GsProblem& pr, int groups) {
     const long BH = (long)pr.B * pr.H, C = 64 / groups;
-    return gs_flat(pr) ? (BH * pr.d + C - 1) / C : BH * ((pr.d + C - 1) / C);
+    return gs_flat(pr, groups) ? (BH * pr.d + C - 1) / C : BH * ((pr.d + C - 1) / C);
 }
 long gs_blocks(long strips, int groups) {   // G > 1: a whole number of 64-channel groups for every XCD
     const long all = groups > 1 ? kXcds * groups : 1;
     return (strips + all - 1) / all * all;
 }
 // Which form.  Measured (us, forward / backward, bf16, coupled; marching with the best G -> chained):
-//     64 strips, 8192 steps        81 / 127 -> 74 / 110      16 strips (fp32), 777 steps   15.4 / 15.5 -> 13.3 / 15.0
-//     157 strips, 4096 steps     110 / 196 -> 94 / 162       4 strips, 4096 steps          19.3 / 26.7 -> 14.6 / 15.5
-//     32 strips, 32768 steps     212 / 300 -> 134 / 205      32 strips, 512 steps             8.8 / 8.6 -> 12.8 / 14.8
+//     64 strips, 8192 steps        81 / 127 -> 74 / 110      4 strips, 4096 steps          19.3 / 26.7 -> 14.6 / 15.5
+//     157 strips, 4096 steps     110 / 196 -> 94 / 162       15 strips (fp32), 777 steps     7.9 / 10.1 -> 12.9 / 14.2
+//     32 strips, 32768 steps     212 / 300 -> 134 / 205      32 strips, 512 steps             7.8 / 8.7 -> 12.8 / 14.8
 //     256 strips, 32768 of 8 documents   113 / 199 (floor 105 / 183; chained 0.85 and 0.97 of that rate)
-// So: few strips of at most 512 steps march, with as many runs of a channel in a wave as make one
+// So: few strips of at most 1024 steps march, with as many runs of a channel in a wave as make one
 // tile of them; longer ones are chained where marching would leave more than a fifth of the
 // chip idle; else strips of 64 channels march.
-constexpr int kGsShort = 512;
+constexpr int kGsShort = 1024;
 GsPlan gs_plan(const GsProblem& pr, bool bwd) {
     GsPlan p{};
-    p.flat = gs_flat(pr);
     p.groups = 1;
     p.strips = gs_strips(pr, 1);
     int tile = bwd ? kGsSaved : kGsWaves * kGsRun;
@@ -721,6 +725,7 @@ GsPlan gs_plan(const GsProblem& pr, bool bwd) {
             p.reach = (int)std::min<long>((bwd ? kGsWavesB : kGsWavesC) * Chain::kEach, std::max<long>(4, kGsUnits / p.strips));
         }
     }
+    p.flat = gs_flat(pr, p.groups);
     p.tiles = (int)(((long)pr.T + (long)tile * p.groups - 1) / ((long)tile * p.groups));
     return p;
 }
@@ -777,8 +782,10 @@ template <typename T, bool COUPLED> hipError_t fwd_launch(const GsPlan& p, const
         hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<T, COUPLED>), grid, block, 0, s, a);
     else if (p.groups == 1)
         DN_GS(1);
-    else
+    else if (p.groups == 2)
         DN_GS(2);
+    else
+        DN_GS(4);
 #undef DN_GS
     prof_end(s);
     return hipGetLastError();
@@ -793,8 +800,10 @@ template <typename T, bool COUPLED> hipError_t bwd_launch(const GsPlan& p, const
         DN_GS(1);
     else if (p.groups == 2)
         DN_GS(2);
-    else
+    else if (p.groups == 4)
         DN_GS(4);
+    else
+        DN_GS(8);
 #undef DN_GS
     prof_end(s);
     return hipGetLastError();

@@ -37,7 +37,8 @@ def run(s, lens=None, coupled=False, h0=True, dhT=True, saved=True, **how):
 
 
 SIZES = [(1, 1, 1, 1), (2, 3, 1, 16), (1, 1, 64, 16), (2, 3, 15, 5), (2, 3, 127, 67), (3, 2, 128, 64), (1, 2, 129, 100),
-         (2, 1, 255, 128), (1, 1, 256, 200), (1, 1, 257, 63), (2, 2, 700, 3), (1, 70, 130, 65)]
+         (2, 1, 255, 128), (1, 1, 256, 200), (1, 1, 257, 63), (2, 2, 700, 3), (1, 70, 130, 65), (1, 1, 1024, 64),
+         (3, 5, 777, 67), (2, 60, 600, 24), (3, 100, 140, 67)]
 
 
 @pytest.mark.parametrize("coupled", [False, True])
@@ -53,8 +54,8 @@ def test_against_the_definition(size, dtype, coupled):
 
 
 @pytest.mark.parametrize("coupled", [False, True])
-@pytest.mark.parametrize("size", [(1, 1, 513, 1), (1, 1, 5000, 33), (2, 1, 4097, 70), (1, 3, 1025, 64), (3, 1, 16384, 64),
-                                  (2, 70, 520, 130)], ids=str)
+@pytest.mark.parametrize("size", [(1, 1, 1025, 1), (1, 1, 5000, 33), (2, 1, 4097, 70), (1, 3, 1025, 64), (3, 1, 16384, 64),
+                                  (2, 70, 1030, 130), (3, 120, 1030, 67)], ids=str)
 def test_chained_tiles(size, coupled):
     """Channels that do not fill the chip by themselves: the tiles of the steps run at once."""
     Bn, H, T, d = size
@@ -79,7 +80,7 @@ def test_many_channels(dtype):
     check(run(s, lens, True, saved=False), *ref, label="recomputed")
 
 
-@pytest.mark.parametrize("T", [420, 530])
+@pytest.mark.parametrize("T", [420, 530, 1100])
 @pytest.mark.parametrize("d", [7, 64, 100])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_lengths(dtype, d, T):
