@@ -657,9 +657,9 @@ __global__ __launch_bounds__(256) void gated_scan_clear_kernel(uint4* p, long n)
 template <typename T, bool COUPLED>
 __global__ __launch_bounds__(256) void gated_scan_recurrent_kernel(const T* x, const float* g, float* state, T* o, int BH,
                                                                    int steps, int d) {
-    const long n = blockIdx.x * 256L + threadIdx.x, row = n / d;
-    if (row >= BH) return;
-    const long at = row * steps * d + (n - row * d);
+    const unsigned n = blockIdx.x * 256u + threadIdx.x, row = n / d;   // 2^28 channels at most
+    if (row >= (unsigned)BH) return;
+    const long at = (long)row * steps * d + (n - row * d);
     float h = state[n], gn = g[at], xn = to_f(x[at]);
     for (int t = 0; t < steps; ++t) {
         const float gc = gn, xc = xn;

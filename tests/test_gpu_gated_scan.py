@@ -300,3 +300,55 @@ def test_writes_stay_in_their_tensors():
     got = dict(o=p["o"].view(torch.bfloat16), dx=p["dx"].view(torch.bfloat16), dg=p["dg"].view(torch.float32),
                hT=p["hT"].view(torch.float32), dh0=p["dh0"].view(torch.float32))
     check({m: got[m].reshape(val[m].shape) for m in got}, val, err)
+
+
+def test_two_calls_at_once():
+    """Chained calls on two streams, their workgroups on the chip together, again and again."""
+    a, b = inputs(1, 2, 9000, 64, seed=21), inputs(1, 3, 7000, 100, dtype=torch.bfloat16, seed=22)
+    want = [run(a, coupled=True), run(b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(20):
+        for i, (s, c) in enumerate(((a, True), (b, False))):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(s, coupled=c))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            for n in g:
+                assert torch.equal(g[n], want[i][n]), n
+
+
+def test_one_workspace_for_calls_in_turn():
+    """A workspace given by the caller, full of what other calls left in it."""
+    s, other = inputs(1, 2, 3000, 64, seed=31), inputs(1, 1, 5000, 130, seed=32)
+    n = max(B.dn_gated_scan_workspace_bytes(B.make_shape(1, H, T, d, d, 64, "fp32", "vector"), p)
+            for H, T, d in ((2, 3000, 64), (1, 5000, 130)) for p in (B.DN_PASS_FWD, B.DN_PASS_BWD_RECOMPUTE))
+    ws = torch.full((n,), 0x41, dtype=torch.uint8, device="cuda")
+    want = run(s, saved=False)
+    for _ in range(3):
+        run(other, saved=False, ws=ws)
+        got = run(s, saved=False, ws=ws)
+        for m in want:
+            assert torch.equal(got[m], want[m])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last head's results against a call on that head alone."""
+    H, T, d = 33, 1 << 20, 64
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty(1, H, T, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    do = torch.empty(1, H, T, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    g = torch.empty(1, H, T, d, device="cuda").uniform_(-0.3, -0.01, generator=gen)
+    o, hT, st = B.gated_scan_fwd(x, g)
+    gr = B.gated_scan_bwd(x, g, None, do, None, st)
+    last = [t[:, -1:].contiguous() for t in (x, g, do)]
+    o1, hT1, st1 = B.gated_scan_fwd(last[0], last[1])
+    gr1 = B.gated_scan_bwd(last[0], last[1], None, last[2], None, st1)
+    for whole, alone in ((o, o1), (hT, hT1), (gr["dx"], gr1["dx"]), (gr["dg"], gr1["dg"]), (gr["dh0"], gr1["dh0"])):
+        part = whole[:, -1:].float()
+        tol = 2.0 ** -7 if whole.dtype == torch.bfloat16 else 24 * 100 * 2.0 ** -24   # both rounded; 100 steps of memory
+        assert float((part - alone.float()).abs().max()) <= tol * float(alone.float().abs().max())
+        assert float(part.abs().max()) > 0

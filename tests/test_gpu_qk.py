@@ -287,3 +287,21 @@ def test_writes_stay_in_their_tensors():
         assert (whole[m][:2048] == 7).all() and (whole[m][-2048:] == 7).all()
         assert (grid[:, :, 0] == 7).all() and (grid[:, :, -1] == 7).all()
     assert (dw[:, :d] == 7).all() and (dw[:, 2 * d:] == 7).all() and (ws[n:] == 0x5a).all()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows against a call on them alone."""
+    T, H, d = 1 << 18, 33, 128
+    both = torch.empty(1, T, 2 * H, d, dtype=torch.bfloat16, device="cuda").normal_()
+    q, k = both[:, :, :H].transpose(1, 2), both[:, :, H:].transpose(1, 2)
+    f, _ = B.rotary_freqs(d, device="cuda")
+    yq, yk = B.qk_norm_fwd(q, k, freqs=f)
+    gr = B.qk_norm_bwd(q, k, yq, yk, freqs=f)
+    tail = slice(T - 5, T)
+    pos = torch.tensor([T - 5], dtype=torch.int32, device="cuda")
+    q1, k1 = q[:, -1:, tail], k[:, -1:, tail]
+    zq, zk = B.qk_norm_fwd(q1, k1, freqs=f, pos=pos)
+    g1 = B.qk_norm_bwd(q1, k1, zq, zk, freqs=f, pos=pos)
+    for whole, part in ((yq, zq), (yk, zk), (gr["dq"], g1["dq"]), (gr["dk"], g1["dk"])):
+        assert torch.equal(whole[:, -1:, tail], part)
+    assert float(zk.abs().max()) > 0
