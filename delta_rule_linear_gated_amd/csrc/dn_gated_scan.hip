@@ -312,9 +312,9 @@ struct Chain {
 };
 
 // Forward, marching.  Outputs, saved states and the last state, each where wanted.
-template <typename T, bool COUPLED, int G>
-__global__ __launch_bounds__(64 * kGsWaves) void gated_scan_fwd_kernel(GsArgs a) {
-    constexpr int R = kGsRun, W = kGsWaves, TILE = W * G * R, C = 64 / G;
+template <typename T, bool COUPLED, int W, int G>
+__global__ __launch_bounds__(64 * W, 4) void gated_scan_fwd_kernel(GsArgs a) {
+    constexpr int R = kGsRun, TILE = W * G * R, C = 64 / G;
     __shared__ float2 part[2][W][C];
     const int w = uniform_wave(), lane = lane_id(), c = lane % C, strip = gs_strip<G>();
     if (strip >= a.strips) return;
@@ -455,10 +455,10 @@ template <typename T, bool COUPLED> __global__ __launch_bounds__(64 * kGsWavesC)
 }
 
 // Backward, marching from the last step; k: tiles behind this one.
-template <typename T, bool COUPLED, int G>
-__global__ __launch_bounds__(64 * kGsWavesB) void gated_scan_bwd_kernel(GsArgs a) {
-    constexpr int R = kGsRunB, W = kGsWavesB, TILE = W * G * R, C = 64 / G;
-    constexpr int SHARE = W / G;   // waves on the steps of one saved state
+template <typename T, bool COUPLED, int W, int G>
+__global__ __launch_bounds__(64 * W, 2) void gated_scan_bwd_kernel(GsArgs a) {
+    constexpr int R = kGsRunB, TILE = W * G * R, C = 64 / G;
+    constexpr int SHARE = W < kGsWavesB ? W : W / G;   // waves on the steps of one saved state (fewer waves: one tile, of the first)
     __shared__ float2 fore[2][W][C], back[2][W][C];
     const int w = uniform_wave(), lane = lane_id(), c = lane % C, strip = gs_strip<G>();
     if (strip >= a.strips) return;
@@ -674,7 +674,7 @@ __global__ __launch_bounds__(256) void gated_scan_recurrent_kernel(const T* x, c
 size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct GsPlan {
-    int flat, chain, groups, tiles, reach;   // groups: runs of a channel in a wave (G)
+    int flat, chain, waves, groups, tiles, reach;   // groups: runs of a channel in a wave (G)
     long strips;
 };
 
@@ -706,12 +706,17 @@ long gs_blocks(long strips, int groups) {   // G > 1: a whole number of 64-chann
 // So: few strips of at most 1024 steps march, with as many runs of a channel in a wave as make one
 // tile of them; longer ones are chained where marching would leave more than a fifth of the
 // chip idle; else strips of 64 channels march.
+// Waves: up to 128 steps only those whose runs they are (131072 channels, 16 steps, of 16 waves -> of
+// one: 44 -> 6.8 us).  Longer, forward: 16 where a unit has one strip (256 strips, 4096 steps:
+// 113 us, of 8 waves 119), 8 where it has two, whose loads then overlap (2048 strips, 512 steps:
+// 133 -> 111; 512 strips, 4096 steps: 224 -> 219; fp32, 1024 strips: 633 -> 646).
 constexpr int kGsShort = 1024;
 GsPlan gs_plan(const GsProblem& pr, bool bwd) {
     GsPlan p{};
     p.groups = 1;
     p.strips = gs_strips(pr, 1);
-    int tile = bwd ? kGsSaved : kGsWaves * kGsRun;
+    p.waves = pr.T <= 16 ? 1 : pr.T <= 64 ? 4 : bwd || pr.T <= 128 || p.strips >= 2 * kGsUnits ? 8 : kGsWaves;
+    int tile = 16 * p.waves;
     const long rounds = (p.strips + kGsUnits - 1) / kGsUnits;
     if (pr.T <= kGsShort && p.strips < kGsUnits) {
         while (tile * p.groups < pr.T) p.groups *= 2;
@@ -775,35 +780,45 @@ unsigned gs_grid(const GsPlan& p) {
 }
 
 template <typename T, bool COUPLED> hipError_t fwd_launch(const GsPlan& p, const GsArgs& a, hipStream_t s) {
-    const dim3 grid(gs_grid(p)), block(64 * (p.chain ? kGsWavesC : kGsWaves));
+    const dim3 grid(gs_grid(p));
     prof_begin(s, "gated_scan_fwd");
-#define DN_GS(G) hipLaunchKernelGGL((gated_scan_fwd_kernel<T, COUPLED, G>), grid, block, 0, s, a)
+#define DN_GS(W, G) hipLaunchKernelGGL((gated_scan_fwd_kernel<T, COUPLED, W, G>), grid, dim3(64 * W), 0, s, a)
     if (p.chain)
-        hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<T, COUPLED>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((gated_scan_fwd_chain_kernel<T, COUPLED>), grid, dim3(64 * kGsWavesC), 0, s, a);
+    else if (p.waves == 1)
+        DN_GS(1, 1);
+    else if (p.waves == 4)
+        DN_GS(4, 1);
+    else if (p.waves == 8)
+        DN_GS(8, 1);
     else if (p.groups == 1)
-        DN_GS(1);
+        DN_GS(16, 1);
     else if (p.groups == 2)
-        DN_GS(2);
+        DN_GS(16, 2);
     else
-        DN_GS(4);
+        DN_GS(16, 4);
 #undef DN_GS
     prof_end(s);
     return hipGetLastError();
 }
 template <typename T, bool COUPLED> hipError_t bwd_launch(const GsPlan& p, const GsArgs& a, hipStream_t s) {
-    const dim3 grid(gs_grid(p)), block(64 * kGsWavesB);
+    const dim3 grid(gs_grid(p));
     prof_begin(s, "gated_scan_bwd");
-#define DN_GS(G) hipLaunchKernelGGL((gated_scan_bwd_kernel<T, COUPLED, G>), grid, block, 0, s, a)
+#define DN_GS(W, G) hipLaunchKernelGGL((gated_scan_bwd_kernel<T, COUPLED, W, G>), grid, dim3(64 * W), 0, s, a)
     if (p.chain)
-        hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<T, COUPLED>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((gated_scan_bwd_chain_kernel<T, COUPLED>), grid, dim3(64 * kGsWavesB), 0, s, a);
+    else if (p.waves == 1)
+        DN_GS(1, 1);
+    else if (p.waves == 4)
+        DN_GS(4, 1);
     else if (p.groups == 1)
-        DN_GS(1);
+        DN_GS(8, 1);
     else if (p.groups == 2)
-        DN_GS(2);
+        DN_GS(8, 2);
     else if (p.groups == 4)
-        DN_GS(4);
+        DN_GS(8, 4);
     else
-        DN_GS(8);
+        DN_GS(8, 8);
 #undef DN_GS
     prof_end(s);
     return hipGetLastError();
@@ -833,7 +848,7 @@ size_t gs_states_bytes(const GsProblem& pr) {
 size_t gs_workspace_bytes(const GsProblem& pr, int pass) { return gs_ws(pr, pass).total; }
 bool gs_fits(const GsProblem& pr) {
     if (pr.B == 0 || pr.H == 0) return true;
-    return (long)pr.B * pr.H <= 0x7fffffffL && gs_blocks(gs_strips(pr, 1), 1) < (1L << 32) / (64 * kGsWaves);
+    return (long)pr.B * pr.H <= 0x7fffffffL && gs_strips(pr, 1) < (1L << 32) / (64 * kGsWaves);
 }
 
 hipError_t launch_gated_scan_fwd(const GsProblem& pr, const GsFwd& f, char* ws, hipStream_t s) {

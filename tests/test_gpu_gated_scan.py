@@ -38,7 +38,8 @@ def run(s, lens=None, coupled=False, h0=True, dhT=True, saved=True, **how):
 
 SIZES = [(1, 1, 1, 1), (2, 3, 1, 16), (1, 1, 64, 16), (2, 3, 15, 5), (2, 3, 127, 67), (3, 2, 128, 64), (1, 2, 129, 100),
          (2, 1, 255, 128), (1, 1, 256, 200), (1, 1, 257, 63), (2, 2, 700, 3), (1, 70, 130, 65), (1, 1, 1024, 64),
-         (3, 5, 777, 67), (2, 60, 600, 24), (3, 100, 140, 67)]
+         (3, 5, 777, 67), (2, 60, 600, 24), (3, 100, 140, 67), (2, 3, 16, 70), (1, 1, 17, 128), (5, 2, 65, 9),
+         (8, 64, 270, 64)]
 
 
 @pytest.mark.parametrize("coupled", [False, True])
