@@ -186,7 +186,7 @@ def run(state):
         if op == "scan_step":
             o = dn.gated_scan_recurrent_fwd(s["x"], s["g"], s["state"], coupled=c["coupled"])
             return {"o": o, "state": s["state"]}
-        turn = dict(freqs=s["freqs"], pos=s["pos"], interleaved=c["interleaved"], amplitude=s["amplitude"],
+        turn = dict(freqs=s["freqs"], pos=s["pos"] if c["rot"] else None, interleaved=c["interleaved"], amplitude=s["amplitude"],
                     lens=s["lens"])
         if op.startswith("norm"):
             turn.update(norm=c["norm"], eps=EPS)
