@@ -142,7 +142,7 @@ __device__ __forceinline__ void qk_group(const QkArgs& a, int group, int& side, 
     n = min(a.per, a.side[side].heads - h0);
 }
 
-// Grid: token tiles, then head groups.
+// Grid: workgroups that walk the token tiles of their head group in steps of a.tiles.
 template <typename T, int D, int TURN, bool NORM> __global__ __launch_bounds__(kQkThreads) void qk_fwd_kernel(QkArgs a) {
     constexpr int LANES = D / 8, TOKENS = kQkThreads / LANES;
     constexpr bool APART = TURN == kTurnHalves;
@@ -151,41 +151,46 @@ template <typename T, int D, int TURN, bool NORM> __global__ __launch_bounds__(k
     qk_group(a, blockIdx.x / a.tiles, sd, h0, nh);
     const QkSide& S = a.side[sd];
     QkPlace k;
-    qk_place<D, TURN>(a, blockIdx.x % a.tiles * TOKENS + threadIdx.x / LANES, p, k);
-    float c[4], s[4], w[8];
-    const T* x = static_cast<const T*>(S.x) + k.b * S.xs[0] + h0 * S.xs[1] + k.t * S.xs[2];
-    T* y = static_cast<T*>(S.out) + k.b * S.os[0] + h0 * S.os[1] + k.t * S.os[2];
-    QkRow<T> rows[kQkHeads];
-    auto fetch = [&](int h) {
-#pragma unroll
-        for (int i = 0; i < kQkHeads; ++i)
-            if (k.live && h + i < nh) rows[i].template load<APART>(x + (h + i) * S.xs[1], k.at, k.bt);
-    };
-    fetch(0);
-    if (TURN != kTurnNone) qk_angles(a, k, p, a.back ? -1.f : 1.f, c, s);
+    qk_place<D, TURN>(a, 0, p, k);   // the lane's elements are the same for every token
+    float w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = NORM && S.w ? S.w[i < 4 ? k.at + i : k.bt + i - 4] : 1.f;
-    for (int h = 0; h < nh; h += kQkHeads) {
-        if (h) fetch(h);
+    const long tokens = (long)a.B * a.T;
+    for (long m0 = blockIdx.x % a.tiles * (long)TOKENS; m0 < tokens; m0 += a.tiles * (long)TOKENS) {
+        qk_place<D, TURN>(a, (int)min(m0 + threadIdx.x / LANES, tokens), p, k);
+        float c[4], s[4];
+        const T* x = static_cast<const T*>(S.x) + k.b * S.xs[0] + h0 * S.xs[1] + k.t * S.xs[2];
+        T* y = static_cast<T*>(S.out) + k.b * S.os[0] + h0 * S.os[1] + k.t * S.os[2];
+        QkRow<T> rows[kQkHeads];
+        auto fetch = [&](int h) {
 #pragma unroll
-        for (int i = 0; i < kQkHeads; ++i) {
-            if (h + i >= nh) break;
-            float v[8] = {};
-            if (k.live) rows[i].open(v);
-            if (NORM) {
-                float sum = 0.f;
+            for (int i = 0; i < kQkHeads; ++i)
+                if (k.live && h + i < nh) rows[i].template load<APART>(x + (h + i) * S.xs[1], k.at, k.bt);
+        };
+        fetch(0);
+        if (TURN != kTurnNone) qk_angles(a, k, p, a.back ? -1.f : 1.f, c, s);
+        for (int h = 0; h < nh; h += kQkHeads) {
+            if (h) fetch(h);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
-                const float r = rsqrtf(fmaf(qk_row_sum<D>(sum), a.share, a.eps));
+            for (int i = 0; i < kQkHeads; ++i) {
+                if (h + i >= nh) break;
+                float v[8] = {};
+                if (k.live) rows[i].open(v);
+                if (NORM) {
+                    float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = v[j] * r * w[j];
+                    for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
+                    const float r = rsqrtf(fmaf(qk_row_sum<D>(sum), a.share, a.eps));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = v[j] * r * w[j];
+                }
+                if (TURN != kTurnNone && k.turned) qk_turn<TURN>(v, c, s);
+                if (!k.live) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+                }
+                if (k.there) QkRow<T>::template store<APART>(y + (h + i) * S.os[1], k.at, k.bt, v);
             }
-            if (TURN != kTurnNone && k.turned) qk_turn<TURN>(v, c, s);
-            if (!k.live) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0.f;
-            }
-            if (k.there) QkRow<T>::template store<APART>(y + (h + i) * S.os[1], k.at, k.bt, v);
         }
     }
 }
