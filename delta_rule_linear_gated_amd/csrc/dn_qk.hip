@@ -45,9 +45,12 @@ __global__ __launch_bounds__(1024) void qk_dw_kernel(QkArgs a) {
 // heads, 1024 steps) 7.5 / 8.0 / 7.3.
 // As many workgroups as run at once, each walking the token tiles, keep reads and writes apart
 // less than a workgroup a tile does: 4 a unit against 8 (backward, l2) 305 -> 350 us (6: 311, 3: 299,
-// 2: 343), against one a tile (forward, l2) 211 -> 220, rotation alone 212 -> 221; but for the rotation
-// back, whose rows lie head by head on both sides, 231 -> 217.
-void qk_split(QkArgs* a) {
+// 2: 343), against one a tile (forward, l2) 211 -> 220, rotation alone 212 -> 221.  But the rotation
+// back, whose rows lie head by head on both sides, takes 231 -> 217, and with the lengths of a
+// padded batch the tiles differ in work (8 sequences of up to 4096 steps, 16 + 16 heads, forward:
+// 101 -> 85): then a workgroup a tile, or in the backward, whose workgroups each leave a partial
+// sum, 8 a unit.
+void qk_split(QkArgs* a, bool bwd) {
     const long tokens = (long)a->B * a->T, per_wg = 256 / (a->d / 8);
     const long tiles = (tokens + per_wg - 1) / per_wg;
     const int most = std::max(a->side[0].heads, a->side[1].heads);
@@ -58,7 +61,8 @@ void qk_split(QkArgs* a) {
     a->groups[0] = groups(0);
     a->groups[1] = groups(1);
     const long all = std::max((long)a->groups[0] + a->groups[1], 1L);
-    a->tiles = (int)(a->back ? tiles : std::min<long>(tiles, std::max(4 * kQkUnits / all, 1L)));
+    const bool uneven = a->lens || a->back;
+    a->tiles = (int)(uneven && !bwd ? tiles : std::min<long>(tiles, std::max((uneven ? 8 : 4) * kQkUnits / all, 1L)));
 }
 
 }  // namespace
@@ -66,20 +70,21 @@ void qk_split(QkArgs* a) {
 bool qk_fits(const QkArgs& in) {
     QkArgs a = in;
     a.back = 1;   // the most workgroups
-    qk_split(&a);
+    qk_split(&a, false);
     return (long)a.tiles * ((long)a.groups[0] + a.groups[1]) < (1L << 32) / 256;
 }
 
 size_t qk_workspace_bytes(const QkArgs& in) {
     QkArgs a = in;
     if ((long)a.B * a.T == 0) return 0;
-    qk_split(&a);
+    a.back = 1;   // the most workgroups, as with lengths
+    qk_split(&a, true);
     return (size_t)a.tiles * (a.groups[0] + a.groups[1]) * a.d * 4;
 }
 
 hipError_t launch_qk_fwd(QkArgs a, hipStream_t s) {
     if ((long)a.B * a.T * (a.side[0].heads + a.side[1].heads) == 0) return hipSuccess;
-    qk_split(&a);
+    qk_split(&a, false);
     prof_begin(s, "qk_fwd");
     const hipError_t e = (a.bf16 ? qk_fwd_bf16 : qk_fwd_f32)(a, (unsigned)(a.tiles * (a.groups[0] + a.groups[1])), s);
     prof_end(s);
@@ -89,7 +94,7 @@ hipError_t launch_qk_fwd(QkArgs a, hipStream_t s) {
 hipError_t launch_qk_bwd(QkArgs a, char* ws, hipStream_t s) {
     const bool none = (long)a.B * a.T * (a.side[0].heads + a.side[1].heads) == 0;
     hipError_t e = hipSuccess;
-    qk_split(&a);
+    qk_split(&a, true);
     a.parts = reinterpret_cast<float*>(ws);
     if (none) {
         a.tiles = 0;   // sums of nothing

@@ -142,7 +142,15 @@ __device__ __forceinline__ void qk_group(const QkArgs& a, int group, int& side, 
     n = min(a.per, a.side[side].heads - h0);
 }
 
-// Grid: workgroups that walk the token tiles of their head group in steps of a.tiles.
+// The token tile of a workgroup in a round of a.tiles.  Shifted from round to round: at equal steps
+// a workgroup could find the same steps of every sequence, and the ends of a padded batch leave
+// half of the workgroups without work.
+__device__ __forceinline__ long qk_tile(const QkArgs& a, int round) {
+    const int shift = (int)((long)a.tiles * 5 / 8);
+    return round * (long)a.tiles + (blockIdx.x % a.tiles + round * (long)shift) % a.tiles;
+}
+
+// Grid: workgroups that walk the token tiles of their head group.
 template <typename T, int D, int TURN, bool NORM> __global__ __launch_bounds__(kQkThreads) void qk_fwd_kernel(QkArgs a) {
     constexpr int LANES = D / 8, TOKENS = kQkThreads / LANES;
     constexpr bool APART = TURN == kTurnHalves;
@@ -156,7 +164,9 @@ template <typename T, int D, int TURN, bool NORM> __global__ __launch_bounds__(k
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = NORM && S.w ? S.w[i < 4 ? k.at + i : k.bt + i - 4] : 1.f;
     const long tokens = (long)a.B * a.T;
-    for (long m0 = blockIdx.x % a.tiles * (long)TOKENS; m0 < tokens; m0 += a.tiles * (long)TOKENS) {
+    for (int round = 0; round * (long)a.tiles * TOKENS < tokens; ++round) {
+        const long m0 = qk_tile(a, round) * TOKENS;
+        if (m0 >= tokens) continue;
         qk_place<D, TURN>(a, (int)min(m0 + threadIdx.x / LANES, tokens), p, k);
         float c[4], s[4];
         const T* x = static_cast<const T*>(S.x) + k.b * S.xs[0] + h0 * S.xs[1] + k.t * S.xs[2];
@@ -212,7 +222,9 @@ template <typename T, int D, int TURN, bool DW> __global__ __launch_bounds__(kQk
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = S.w ? S.w[i < 4 ? k.at + i : k.bt + i - 4] : 1.f;
     const long ystep = (long)a.T * D, tokens = (long)a.B * a.T;
-    for (long m0 = blockIdx.x % a.tiles * (long)TOKENS; m0 < tokens; m0 += a.tiles * (long)TOKENS) {
+    for (int round = 0; round * (long)a.tiles * TOKENS < tokens; ++round) {
+        const long m0 = qk_tile(a, round) * TOKENS;
+        if (m0 >= tokens) continue;
         qk_place<D, TURN>(a, (int)min(m0 + threadIdx.x / LANES, tokens), p, k);
         float c[4], s[4];
         const T* x = static_cast<const T*>(S.x) + k.b * S.xs[0] + h0 * S.xs[1] + k.t * S.xs[2];
