@@ -1035,7 +1035,7 @@ def qk_norm_bwd(q, k, dyq, dyk, wq=None, wk=None, norm="l2", eps=1e-6, freqs=Non
 
 
 def rotary_fwd(q, k, freqs, pos=None, interleaved=False, amplitude=1.0, lens=None, stream=None):
-    """Rows of queries and keys rotated by position: of the first 2 * len(freqs) elements of a head the pairs
+    """Rows of queries and keys rotated by position: of the first 2 * len(freqs) (a multiple of 8) elements of a head the pairs
     (m, m + len(freqs)) or, ``interleaved``, (2m, 2m + 1) by position * freqs[m], times ``amplitude`` (see
     rotary_freqs); the others stay.  q [B,Hq,T,d], k [B,Hk,T,d] (either None), any order of the dimensions but the last;
     ``pos``: None (the step), int32 [B] (the position of the first step) or int32 [B,T]; ``lens``: int32 [B], rows from
@@ -1060,7 +1060,8 @@ def rotary_bwd(dyq, dyk, freqs, pos=None, interleaved=False, amplitude=1.0, lens
 
 
 class QKNorm(torch.autograd.Function):
-    """yq, yk = QKNorm.apply(q, k, wq, wk, norm, eps, freqs, pos, interleaved, amplitude, lens), as qk_norm_fwd."""
+    """yq, yk = QKNorm.apply(q, k, wq, wk, norm, eps, freqs, pos, interleaved, amplitude, lens), as qk_norm_fwd.  For
+    capture into a HIP graph see LinearAttention."""
 
     @staticmethod
     def forward(ctx, q, k, wq=None, wk=None, norm="l2", eps=1e-6, freqs=None, pos=None, interleaved=False,
@@ -1079,7 +1080,8 @@ class QKNorm(torch.autograd.Function):
 
 
 class Rotary(torch.autograd.Function):
-    """yq, yk = Rotary.apply(q, k, freqs, pos, interleaved, amplitude, lens), as rotary_fwd."""
+    """yq, yk = Rotary.apply(q, k, freqs, pos, interleaved, amplitude, lens), as rotary_fwd.  For capture into a HIP
+    graph see LinearAttention."""
 
     @staticmethod
     def forward(ctx, q, k, freqs, pos=None, interleaved=False, amplitude=1.0, lens=None):

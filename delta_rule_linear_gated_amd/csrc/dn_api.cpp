@@ -1159,6 +1159,7 @@ dn_status qk_strides(const dn::QkArgs& a, int heads, const int64_t stride[3], bo
 }
 
 void qk_dense(const dn::QkArgs& a, int heads, long to[3]) {
+    if (a.B == 0) return;   // no rows: heads and steps may be any
     to[0] = (long)heads * a.T * a.d;
     to[1] = (long)a.T * a.d;
     to[2] = a.d;

@@ -419,8 +419,7 @@ dn_status dn_tree_commit_counts(const dn_shape* shape, const void* k, const floa
  *            last step, o, dx and dg are zero there)
  *   forward : o io like x; hT fp32 [B][H][dv] (NULL = not wanted); states (fp32,
  *            dn_gated_scan_states_bytes: [B][H][ceil(T / 128)][dv], the state entering
- *            each run of 128 steps; those behind a sequence's end are left as they were;
- *            NULL = not saved)
+ *            each run of 128 steps, behind a sequence's end its last one; NULL = not saved)
  *   backward: the vector-Jacobian products of L = <o, dout> + <hT, dhT> (dhT NULL = zero):
  *            dx io, dg fp32 like g, dh0 fp32 (NULL = not wanted), from the states that the
  *            forward saved for the same inputs (h0 is then not read) or, NULL, from h0
