@@ -44,7 +44,7 @@ struct GsArgs {
     int BH, H, T, d;
     int strips, tiles;           // tiles of a strip
     int reach;                   // a chained tile takes at most reach maps before its own
-    int flat;                    // channel of a lane: 64 strip + lane of all, else of one head's row
+    int flat;                    // strips of the channels of all heads in a row, else of one head's
     int NS;                      // saved states of a row
     const void *x, *y;           // y: dout
     const float* g;
@@ -702,7 +702,7 @@ long gs_blocks(long strips, int groups) {   // G > 1: a whole number of 64-chann
 //     64 strips, 8192 steps        81 / 127 -> 74 / 110      4 strips, 4096 steps          19.3 / 26.7 -> 14.6 / 15.5
 //     157 strips, 4096 steps     110 / 196 -> 94 / 162       15 strips (fp32), 777 steps     7.9 / 10.1 -> 12.9 / 14.2
 //     32 strips, 32768 steps     212 / 300 -> 134 / 205      32 strips, 512 steps             7.8 / 8.7 -> 12.8 / 14.8
-//     256 strips, 32768 of 8 documents   113 / 199 (floor 105 / 183; chained 0.85 and 0.97 of that rate)
+// (256 strips, 4096 steps, as many bytes as 32 strips, 32768 steps: marching 113 / 199, floor 105 / 183.)
 // So: few strips of at most 1024 steps march, with as many runs of a channel in a wave as make one
 // tile of them; longer ones are chained where marching would leave more than a fifth of the
 // chip idle; else strips of 64 channels march.
