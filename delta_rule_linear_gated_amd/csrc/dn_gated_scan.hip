@@ -726,7 +726,8 @@ GsPlan gs_plan(const GsProblem& pr, bool bwd) {
         if (p.strips * (((long)pr.T + ctile - 1) / ctile) < (1L << 30)) {
             p.chain = 1;
             tile = ctile;
-            // the tiles of a strip that are in flight at once (twice as many: within 2 %)
+            // the tiles of a strip that are in flight at once (twice as many: within 2 %), as far as every
+            // wave has eight to ask for (more for one strip, 65536 steps: 29 -> 33 us)
             p.reach = (int)std::min<long>((bwd ? kGsWavesB : kGsWavesC) * Chain::kEach, std::max<long>(4, kGsUnits / p.strips));
         }
     }
