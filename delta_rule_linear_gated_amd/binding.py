@@ -800,28 +800,31 @@ def tree_commit(k, u, g, parent, accept, state, stream=None, counts=None):
 # ------------------------------------------------------------------ gated linear recurrence
 
 
+def _fits(t, dt, shp, index):
+    """What _check_tensors asks of one tensor, without its messages; index: of the CUDA device, -1: on the CPU."""
+    return t.dtype is dt and t.shape == shp and t.is_contiguous() and t.get_device() == index
+
+
 def _scan_args(x, g, coupled, ws=None, h0=None, state=None, lens=None, do=None, dhT=None, states=None):
     """Shape descriptor of checked tensors."""
     shape = x.shape
     if len(shape) != 4:
         raise ValueError(f"x must be [B,H,T,d], got shape {tuple(shape)}")
     B, H, T, d = shape
-    io, f32, dev = x.dtype, torch.float32, x.device
+    io, f32, index = x.dtype, torch.float32, x.get_device()
     if io not in _IO_DTYPES:
         raise ValueError(f"x must be float32 or bfloat16, got {io}")
-    if ws is not None and not (ws.is_contiguous() and ws.device == dev):   # its size: the C ABI
-        raise ValueError(f"ws must be contiguous and on {dev}")
-    want = [("x", x, io, shape), ("g", g, f32, shape)]   # and what is given: a checked tensor costs 0.6 us
-    for n, t in (("h0", h0), ("state", state), ("dhT", dhT)):
-        if t is not None:
-            want.append((n, t, f32, (B, H, d)))
-    if lens is not None:
-        want.append(("lens", lens, torch.int32, (B,)))
-    if do is not None:
-        want.append(("do", do, io, shape))
-    if states is not None:
-        want.append(("states", states, f32, (B, H, -(-T // 128), d)))
-    _check_tensors(dev, *want)
+    if ws is not None and not (ws.is_contiguous() and ws.device == x.device):   # its size: the C ABI
+        raise ValueError(f"ws must be contiguous and on {x.device}")
+    row = (B, H, d)
+    if not (_fits(x, io, shape, index) and _fits(g, f32, shape, index) and (h0 is None or _fits(h0, f32, row, index))
+            and (state is None or _fits(state, f32, row, index)) and (dhT is None or _fits(dhT, f32, row, index))
+            and (do is None or _fits(do, io, shape, index)) and (lens is None or _fits(lens, torch.int32, (B,), index))
+            and (states is None or _fits(states, f32, (B, H, -(-T // 128), d), index))
+            and index >= 0 and index == torch.cuda.current_device()):
+        _check_tensors(x.device, ("x", x, io, shape), ("g", g, f32, shape), ("h0", h0, f32, row),
+                       ("state", state, f32, row), ("dhT", dhT, f32, row), ("do", do, io, shape),
+                       ("lens", lens, torch.int32, (B,)), ("states", states, f32, (B, H, -(-T // 128), d)))
     return Shape(B, H, T, d, d, 64, DN_BF16 if io is torch.bfloat16 else DN_F32, DN_GATE_VECTOR,
                  DN_FLAG_COUPLED if coupled else 0, 0.0)
 
@@ -942,32 +945,28 @@ def _qk_args(q, k, wq, wk, norm, eps, freqs, pos, interleaved, amplitude, lens, 
         raise ValueError(f"{names[0]} or {names[1]} must be given")
     if one.dim() != 4:
         raise ValueError(f"{names[0]} and {names[1]} must be [B,heads,T,d], got shape {tuple(one.shape)}")
-    B, _, T, d = one.shape
-    io, dev = one.dtype, one.device
+    B, Hq, T, d = one.shape
+    io, index = one.dtype, one.get_device()
     if io not in _IO_DTYPES:
         raise ValueError(f"{names[0]} and {names[1]} must be float32 or bfloat16, got {io}")
-    rows = []
-    for n, t, dy in ((names[0], q, dyq), (names[1], k, dyk)):
-        if t is None:
-            rows += (0, (0, 0, 0))
-            continue
-        if t.dim() != 4:
-            raise ValueError(f"{n} must be [{B},heads,{T},{d}], got shape {tuple(t.shape)}")
-        b, heads, steps, width = t.shape
-        if b != B or steps != T or width != d:
-            raise ValueError(f"{n} must be [{B},heads,{T},{d}], got shape {tuple(t.shape)}")
-        if t.dtype != io:
-            raise ValueError(f"{n} must be {io}, got {t.dtype}")
-        if t.device != dev:
-            raise ValueError(f"every tensor must be on {dev}, found one on {t.device}")
-        st = t.stride()
-        if st[3] != 1 and d > 1:
-            raise ValueError(f"the rows of {n} must be dense")
-        rows += (heads, st[:3])
-        if dy is not None and (dy.dtype != io or dy.shape != t.shape or not dy.is_contiguous() or dy.device != dev):
-            raise ValueError(f"d{'y' + n} must be contiguous {io} of shape {tuple(t.shape)} on {dev}, got {dy.dtype}, "
-                             f"{tuple(dy.shape)} on {dy.device}")
-    rot, kind = 0, DN_POS_STEP
+    sq = one.stride()
+    if sq[3] != 1 and d > 1:
+        raise ValueError(f"the rows of {names[0]} and {names[1]} must be dense")
+    if q is None:
+        Hk, sk, Hq, sq = Hq, sq, 0, (0, 0, 0)
+    elif k is None:
+        Hk, sk = 0, (0, 0, 0)
+    else:
+        if k.dim() != 4 or k.shape[0] != B or k.shape[2] != T or k.shape[3] != d:
+            raise ValueError(f"{names[1]} must be [{B},heads,{T},{d}], got shape {tuple(k.shape)}")
+        if k.dtype is not io:
+            raise ValueError(f"{names[1]} must be {io}, got {k.dtype}")
+        if k.get_device() != index:
+            raise ValueError(f"every tensor must be on {q.device}, found one on {k.device}")
+        Hk, sk = k.shape[1], k.stride()
+        if sk[3] != 1 and d > 1:
+            raise ValueError(f"the rows of {names[1]} must be dense")
+    rot, kind, pshape = 0, DN_POS_STEP, None
     if freqs is not None:
         if freqs.dim() != 1:
             raise ValueError(f"freqs must be [rot / 2], got shape {tuple(freqs.shape)}")
@@ -975,25 +974,21 @@ def _qk_args(q, k, wq, wk, norm, eps, freqs, pos, interleaved, amplitude, lens, 
             raise ValueError("freqs is a constant: it gets no gradient")
         rot = 2 * freqs.shape[0]
         if pos is not None:
-            kind = DN_POS_EACH if pos.dim() == 2 else DN_POS_START
+            kind, pshape = (DN_POS_EACH, (B, T)) if pos.dim() == 2 else (DN_POS_START, (B,))
     elif pos is not None:
         raise ValueError("pos without freqs")
-    f32, i32 = torch.float32, torch.int32
-    want = []   # of what is given: a checked tensor costs 0.6 us
-    if freqs is not None:
-        want.append(("freqs", freqs, torch.float64, (rot // 2,)))
-    if pos is not None:
-        want.append(("pos", pos, i32, (B, T) if kind == DN_POS_EACH else (B,)))
-    if wq is not None:
-        want.append(("wq", wq, f32, (d,)))
-    if wk is not None:
-        want.append(("wk", wk, f32, (d,)))
-    if lens is not None:
-        want.append(("lens", lens, i32, (B,)))
-    _check_tensors(dev, *want)
-    return QKShape(B, rows[0], rows[2], T, d, rot, DN_BF16 if io == torch.bfloat16 else DN_F32, norm,
-                   DN_ROT_NEIGHBOURS if interleaved else DN_ROT_HALVES, kind, eps, amplitude, *rows[1], *rows[3],
-                   *((0, 0, 0) if dq is None else dq.stride()[:3]), *((0, 0, 0) if dk is None else dk.stride()[:3]))
+    f32, i32, f64 = torch.float32, torch.int32, torch.float64
+    if not ((freqs is None or _fits(freqs, f64, (rot // 2,), index)) and (pos is None or _fits(pos, i32, pshape, index))
+            and (wq is None or _fits(wq, f32, (d,), index)) and (wk is None or _fits(wk, f32, (d,), index))
+            and (lens is None or _fits(lens, i32, (B,), index)) and (dyq is None or _fits(dyq, io, (B, Hq, T, d), index))
+            and (dyk is None or _fits(dyk, io, (B, Hk, T, d), index)) and index >= 0 and index == torch.cuda.current_device()):
+        _check_tensors(one.device, ("freqs", freqs, f64, (rot // 2,)), ("pos", pos, i32, pshape), ("wq", wq, f32, (d,)),
+                       ("wk", wk, f32, (d,)), ("lens", lens, i32, (B,)), ("dyq", dyq, io, (B, Hq, T, d)),
+                       ("dyk", dyk, io, (B, Hk, T, d)))
+    oq, ok = (0, 0, 0) if dq is None else dq.stride(), (0, 0, 0) if dk is None else dk.stride()
+    return QKShape(B, Hq, Hk, T, d, rot, DN_BF16 if io is torch.bfloat16 else DN_F32, norm,
+                   DN_ROT_NEIGHBOURS if interleaved else DN_ROT_HALVES, kind, eps, amplitude, sq[0], sq[1], sq[2], sk[0],
+                   sk[1], sk[2], oq[0], oq[1], oq[2], ok[0], ok[1], ok[2])
 
 
 def _qk_norm(norm):
