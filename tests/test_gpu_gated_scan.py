@@ -81,6 +81,24 @@ def test_many_channels(dtype):
     check(run(s, lens, True, saved=False), *ref, label="recomputed")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [(3, 50, 600, 24), (2, 65, 300, 100), (4, 70, 300, 67), (2, 3, 1500, 100), (3, 40, 1100, 5),
+                                  (3, 1, 140, 1000)], ids=str)
+def test_strips_of_one_and_of_all_heads(size, dtype):
+    """Widths that leave lanes of a strip to the next head's channels or idle, in every form of the scan, with
+    sequences that end inside it; the results that are not wanted left out."""
+    s = inputs(*size, dtype=dtype, seed=sum(size))
+    T = size[2]
+    lens = torch.tensor([T, T - 130, 3, T][:size[0]], dtype=torch.int32).cuda()
+    ref = reference(s["x"], s["g"], s["h0"], lens, True, s["do"], s["dhT"])
+    got = run(s, lens, True)
+    check(got, *ref)
+    o, hT, st = B.gated_scan_fwd(s["x"], s["g"], s["h0"], lens=lens, coupled=True, want_hT=False)
+    gr = B.gated_scan_bwd(s["x"], s["g"], s["h0"], s["do"], s["dhT"], st, lens=lens, coupled=True, want_dh0=False)
+    assert hT is None and gr["dh0"] is None
+    assert torch.equal(o, got["o"]) and torch.equal(gr["dx"], got["dx"]) and torch.equal(gr["dg"], got["dg"])
+
+
 @pytest.mark.parametrize("T", [420, 530, 1100])
 @pytest.mark.parametrize("d", [7, 64, 100])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

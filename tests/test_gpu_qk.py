@@ -305,3 +305,23 @@ def test_offsets_past_32_bits():
     for whole, part in ((yq, zq), (yk, zk), (gr["dq"], g1["dq"]), (gr["dk"], g1["dk"])):
         assert torch.equal(whole[:, -1:, tail], part)
     assert float(zk.abs().max()) > 0
+
+
+def test_one_weight_for_both_and_one_gradient():
+    """The same weight for queries and keys gets both gradients; a weight of one side alone."""
+    s = rows(2, 3, 2, 40, 64, torch.float32, seed=12)
+    w = s["wq"].requires_grad_()
+    yq, yk = B.QKNorm.apply(s["q"], s["k"], w, w, "rms")
+    (gw,) = torch.autograd.grad((yq * s["dyq"]).sum() + (yk * s["dyk"]).sum(), [w])
+    w = w.detach()
+    total, bound = 0, 0
+    for n in "qk":
+        v, e = reference(s[n], w, "rms", 1e-6, dy=s["dy" + n])
+        total, bound = total + v["dw"], bound + e["dw"] + U32 * v["dw"].abs()
+    assert ((gw.double() - total).abs() <= bound).all()
+    gr = B.qk_norm_bwd(s["q"], s["k"], s["dyq"], s["dyk"], None, w, norm="rms")
+    assert gr["dwq"] is None
+    v, e = reference(s["k"], w, "rms", 1e-6, dy=s["dyk"])
+    check({"dw": gr["dwk"], "dx": gr["dk"]}, {n: v[n] for n in ("dw", "dx")}, e)
+    v, e = reference(s["q"], None, "rms", 1e-6, dy=s["dyq"])
+    check({"dx": gr["dq"]}, {"dx": v["dx"]}, e)
