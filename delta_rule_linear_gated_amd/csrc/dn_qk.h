@@ -28,7 +28,7 @@ struct QkArgs {
     int pos_kind;                // 0: t, 1: pos[b] + t, 2: pos[b][t]
     QkSide side[2];
     float* parts;                // partial sums of dw
-    int tiles, groups[2], per;   // launch: token tiles, head groups of each side, heads of a group
+    int tiles, groups[2], per;   // launch: workgroups of a head group, head groups of each side, heads of a group
 };
 bool qk_fits(const QkArgs& a);   // whether one launch holds it
 size_t qk_workspace_bytes(const QkArgs& a);

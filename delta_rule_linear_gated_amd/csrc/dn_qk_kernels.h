@@ -7,8 +7,10 @@
 // members of every rotated pair lie in one lane (halves: elements 4p and rot / 2 + 4p on; else,
 // and in the part that is not rotated, 8p on) and only the row's sum crosses lanes.  A lane
 // keeps its token (its angles: fp64, reduced to an eighth turn, then short series) over the
-// heads of a group.  The bytes of the rows are what bounds it: all rows of a group are
-// loaded before the first is worked on.
+// heads of a group.  The bytes of the rows are what bounds it, read and written once, four rows of
+// a lane in flight (backward: two of each tensor).  At 32 + 32 heads of 128, 32768 steps, bf16: l2
+// 211 us (5.1 TB/s), rms with halves rotated 221, rotation alone 212, backward of l2 306 (5.3 TB/s),
+// of rms with rotation and weights 320; a large copy runs at 5.1 to 5.2.
 #pragma once
 
 #include "dn_device.h"
