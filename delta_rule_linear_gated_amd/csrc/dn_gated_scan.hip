@@ -706,9 +706,13 @@ long gs_blocks(long strips, int groups) {   // G > 1: a whole number of 64-chann
 //     157 strips, 4096 steps     110 / 196 -> 94 / 162       15 strips (fp32), 777 steps     7.9 / 10.1 -> 12.9 / 14.2
 //     32 strips, 32768 steps     212 / 300 -> 134 / 205      32 strips, 512 steps             7.8 / 8.7 -> 12.8 / 14.8
 // (256 strips, 4096 steps, as many bytes as 32 strips, 32768 steps: marching 113 / 199, floor 105 / 183.)
-// So: few strips of at most 1024 steps march, with as many runs of a channel in a wave as make one
-// tile of them; longer ones are chained where marching would leave more than a fifth of the
-// chip idle; else strips of 64 channels march.
+// So: up to 1024 steps march, as many runs of a channel in a wave as make one tile of them and still
+// leave one round of workgroups (224 strips, 1000 steps, of one tile -> so: 41 / 91 -> 31 / 47 us;
+// 15 strips, 777 steps, forward, 16 waves with four runs -> 8 with eight: 8.0 -> 6.2), a round being
+// two workgroups of a unit forward and one backward.  Forward with one instead: 128 strips, 300 steps
+// 9.5 -> 10.5, 57 strips (fp32), 777 steps 10.9 -> 13.1, 224 strips, 300 steps 14.3 -> 14.8, but
+// 64 strips, 1000 steps 13.0 -> 12.1, 160 strips, 600 steps 19.4 -> 18.8.  Longer ones are chained
+// where marching would leave more than a fifth of the chip idle; else strips of 64 channels march.
 // Waves: up to 128 steps only those whose runs they are (131072 channels, 16 steps, of 16 waves -> of
 // one: 44 -> 6.8 us).  Longer, forward: 16 where a unit has one strip (256 strips, 4096 steps:
 // 113 us, of 8 waves 119), 8 where it has two, whose loads then overlap (2048 strips, 512 steps:
@@ -721,8 +725,10 @@ GsPlan gs_plan(const GsProblem& pr, bool bwd) {
     p.waves = pr.T <= 16 ? 1 : pr.T <= 64 ? 4 : bwd || pr.T <= 128 || p.strips >= 2 * kGsUnits ? 8 : kGsWaves;
     int tile = 16 * p.waves;
     const long rounds = (p.strips + kGsUnits - 1) / kGsUnits;
-    if (pr.T <= kGsShort && p.strips < kGsUnits) {
-        while (tile * p.groups < pr.T) p.groups *= 2;
+    if (pr.T > 128 && pr.T <= kGsShort && p.strips < kGsUnits) {
+        auto blocks = [&](int g) { return gs_blocks(gs_strips(pr, g), g); };
+        while (128 * p.groups < pr.T && blocks(2 * p.groups) <= (bwd ? 1 : 2) * kGsUnits) p.groups *= 2;
+        if (p.groups > 1) p.waves = 8, tile = 128;
         p.strips = gs_strips(pr, p.groups);
     } else if (pr.T > kGsShort && p.strips * 5 < rounds * kGsUnits * 4) {
         const int ctile = bwd ? kGsSaved : kGsWavesC * kGsRun;
@@ -793,14 +799,16 @@ template <typename T, bool COUPLED> hipError_t fwd_launch(const GsPlan& p, const
         DN_GS(1, 1);
     else if (p.waves == 4)
         DN_GS(4, 1);
-    else if (p.waves == 8)
-        DN_GS(8, 1);
-    else if (p.groups == 1)
+    else if (p.waves == 16)
         DN_GS(16, 1);
+    else if (p.groups == 1)
+        DN_GS(8, 1);
     else if (p.groups == 2)
-        DN_GS(16, 2);
+        DN_GS(8, 2);
+    else if (p.groups == 4)
+        DN_GS(8, 4);
     else
-        DN_GS(16, 4);
+        DN_GS(8, 8);
 #undef DN_GS
     prof_end(s);
     return hipGetLastError();

@@ -83,7 +83,8 @@ def test_many_channels(dtype):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("size", [(3, 50, 600, 24), (2, 65, 300, 100), (4, 70, 300, 67), (2, 3, 1500, 100), (3, 40, 1100, 5),
-                                  (3, 1, 140, 1000)], ids=str)
+                                  (3, 1, 140, 1000), (4, 40, 300, 64), (3, 10, 700, 64),
+                                  (2, 40, 600, 64), (1, 40, 700, 64)], ids=str)
 def test_strips_of_one_and_of_all_heads(size, dtype):
     """Widths that leave lanes of a strip to the next head's channels or idle, in every form of the scan, with
     sequences that end inside it; the results that are not wanted left out."""
