@@ -711,8 +711,9 @@ long gs_blocks(long strips, int groups) {   // G > 1: a whole number of 64-chann
 // 15 strips, 777 steps, forward, 16 waves with four runs -> 8 with eight: 8.0 -> 6.2), a round being
 // two workgroups of a unit forward and one backward.  Forward with one instead: 128 strips, 300 steps
 // 9.5 -> 10.5, 57 strips (fp32), 777 steps 10.9 -> 13.1, 224 strips, 300 steps 14.3 -> 14.8, but
-// 64 strips, 1000 steps 13.0 -> 12.1, 160 strips, 600 steps 19.4 -> 18.8.  Longer ones are chained
-// where marching would leave more than a fifth of the chip idle; else strips of 64 channels march.
+// 64 strips, 1000 steps 13.0 -> 12.1, 160 strips, 600 steps 19.4 -> 18.8; backward with two: 64
+// strips, 1000 steps 16.5 -> 22.1, 160 strips, 600 steps 25.7 -> 31.0.  Longer ones are chained where
+// marching would leave more than a fifth of the chip idle; else strips of 64 channels march.
 // Waves: up to 128 steps only those whose runs they are (131072 channels, 16 steps, of 16 waves -> of
 // one: 44 -> 6.8 us).  Longer, forward: 16 where a unit has one strip (256 strips, 4096 steps:
 // 113 us, of 8 waves 119), 8 where it has two, whose loads then overlap (2048 strips, 512 steps:
