@@ -31,9 +31,8 @@ COMMON = [
 
 
 def sources() -> list[str]:
-    """dn_api.cpp, dn_profile.cpp and every .hip unit (the per-variant kernel units and dn_launch.hip)."""
-    hips = sorted(f for f in os.listdir(CSRC) if f.endswith(".hip"))
-    return ["dn_api.cpp", "dn_profile.cpp", *hips]
+    """Every .cpp (host code) and .hip unit (the per-variant kernel units and dn_launch.hip)."""
+    return sorted(f for f in os.listdir(CSRC) if f.endswith((".cpp", ".hip")))
 
 
 def _compile(src: str) -> str:

@@ -1,5 +1,5 @@
 // dn_qk.h -- what the C-ABI layer and the kernels of the queries' and keys' norms and
-// rotations (dn_qk.hip, dn_qk_kernels.h) share.  Layouts as in include/dn.h.
+// rotations (dn_qk_plan.cpp, dn_qk.hip, dn_qk_kernels.h) share.  Layouts as in include/dn.h.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -30,6 +30,7 @@ struct QkArgs {
     float* parts;                // partial sums of dw
     int tiles, groups[2], per;   // launch: workgroups of a head group, head groups of each side, heads of a group
 };
+void qk_split(QkArgs* a, bool bwd);
 bool qk_fits(const QkArgs& a);   // whether one launch holds it
 size_t qk_workspace_bytes(const QkArgs& a);
 hipError_t launch_qk_fwd(QkArgs a, hipStream_t s);

@@ -1,7 +1,5 @@
 // dn_qk.hip -- launches of the queries' and keys' norms and rotations
-// (dn_qk_kernels.h): the split of tokens and heads, and the sums of the weights' gradients.
-#include <algorithm>
-
+// (dn_qk_kernels.h), split as dn_qk_plan.cpp says, and the sums of the weights' gradients.
 #include "dn_device.h"
 #include "dn_internal.h"
 #include "dn_qk.h"
@@ -9,8 +7,6 @@
 namespace dn {
 
 namespace {
-
-constexpr int kQkUnits = 256;   // compute units
 
 // Sum of the workgroups' partial dw: 16 channels a workgroup, 64 threads a channel over the
 // entries, eight loads in flight each (the sums are a chain of latencies: 16 threads with one
@@ -39,51 +35,10 @@ __global__ __launch_bounds__(1024) void qk_dw_kernel(QkArgs a) {
     a.side[sd].dw[j] = sum;
 }
 
-// Heads a lane takes, and the workgroups.  More heads a lane share its angles; fewer fill the
-// chip.  Measured at 32 + 32 heads of 128, 32768 steps, bf16 (us, rms with halves rotated, 4 / 8 /
-// 16 heads): 234 / 223 / 217, backward without weights 347 / 329 / 328, with few tokens (16 + 16
-// heads, 1024 steps) 7.5 / 8.0 / 7.3.
-// As many workgroups as run at once, each walking the token tiles, keep reads and writes apart
-// less than a workgroup a tile does: 4 a unit against 8 (backward, l2) 305 -> 350 us (6: 311, 3: 299,
-// 2: 343), against one a tile (forward, l2) 211 -> 220, rotation alone 212 -> 221.  But the rotation
-// back, whose rows lie head by head on both sides, takes 231 -> 217, and with the lengths of a
-// padded batch the tiles differ in work (8 sequences of up to 4096 steps, 16 + 16 heads, forward:
-// 101 -> 85): then a workgroup a tile, or in the backward, whose workgroups each leave a partial
-// sum, 8 a unit.
-void qk_split(QkArgs* a, bool bwd) {
-    const long tokens = (long)a->B * a->T, per_wg = 256 / (a->d / 8);
-    const long tiles = (tokens + per_wg - 1) / per_wg;
-    const int most = std::max(a->side[0].heads, a->side[1].heads);
-    int per = 8;
-    auto groups = [&](int side) { return (a->side[side].heads + per - 1) / per; };
-    while (per > 1 && (per >= 2 * most || tiles * (groups(0) + groups(1)) < 4 * kQkUnits)) per /= 2;
-    a->per = per;
-    a->groups[0] = groups(0);
-    a->groups[1] = groups(1);
-    const long all = std::max((long)a->groups[0] + a->groups[1], 1L);
-    const bool uneven = a->lens || a->back;
-    a->tiles = (int)(uneven && !bwd ? tiles : std::min<long>(tiles, std::max((uneven ? 8 : 4) * kQkUnits / all, 1L)));
-}
-
 }  // namespace
 
-bool qk_fits(const QkArgs& in) {
-    QkArgs a = in;
-    a.back = 1;   // the most workgroups
-    qk_split(&a, false);
-    return (long)a.tiles * ((long)a.groups[0] + a.groups[1]) < (1L << 32) / 256;
-}
-
-size_t qk_workspace_bytes(const QkArgs& in) {
-    QkArgs a = in;
-    if ((long)a.B * a.T == 0) return 0;
-    a.back = 1;   // the most workgroups, as with lengths
-    qk_split(&a, true);
-    return (size_t)a.tiles * (a.groups[0] + a.groups[1]) * a.d * 4;
-}
-
 hipError_t launch_qk_fwd(QkArgs a, hipStream_t s) {
-    if ((long)a.B * a.T * (a.side[0].heads + a.side[1].heads) == 0) return hipSuccess;
+    if ((long)a.B * a.T * ((long)a.side[0].heads + a.side[1].heads) == 0) return hipSuccess;
     qk_split(&a, false);
     prof_begin(s, "qk_fwd");
     const hipError_t e = (a.bf16 ? qk_fwd_bf16 : qk_fwd_f32)(a, (unsigned)(a.tiles * (a.groups[0] + a.groups[1])), s);
@@ -92,7 +47,7 @@ hipError_t launch_qk_fwd(QkArgs a, hipStream_t s) {
 }
 
 hipError_t launch_qk_bwd(QkArgs a, char* ws, hipStream_t s) {
-    const bool none = (long)a.B * a.T * (a.side[0].heads + a.side[1].heads) == 0;
+    const bool none = (long)a.B * a.T * ((long)a.side[0].heads + a.side[1].heads) == 0;
     hipError_t e = hipSuccess;
     qk_split(&a, true);
     a.parts = reinterpret_cast<float*>(ws);
