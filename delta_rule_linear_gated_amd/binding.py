@@ -840,7 +840,8 @@ def gated_scan_fwd(x, g, h0=None, lens=None, coupled=False, save_states=True, wa
     """Gated linear recurrence over whole sequences, a state for each channel: h_t = exp(g_t) h_{t-1} + w_t x_t,
     o_t = h_t, with w_t = 1 or, ``coupled``, 1 - exp(g_t).  x [B,H,T,d] (any d), ``g`` fp32 like x (log-decays),
     ``h0`` fp32 [B,H,d]; ``lens``: int32 [B], the steps of each batch element (o is zero past them, hT the state
-    after them).  Returns (o, hT or None, states or None): states is what gated_scan_bwd takes."""
+    after them); ``ws``: a workspace of the caller's, for calls that are ordered among themselves.  Returns (o, hT or
+    None, states or None): states is what gated_scan_bwd takes."""
     sh = _scan_args(x, g, coupled, ws, h0=h0, lens=lens)
     with _allocating(stream):
         o = torch.empty_like(x)

@@ -21,6 +21,7 @@ struct GsFwd {
     void* o;
     float* hT;
     float* states;
+    int first_tile = 0;   // a chain begins with it (else 0 in tests alone: the messages of those before it never come)
 };
 struct GsBwd {
     const void* x;
@@ -32,6 +33,7 @@ struct GsBwd {
     const float* states;   // NULL: recomputed in the workspace
     void* dx;
     float *dg, *dh0;
+    int first_tile = 0;
 };
 size_t gs_states_bytes(const GsProblem& pr);
 // pass: 0 forward, 1 backward with saved states, 2 backward recomputing them

@@ -26,6 +26,7 @@
 #include "dn_device.h"
 #include "dn_gated_scan.h"
 #include "dn_internal.h"
+#include "dn_wait.h"
 
 namespace dn {
 
@@ -203,12 +204,20 @@ __device__ __forceinline__ int uniform_wave() { return __builtin_amdgcn_readfirs
 // between: those need no state, so that tiles in flight at once do not wait for one
 // another's outputs.  The association depends on the tile alone, and so do the bits.
 //
-// Every wait ends: tiles are handed out in order by a counter, a workgroup finishes its own in
+// Every message comes: tiles are handed out in order by a counter, a workgroup finishes its own in
 // that order, and a tile waits for earlier ones only, so that the earliest unfinished tile
-// waits for nothing, however few workgroups run.
+// waits for nothing, however few workgroups run.  That holds while nobody else writes to the
+// workspace; where somebody does (two calls on it that are not ordered), messages may be wiped
+// out for good.  So a wave stops looking at a word after kLooks looks, 0.14 s (a tile takes 5 us),
+// and goes on with a NaN in its place.  A message concerns the next reach + 1 tiles of its strip
+// alone, a few of each workgroup, which wait for nine words each at most, and those that they keep
+// waiting: the launch ends within seconds.  (A count of its own for each word, with one way out of
+// the loop, costs no time, 32768 steps of 16 heads or 65536 of one; one count kept over the tiles, in
+// a register or in LDS, or a second way out made the bf16 forward 4 % slower.)
 struct Chain {
     static constexpr int kEach = 8;    // maps that a wave gathers
-    static constexpr unsigned kUnset = 0xffffffffu;   // a NaN
+    static constexpr int kLooks = 1 << 20;
+    static constexpr unsigned kUnset = 0xffffffffu, kNan = 0x7fc00000u;   // a NaN that no value is written as; the one that NaNs are
     static constexpr int kMessage = 64 * 8 + 64 * 4, kHead = 256;   // bytes
 
     static __device__ __forceinline__ char* message(const GsArgs& a, int at) { return a.chain + kHead + (long)at * kMessage; }
@@ -219,7 +228,7 @@ struct Chain {
         return reinterpret_cast<unsigned*>(message(a, at) + 64 * 8) + lane_id();
     }
     static __device__ __forceinline__ unsigned bits(float v) {   // any NaN as the quiet one
-        return v == v ? __builtin_bit_cast(unsigned, v) : 0x7fc00000u;
+        return v == v ? __builtin_bit_cast(unsigned, v) : kNan;
     }
     static __device__ __forceinline__ void put_map(const GsArgs& a, int at, float2 m) {
         __hip_atomic_store(map_of(a, at), (unsigned long long)bits(m.y) << 32 | bits(m.x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -289,19 +298,23 @@ struct Chain {
             share(a, at, w, k, n, m);
             float p = w == 0 ? 0.f : 1.f, e = first;
             if (w == 0 && k > n) {
-                while (!__all(base != kUnset)) {
-                    __builtin_amdgcn_s_sleep(1);
-                    base = get_last(a, at - (n + 1) * a.strips);
-                }
+                wait_until([&] { return __all(base != kUnset); },
+                           [&] {
+                               __builtin_amdgcn_s_sleep(1);
+                               base = get_last(a, at - (n + 1) * a.strips);
+                           },
+                           [&] { base = kNan; }, kLooks);
                 e = __builtin_bit_cast(float, base);
             }
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 if (i >= m) break;
-                while (!__all((unsigned)u[i] != kUnset)) {
-                    __builtin_amdgcn_s_sleep(1);
-                    u[i] = get_map(a, at - (n - w * kEach - i) * a.strips);
-                }
+                wait_until([&] { return __all((unsigned)u[i] != kUnset); },
+                           [&] {
+                               __builtin_amdgcn_s_sleep(1);
+                               u[i] = get_map(a, at - (n - w * kEach - i) * a.strips);
+                           },
+                           [&] { u[i] = (unsigned long long)kNan << 32 | kNan; }, kLooks);
                 const float q = __builtin_bit_cast(float, (unsigned)u[i]);
                 if (w > 0) p *= q;
                 e = fmaf(q, e, __builtin_bit_cast(float, (unsigned)(u[i] >> 32)));
@@ -647,11 +660,11 @@ template <typename T, bool COUPLED> __global__ __launch_bounds__(64 * kGsWavesB)
     }
 }
 
-// Before a chain: the counter is zero, every word of the messages unset.
-__global__ __launch_bounds__(256) void gated_scan_clear_kernel(uint4* p, long n) {
+// Before a chain: the counter stands at the first tile, every word of the messages is unset.
+__global__ __launch_bounds__(256) void gated_scan_clear_kernel(uint4* p, long n, int first_tile) {
     for (long i = blockIdx.x * 256L + threadIdx.x; i < n; i += gridDim.x * 256L) {
         const unsigned v = i < Chain::kHead / 16 ? 0u : Chain::kUnset;
-        p[i] = make_uint4(v, v, v, v);
+        p[i] = make_uint4(i == 0 ? first_tile : v, v, v, v);
     }
 }
 
@@ -778,11 +791,11 @@ GsArgs gs_args(const GsProblem& pr, const GsPlan& p, const void* x, const float*
     return a;
 }
 
-hipError_t clear_chain(const GsPlan& p, char* ws, hipStream_t s) {
+hipError_t clear_chain(const GsPlan& p, char* ws, int first_tile, hipStream_t s) {
     const long n = (long)(gs_chain_bytes(p) / 16);
     prof_begin(s, "gated_scan_clear");
     hipLaunchKernelGGL(gated_scan_clear_kernel, dim3((unsigned)std::min<long>((n + 255) / 256, 4 * kGsUnits)), dim3(256), 0, s,
-                       reinterpret_cast<uint4*>(ws), n);
+                       reinterpret_cast<uint4*>(ws), n, first_tile);
     prof_end(s);
     return hipGetLastError();
 }
@@ -836,17 +849,17 @@ template <typename T, bool COUPLED> hipError_t bwd_launch(const GsPlan& p, const
     prof_end(s);
     return hipGetLastError();
 }
-hipError_t fwd_any(const GsProblem& pr, const GsPlan& p, const GsArgs& a, hipStream_t s) {
+hipError_t fwd_any(const GsProblem& pr, const GsPlan& p, const GsArgs& a, int first_tile, hipStream_t s) {
     if (p.chain) {
-        const hipError_t e = clear_chain(p, a.chain, s);
+        const hipError_t e = clear_chain(p, a.chain, first_tile, s);
         if (e != hipSuccess) return e;
     }
     if (pr.bf16) return pr.coupled ? fwd_launch<bf16, true>(p, a, s) : fwd_launch<bf16, false>(p, a, s);
     return pr.coupled ? fwd_launch<float, true>(p, a, s) : fwd_launch<float, false>(p, a, s);
 }
-hipError_t bwd_any(const GsProblem& pr, const GsPlan& p, const GsArgs& a, hipStream_t s) {
+hipError_t bwd_any(const GsProblem& pr, const GsPlan& p, const GsArgs& a, int first_tile, hipStream_t s) {
     if (p.chain) {
-        const hipError_t e = clear_chain(p, a.chain, s);
+        const hipError_t e = clear_chain(p, a.chain, first_tile, s);
         if (e != hipSuccess) return e;
     }
     if (pr.bf16) return pr.coupled ? bwd_launch<bf16, true>(p, a, s) : bwd_launch<bf16, false>(p, a, s);
@@ -872,7 +885,7 @@ hipError_t launch_gated_scan_fwd(const GsProblem& pr, const GsFwd& f, char* ws, 
     a.out = f.o;
     a.last = f.hT;
     a.states = f.states;
-    return fwd_any(pr, p, a, s);
+    return fwd_any(pr, p, a, f.first_tile, s);
 }
 
 hipError_t launch_gated_scan_bwd(const GsProblem& pr, const GsBwd& f, char* ws, hipStream_t s) {
@@ -884,7 +897,7 @@ hipError_t launch_gated_scan_bwd(const GsProblem& pr, const GsBwd& f, char* ws, 
         GsArgs a = gs_args(pr, p, f.x, f.g, f.lens, ws);
         a.first = f.h0;
         a.states = again;
-        const hipError_t e = fwd_any(pr, p, a, s);
+        const hipError_t e = fwd_any(pr, p, a, 0, s);
         if (e != hipSuccess) return e;
         states = again;
     }
@@ -896,7 +909,7 @@ hipError_t launch_gated_scan_bwd(const GsProblem& pr, const GsBwd& f, char* ws, 
     a.out = f.dx;
     a.dg = f.dg;
     a.last = f.dh0;
-    return bwd_any(pr, p, a, s);
+    return bwd_any(pr, p, a, f.first_tile, s);
 }
 
 hipError_t launch_gated_scan_recurrent(const GsProblem& pr, const void* x, const float* g, float* state, void* o,

@@ -424,7 +424,9 @@ dn_status dn_tree_commit_counts(const dn_shape* shape, const void* k, const floa
  *            dx io, dg fp32 like g, dh0 fp32 (NULL = not wanted), from the states that the
  *            forward saved for the same inputs (h0 is then not read) or, NULL, from h0
  *   ws     : >= dn_gated_scan_workspace_bytes(shape, DN_PASS_FWD, DN_PASS_BWD with saved
- *            states, or DN_PASS_BWD_RECOMPUTE without)
+ *            states, or DN_PASS_BWD_RECOMPUTE without); calls that share one have to be
+ *            ordered.  Two that are not give wrong values or NaN, and may take some seconds
+ *            before they end
  * Everything is held in fp32 between its inputs and outputs.  A decay below 2^-126 is zero
  * (g < -87.34, -inf among them): it resets the state.  Positive gates grow the state;
  * where they sum to more than 88 over some run of steps, results overflow (Inf or NaN)
