@@ -88,6 +88,7 @@ struct Buf {
     const void* p;
     size_t bytes;
     bool output;
+    int apart = 0;   // buffers of one number, not 0, are known to share no element
 };
 
 // Required pointers must be non-NULL when non-empty; all must be 16-byte
@@ -103,7 +104,7 @@ dn_status check_buffers(std::initializer_list<Buf> bufs) {   // no allocation: n
         if (!a.p || a.bytes == 0) continue;
         for (const Buf* j = i + 1; j != bufs.end(); ++j) {
             const Buf& b = *j;
-            if (!b.p || b.bytes == 0 || (!a.output && !b.output)) continue;
+            if (!b.p || b.bytes == 0 || (!a.output && !b.output) || (a.apart && a.apart == b.apart)) continue;
             const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), a1 = a0 + a.bytes;
             const uintptr_t b0 = reinterpret_cast<uintptr_t>(b.p), b1 = b0 + b.bytes;
             if (a0 < b1 && b0 < a1) return fail(DN_ERR_INVALID, "%s overlaps %s", a.name, b.name);
@@ -1158,6 +1159,41 @@ dn_status qk_strides(const dn::QkArgs& a, int heads, const int64_t stride[3], bo
     return DN_OK;
 }
 
+// Whether rows of both outputs lie between one another's and share no element: those of one tensor's
+// slices, with the same strides.  Row (b, h, t) of the second begins `from` + the sum of index * stride
+// elements behind the first's first row, so that two rows meet where from + sum of i * stride is less than
+// d away from zero, i a difference of indices.  Each stride steps over all that the smaller
+// ones reach (qk_strides), so only the two i next to -from / stride can do that, largest stride first.
+bool qk_meet(const long stride[3], const long first[3], const long last[3], int n, __int128 from, int d) {
+    if (n == 0) return from < d && from > -d;
+    const __int128 s = stride[n - 1];
+    const __int128 i = from > 0 ? -((from + s - 1) / s) : -from / s;   // -from / s rounded down
+    for (const __int128 k : {i, i + 1})
+        if (k >= first[n - 1] && k <= last[n - 1] && qk_meet(stride, first, last, n - 1, from + k * s, d)) return true;
+    return false;
+}
+bool qk_apart(const dn::QkArgs& a) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.side[0].out), q = reinterpret_cast<uintptr_t>(a.side[1].out);
+    const long E = a.bf16 ? 2 : 4, hq = a.side[0].heads, hk = a.side[1].heads;
+    if (!p || !q || (p - q) % E != 0) return false;
+    const long sizes[3] = {a.B, std::max(hq, hk), a.T};
+    long stride[3], first[3], last[3];
+    int n = 0;
+    int order[3] = {0, 1, 2};
+    auto step = [&](int i) { return std::max(a.side[0].os[i], a.side[1].os[i]); };   // 0 where a side has size 1
+    std::sort(order, order + 3, [&](int i, int j) { return step(i) < step(j); });
+    for (int i : order) {
+        if (sizes[i] <= 1) continue;
+        const long u = a.side[0].os[i], v = a.side[1].os[i];
+        if (u && v && u != v) return false;
+        stride[n] = step(i);
+        first[n] = -((i == 1 ? hq : sizes[i]) - 1);
+        last[n++] = (i == 1 ? hk : sizes[i]) - 1;
+    }
+    const __int128 from = q >= p ? (__int128)(q - p) / E : -((__int128)(p - q) / E);
+    return !qk_meet(stride, first, last, n, from, a.d);
+}
+
 void qk_dense(const dn::QkArgs& a, int heads, long to[3]) {
     if (a.B == 0) return;   // no rows: heads and steps may be any
     to[0] = (long)heads * a.T * a.d;
@@ -1244,6 +1280,8 @@ dn_status dn_qk_bwd(const dn_qk_shape* shape, const void* q, const void* k, cons
     DN_TRY(need(dk, ndk, "dk"));
     if (ws_bytes < nws) return fail(DN_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, nws);
     DN_TRY(need(ws, nws, "workspace"));
+    a.side[0].out = dq, a.side[1].out = dk;
+    const int apart = ndq && ndk && qk_apart(a);
     DN_TRY(check_buffers({{"q", q, nq, false},
                           {"k", k, nk, false},
                           {"dyq", dyq, shape->Hq * row, false},
@@ -1253,16 +1291,16 @@ dn_status dn_qk_bwd(const dn_qk_shape* shape, const void* q, const void* k, cons
                           {"freqs", freqs, nf, false},
                           {"pos", pos, np, false},
                           {"lens", lens, (size_t)a.B * 4, false},
-                          {"dq", dq, ndq, true},
-                          {"dk", dk, ndk, true},
+                          {"dq", dq, ndq, true, apart},
+                          {"dk", dk, ndk, true, apart},
                           {"dwq", dwq, nw, true},
                           {"dwk", dwk, nw, true},
                           {"workspace", ws, nws, true}}));
     a.freqs = freqs;
     a.pos = pos;
     a.lens = lens;
-    a.side[0].x = norm ? q : dyq, a.side[0].dy = dyq, a.side[0].w = wq, a.side[0].out = dq, a.side[0].dw = dwq;
-    a.side[1].x = norm ? k : dyk, a.side[1].dy = dyk, a.side[1].w = wk, a.side[1].out = dk, a.side[1].dw = dwk;
+    a.side[0].x = norm ? q : dyq, a.side[0].dy = dyq, a.side[0].w = wq, a.side[0].dw = dwq;
+    a.side[1].x = norm ? k : dyk, a.side[1].dy = dyk, a.side[1].w = wk, a.side[1].dw = dwk;
     if (!norm) {   // a rotation's gradient is the rotation back
         for (dn::QkSide& s : a.side) qk_dense(a, s.heads, s.xs);
         a.back = 1;

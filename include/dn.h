@@ -470,7 +470,9 @@ dn_status dn_gated_scan_recurrent_fwd(const dn_shape* shape, const void* x, cons
  *            y, dq and dk, their inputs are not used
  *   forward : yq io [B][Hq][T][d], yk io [B][Hk][T][d]
  *   backward: from dyq, dyk (like yq, yk): dq, dk by dq_stride and dk_stride, whose rows may
- *            not share memory; dwq, dwk fp32 [d] (NULL = not wanted), summed over all rows.
+ *            not share memory (rows of one may lie between the other's where both have the
+ *            same strides: slices of the gradient of one projection); dwq, dwk fp32 [d]
+ *            (NULL = not wanted), summed over all rows.
  *            Without a norm q, k and the weights are NULL.  ws >= dn_qk_workspace_bytes
  *            (only where dwq or dwk is wanted)
  * Norms, angles (in fp64 up to the reduced angle) and rotations are held to fp32.  A row of
