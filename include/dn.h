@@ -475,8 +475,10 @@ dn_status dn_gated_scan_recurrent_fwd(const dn_shape* shape, const void* x, cons
  *            (NULL = not wanted), summed over all rows.
  *            Without a norm q, k and the weights are NULL.  ws >= dn_qk_workspace_bytes
  *            (only where dwq or dwk is wanted)
- * Norms, angles (in fp64 up to the reduced angle) and rotations are held to fp32.  A row of
- * zeros with eps == 0 gives NaN; the sum of squares overflows beyond 1.8e19.  NaN or Inf
+ * Norms, angles (in fp64 up to the reduced angle) and rotations are held to fp32.  The sum
+ * of squares is fp32: a row longer than 1.8e19 gives zeros, and with eps == 0 a row of
+ * elements below 1e-19, whose squares leave fp32's normal numbers, is not of unit length: the
+ * smaller they are the fewer bits are left, below 2.6e-23 it is Inf, and a row of zeros NaN.  NaN or Inf
  * stays in its row (in its pair without a norm), and in dwq, dwk.  Errors as for
  * dn_chunk_fwd.
  */
