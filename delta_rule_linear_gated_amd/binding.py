@@ -911,7 +911,11 @@ def rotary_freqs(rot, base=10000.0, scaling=None, factor=1.0, trained=None, fast
       "linear"  all angles divided by the factor (interpolated positions)
       "ntk"     the base raised so that the slowest pair is divided by the factor and the fastest stays
       "yarn"    pairs that turn ``fast`` times and more within ``trained`` positions stay, those that turn ``slow``
-                times and fewer are divided by the factor, in between by a ramp; amplitude 0.1 ln(factor) + 1
+                times and fewer are divided by the factor, in between a ramp that is linear in the turns;
+                amplitude 0.1 ln(factor) + 1.  Where a model was trained with a ramp that is linear in the
+                pair's index m (between the pairs that turn ``fast`` times and ``slow`` times, rounded outwards),
+                the angles in between are other ones (rot 128, factor 8, trained 4096: 25 of 64 pairs, by up to
+                57 %): such frequencies are computed by the caller and handed over as ``freqs``
     Returns (freqs, amplitude)."""
     if rot <= 0 or rot % 2:
         raise ValueError(f"rot must be positive and even, got {rot}")
