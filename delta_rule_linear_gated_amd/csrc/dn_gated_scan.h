@@ -1,5 +1,5 @@
 // dn_gated_scan.h -- what the C-ABI layer and the kernels of the gated linear
-// recurrence (dn_gated_scan.hip) share.  Layouts as in include/dn.h.
+// recurrence (dn_gated_scan_plan.cpp, dn_gated_scan.hip) share.  Layouts as in include/dn.h.
 #pragma once
 
 #include <hip/hip_runtime.h>
