@@ -8,10 +8,12 @@
 // in registers, the waves exchange the maps through LDS (one barrier), each takes its run's
 // first state through the maps before it and goes over its registers again for the outputs.
 // All of a tile's rows are loaded while the one before is worked on, and every tensor is
-// read once: the bytes bound it (8 x 16 heads of 128, 4096 steps, bf16: forward 113 us, 4.8 TB/s;
-// backward 199 us, 4.7 TB/s; a large copy runs at 5.1).  Waves and runs were chosen by
-// measurement: forward 16 x 16 steps (8 x 16: 139 us, 8 x 32: 126, 16 x 8: 138), backward 8 x 16
-// (16 x 8: 225, 4 x 32: 211).
+// read once: the bytes bound it (8 x 16 heads of 128, 4096 steps, bf16: forward 114 us, backward
+// 200, 4.7 TB/s both; a large copy runs at 5.1).
+//
+// Times here and at gs_plan are of calls in a captured graph, clearing included, on inputs that no
+// cache holds.  In a training step the backward finds part of the forward's inputs in the last-level
+// cache: the two of this case take 292 together, and a trace of them shows 120 and 176.
 //
 // Marching, a workgroup walks the tiles of one strip, the state in a register.  Where the strips
 // do not fill the chip (gs_plan), the tiles of all strips are handed out in the order of their
@@ -205,9 +207,9 @@ __device__ __forceinline__ int uniform_wave() { return __builtin_amdgcn_readfirs
 // out for good.  So a wave stops looking at a word after kLooks looks, 0.14 s (a tile takes 5 us),
 // and goes on with a NaN in its place.  A message concerns the next reach + 1 tiles of its strip
 // alone, a few of each workgroup, which wait for nine words each at most, and those that they keep
-// waiting: the launch ends within seconds.  (A count of its own for each word, with one way out of
-// the loop, costs no time, 32768 steps of 16 heads or 65536 of one; one count kept over the tiles, in
-// a register or in LDS, or a second way out made the bf16 forward 4 % slower.)
+// waiting: the launch ends within seconds.  (A count of its own for each word costs up to 2 %: 16
+// heads of 128, 32768 steps, a call that saves no states 127.2 -> 129.5 us; one count kept over the
+// tiles, in a register or in LDS, made the bf16 forward 4 % slower.)
 struct Chain {
     static constexpr int kEach = kGsEach;
     static constexpr int kLooks = 1 << 20;
@@ -318,7 +320,8 @@ struct Chain {
     };
 };
 
-// Forward, marching.  Outputs, saved states and the last state, each where wanted.
+// Forward, marching.  Outputs, saved states and the last state, each where wanted.  Four waves a SIMD
+// leave 128 registers; bf16 with two or four runs a wave (coupled) or four or eight (not) spills two.
 template <typename T, bool COUPLED, int W, int G>
 __global__ __launch_bounds__(64 * W, 4) void gated_scan_fwd_kernel(GsArgs a) {
     constexpr int R = kGsRun, TILE = W * G * R, C = 64 / G;
@@ -373,8 +376,9 @@ __global__ __launch_bounds__(64 * W, 4) void gated_scan_fwd_kernel(GsArgs a) {
 
 // Forward, chained: outputs are a tile behind the maps, so that a tile's map has been on its
 // way to the others for as long as a tile takes when they ask for it (32 strips, 32768 steps, bf16:
-// outputs at once 168 us, a tile behind 131, 4.2 TB/s).  12 waves: as many as have the registers of
-// two tiles (8: 161 us).
+// 131 us, 4.1 TB/s; outputs at once, as it was first, 168).  12 waves: as many as have the registers of
+// two tiles, 168 each (bf16 157 and 159; fp32 all, and coupled it spills six; 24 to 39 scalars lie in
+// vector registers' lanes).
 template <typename T, bool COUPLED> __global__ __launch_bounds__(64 * kGsWavesC) void gated_scan_fwd_chain_kernel(GsArgs a) {
     constexpr int R = kGsRun, W = kGsWavesC, TILE = W * R;
     __shared__ float2 part[2][W][64], gathered[2][W][64];
@@ -545,7 +549,7 @@ __global__ __launch_bounds__(64 * W, 2) void gated_scan_bwd_kernel(GsArgs a) {
 
 // Backward, chained from the last tile of every strip; results are a tile behind the maps.  The
 // states inside a tile come from the saved one at its start and wait for no other tile (32 strips,
-// 32768 steps, bf16: 205 us, 4.6 TB/s; results at once 250).
+// 32768 steps, bf16: 206 us, 4.6 TB/s; results at once, as it was first, 250).
 template <typename T, bool COUPLED> __global__ __launch_bounds__(64 * kGsWavesB) void gated_scan_bwd_chain_kernel(GsArgs a) {
     constexpr int R = kGsRunB, W = kGsWavesB, TILE = W * R;
     static_assert(TILE == kGsSaved, "a tile begins at a saved state");

@@ -12,11 +12,14 @@ size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Strips of 64 / G channels: of one head's row, or (flat) of the channels of all heads in a row, so
 // that odd widths leave no lane idle, but lanes of two heads read twice the cache lines.  Measured
-// (us, forward, one head's -> flat): d 67 (47 % of the lanes idle), 2000 steps 99 -> 81; d 100 (22 %)
-// 65 -> 72; 777 steps of 15 heads as one tile (few strips either way), d 67 10.1 -> 13.9, but of 150
-// heads of 24, 300 strips -> 225, 15.1 -> 12.4.  So flat where more than a quarter of the lanes
-// would idle, or several runs a wave would take more than one round of the chip; never
-// where a strip's rows lie further apart than a 31-bit byte offset.
+// (us, forward / backward, one head's -> flat):
+//     marching, 280 heads, 2000 steps     d 67 (47 % of the lanes idle) 141 / 218 -> 101 / 180, d 100 (22 %) 151 / 257 -> 153 / 277
+//     marching, 300 heads of 100, 3334 steps      258 / 466 -> 275 / 498
+//     chained, 80 heads of 100, 3334 steps        75 / 127 -> 72 / 128, fp32 88 / 160 -> 88 / 165
+//     one tile, fp32, 777 steps                   15 heads of 67 8.1 / 11.6 -> 10.6 / 15.5, 150 heads of 24 11.1 / 18.8 -> 11.2 / 17.3
+// So flat where more than a quarter of the lanes would idle, in every form, or where several runs a
+// wave would take more than one round of the chip; never where a strip's rows lie further apart
+// than a 31-bit byte offset.
 bool gs_flat(const GsProblem& pr, int groups) {
     const long C = 64 / groups, per = (pr.d + C - 1) / C, rows = 63 / pr.d + 2;   // a strip touches at most that many
     if (rows * pr.T >= kGsRange / 4 / pr.d) return false;
@@ -34,22 +37,24 @@ long gs_blocks(long strips, int groups) {   // G > 1: a whole number of 64-chann
     return (strips + all - 1) / all * all;
 }
 // Which form.  Measured (us, forward / backward, bf16, coupled; marching with the best G -> chained):
-//     64 strips, 8192 steps        81 / 127 -> 74 / 110      4 strips, 4096 steps          19.3 / 26.7 -> 14.6 / 15.5
-//     157 strips, 4096 steps     110 / 196 -> 94 / 162       15 strips (fp32), 777 steps     7.9 / 10.1 -> 12.9 / 14.2
-//     32 strips, 32768 steps     212 / 300 -> 134 / 205      32 strips, 512 steps             7.8 / 8.7 -> 12.8 / 14.8
-// (256 strips, 4096 steps, as many bytes as 32 strips, 32768 steps: marching 113 / 199, floor 105 / 183.)
+//     64 strips, 8192 steps        77 / 132 -> 74 / 113      4 strips, 4096 steps          18.5 / 26.5 -> 14.6 / 15.6
+//     157 strips, 4096 steps     109 / 191 -> 93 / 160       15 strips (fp32), 777 steps     6.8 / 9.9 -> 13.0 / 14.4
+//     32 strips, 32768 steps     180 / 297 -> 131 / 206      32 strips, 512 steps             6.1 / 8.7 -> 13.2 / 14.7
+// (256 strips, 4096 steps, as many bytes as 32 strips, 32768 steps: marching 114 / 200; a copy of as
+// many bytes, half of them written, 105 / 183.)
 // So: up to 1024 steps march, as many runs of a channel in a wave as make one tile of them and still
-// leave one round of workgroups (224 strips, 1000 steps, of one tile -> so: 41 / 91 -> 31 / 47 us;
-// 15 strips, 777 steps, forward, 16 waves with four runs -> 8 with eight: 8.0 -> 6.2), a round being
-// two workgroups of a unit forward and one backward.  Forward with one instead: 128 strips, 300 steps
-// 9.5 -> 10.5, 57 strips (fp32), 777 steps 10.9 -> 13.1, 224 strips, 300 steps 14.3 -> 14.8, but
-// 64 strips, 1000 steps 13.0 -> 12.1, 160 strips, 600 steps 19.4 -> 18.8; backward with two: 64
-// strips, 1000 steps 16.5 -> 22.1, 160 strips, 600 steps 25.7 -> 31.0.  Longer ones are chained where
-// marching would leave more than a fifth of the chip idle; else strips of 64 channels march.
+// leave one round of workgroups (224 strips, 1000 steps, of one tile -> so: 43 / 92 -> 30 / 46 us), a
+// round being two workgroups of a unit forward and one backward.  Forward with one instead: 128
+// strips, 300 steps 9.5 -> 10.5, 57 strips (fp32), 777 steps 11.0 -> 13.2, 224 strips, 300 steps 14.3 ->
+// 14.8; backward with two: 128 strips, 300 steps 13.9 -> 15.7, 64 strips, 1000 steps 16.3 -> 22, 160
+// strips, 600 steps 25.6 -> 30.5.  One bound for all lengths, though with one round 64 strips, 1000
+// steps forward would take 12.1 instead of 13.0, 160 strips, 600 steps 18.9 instead of 19.4.  Longer
+// ones are chained where marching would leave more than a fifth of the chip idle; else strips of 64
+// channels march.
 // Waves: up to 128 steps only those whose runs they are (131072 channels, 16 steps, of 16 waves -> of
-// one: 44 -> 6.8 us).  Longer, forward: 16 where a unit has one strip (256 strips, 4096 steps:
-// 113 us, of 8 waves 119), 8 where it has two, whose loads then overlap (2048 strips, 512 steps:
-// 133 -> 111; 512 strips, 4096 steps: 224 -> 219; fp32, 1024 strips: 633 -> 646).
+// one: 46 -> 6.8 us).  Longer, forward: 16 where a unit has one strip (256 strips, 4096 steps:
+// 113 us, of 8 waves 117), 8 where it has two, whose loads then overlap (2048 strips, 512 steps:
+// 130 -> 111; 512 strips, 4096 steps: 222 -> 217; fp32, 1024 strips: 625 both).
 constexpr int kGsShort = 1024;
 GsPlan gs_plan(const GsProblem& pr, bool bwd) {
     GsPlan p{};

@@ -428,10 +428,10 @@ dn_status dn_tree_commit_counts(const dn_shape* shape, const void* k, const floa
  *            ordered.  Two that are not give wrong values or NaN, and may take some seconds
  *            before they end
  * Everything is held in fp32 between its inputs and outputs.  A decay below 2^-126 is zero
- * (g < -87.34, -inf among them): it resets the state.  Positive gates grow the state;
- * where they sum to more than 88 over some run of steps, results overflow (Inf or NaN)
- * whatever the state holds.  NaN or Inf stays in its channel.  Layouts, validation and
- * errors as for dn_chunk_fwd.
+ * (g < -87.34, -inf among them): it resets the state; the decay of a run of steps whose gates
+ * sum to that may be taken as zero too.  Positive gates grow the state; where they sum to more
+ * than 88 over some run of steps, results overflow (Inf or NaN) whatever the state holds.
+ * NaN or Inf stays in its channel.  Layouts, validation and errors as for dn_chunk_fwd.
  *
  * dn_gated_scan_recurrent_fwd: T steps, the state (fp32 [B][H][dv]) updated in place; no
  * workspace.
