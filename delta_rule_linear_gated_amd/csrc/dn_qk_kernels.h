@@ -269,17 +269,20 @@ template <typename T, int D, int TURN, bool DW> __global__ __launch_bounds__(kQk
             }
         }
         if (!DW) continue;
-        // The tokens of a lane may be many thousands: what an addition rounds off (`over`) goes into the
-        // next one (Kahan's sum), so that the error does not grow with them: 2^24 equal rows, 8 heads,
-        // 255 half steps of fp32 -> 16.  Costs no time but with one head a token (d 16: 21.0 -> 21.5 us).
+        // The tokens of a lane may be many thousands: what each addition rounds off is added up by itself
+        // (over), so that the error does not grow with them: 2^24 equal rows, 8 heads, 255 half steps of
+        // fp32 -> 16.  Time: none where rows are many, half a microsecond and up to 1 of 20 with few (one head
+        // of 16, 39 sequences of 10220 steps).
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float add = sum[j] - over[j], to = dw[j] + add;
-            over[j] = (to - dw[j]) - add;
+            const float to = dw[j] + sum[j];
+            over[j] += (to - dw[j]) - sum[j];
             dw[j] = to;
         }
     }
     if (!DW) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[j] = fabsf(over[j]) < __builtin_inff() ? dw[j] - over[j] : dw[j];   // not of an infinite sum
     // over the tokens of the workgroup: lanes of the same elements, then the waves
     __shared__ float part[kQkThreads / 64][D];
 #pragma unroll

@@ -60,3 +60,26 @@ def test_padded_batch_over_many_tiles():
         off = float(((dw.double() - total).abs() / (terms * U32)).max())
         print(f"weights: {off:.2f} half steps", flush=True)
         assert off <= SUM
+
+
+@pytest.mark.parametrize("what", ["infinite", "overflowing"])
+def test_infinite_sums(what):
+    """A cotangent's infinity, or finite terms whose sum overflows, give an infinite gradient of that channel's weight, as
+    a plain sum does, wherever the row lies; the other channels keep their bits."""
+    H, T, d = 1, 40000, 128
+    gen = torch.Generator().manual_seed(9)
+    q = torch.randn(1, H, T, d, generator=gen).cuda()
+    q[..., 7] = torch.copysign(q[..., 7].abs() * 1e3 + 1e3, q[..., 7])   # the unit row's other elements are small
+    dy = torch.randn(1, H, T, d, generator=gen).cuda()
+    w = torch.ones(d, device="cuda")
+    clean = B.qk_norm_bwd(q, None, dy, None, w, None)["dwq"]
+    for t in (0, 5, 20001, T - 1):
+        bad = dy.clone()
+        if what == "infinite":
+            bad[0, 0, t, 7] = torch.copysign(torch.tensor(float("inf")).cuda(), q[0, 0, t, 7])
+        else:   # of every row: two terms of a thread overflow
+            bad[..., 7] = torch.copysign(torch.tensor(3e38).cuda(), q[..., 7])
+        dw = B.qk_norm_bwd(q, None, bad, None, w, None)["dwq"]
+        assert float(dw[7]) == float("inf"), (t, float(dw[7]))
+        rest = torch.arange(d, device="cuda") != 7
+        assert torch.equal(dw[rest], clean[rest])
