@@ -21,7 +21,7 @@ struct GsFwd {
     void* o;
     float* hT;
     float* states;
-    int first_tile = 0;   // a chain begins with it (else 0 in tests alone: the messages of those before it never come)
+    int first_tile = 0;   // a chain begins with it; not 0 in tests alone, where the messages of those before it never come
 };
 struct GsBwd {
     const void* x;

@@ -9,8 +9,8 @@
 // keeps its token (its angles: fp64, reduced to an eighth turn, then short series) over the
 // heads of a group.  The bytes of the rows are what bounds it, read and written once, four rows of
 // a lane in flight (backward: two of each tensor).  At 32 + 32 heads of 128, 32768 steps, bf16: l2
-// 211 us (5.1 TB/s), rms with halves rotated 221, rotation alone 212, backward of l2 306 (5.3 TB/s),
-// of rms with rotation and weights 320; a large copy runs at 5.1 to 5.2.
+// 211 us (5.1 TB/s), rms with halves rotated 220, rotation alone 215, backward of l2 304 (5.3 TB/s),
+// of rms with rotation and weights 323; a large copy runs at 5.1 to 5.2.
 #pragma once
 
 #include "dn_device.h"

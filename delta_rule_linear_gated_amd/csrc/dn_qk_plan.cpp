@@ -9,16 +9,17 @@ namespace dn {
 constexpr int kQkUnits = 256;   // compute units
 
 // Heads a lane takes, and the workgroups.  More heads a lane share its angles; fewer fill the
-// chip.  Measured at 32 + 32 heads of 128, 32768 steps, bf16 (us, rms with halves rotated, 4 / 8 /
-// 16 heads): 234 / 223 / 217, backward without weights 347 / 329 / 328, with few tokens (16 + 16
-// heads, 1024 steps) 7.5 / 8.0 / 7.3.
+// chip.  Measured at 32 + 32 heads of 128, 32768 steps, bf16 (us of calls in a captured graph; rms with
+// halves rotated, 4 / 8 / 16 heads): 228 / 220 / 218, backward without weights 299 / 300 / 314.
 // As many workgroups as run at once, each walking the token tiles, keep reads and writes apart
-// less than a workgroup a tile does: 4 a unit against 8 (backward, l2) 305 -> 350 us (6: 311, 3: 299,
-// 2: 343), against one a tile (forward, l2) 211 -> 220, rotation alone 212 -> 221.  But the rotation
-// back, whose rows lie head by head on both sides, takes 231 -> 217, and with the lengths of a
-// padded batch the tiles differ in work (8 sequences of up to 4096 steps, 16 + 16 heads, forward:
-// 101 -> 85): then a workgroup a tile, or in the backward, whose workgroups each leave a partial
-// sum, 8 a unit.
+// less than a workgroup a tile does: 4 a unit against 8 (backward, l2) 304 -> 348 us (6: 310, 3: 298,
+// 2: 341), against one a tile (forward, l2) 210 -> 224, rotation alone 215 -> 221.  But the rotation
+// back, whose rows lie head by head on both sides, takes 239 -> 231 (32 + 8 heads, 2 sequences of
+// 16384 steps 152 -> 139; but 64 of 512, 32 + 32 heads, 217 -> 283), and with the lengths of a padded
+// batch the tiles differ in work (8 sequences of up to 4096 steps, 16 + 16 heads, forward: 101 -> 84):
+// then a workgroup a tile, or in the backward, whose workgroups each leave a partial sum, 8 a unit
+// (which does not pay with every draw of lengths: this batch, l2, 120 -> 125, 64 sequences of up to 512
+// steps 246 -> 287).
 void qk_split(QkArgs* a, bool bwd) {
     const long tokens = (long)a->B * a->T, per_wg = 256 / (a->d / 8);
     const long tiles = (tokens + per_wg - 1) / per_wg;
